@@ -33,6 +33,7 @@ ERR_HIP = 7
 F32 = 0
 BF16 = 1
 I32 = 2
+E8M0 = 3
 ACT_NONE = 0
 ACT_GELU = 1
 MAX_K = 133136
@@ -48,6 +49,11 @@ EXPORTED = (
     "convrot_lora_down",
     "convrot_lora_up_add",
     "convrot_linear_lora",
+    "convrot_fp8_quantize_weights",
+    "convrot_fp8_pack_activations",
+    "convrot_fp8_linear_grouped",
+    "convrot_block_norm",
+    "convrot_rope_apply",
     "convrot_status_string",
     "convrot_version",
 )
@@ -124,6 +130,16 @@ def lib() -> ctypes.CDLL:
                                           ctypes.POINTER(ConvrotLora), i32, ctypes.POINTER(vp),
                                           ctypes.POINTER(i64), i32, vp]
         L.convrot_linear_lora.restype = ctypes.c_int
+        L.convrot_fp8_quantize_weights.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+        L.convrot_fp8_quantize_weights.restype = ctypes.c_int
+        L.convrot_fp8_pack_activations.argtypes = [vp, i32, i64, i64, i64, vp, vp]
+        L.convrot_fp8_pack_activations.restype = ctypes.c_int
+        L.convrot_fp8_linear_grouped.argtypes = [vp, vp, i32, vp, vp, i32, i32, vp]
+        L.convrot_fp8_linear_grouped.restype = ctypes.c_int
+        L.convrot_block_norm.argtypes = [vp, vp]
+        L.convrot_block_norm.restype = ctypes.c_int
+        L.convrot_rope_apply.argtypes = [vp, vp]
+        L.convrot_rope_apply.restype = ctypes.c_int
         L.convrot_status_string.argtypes = [ctypes.c_int]
         L.convrot_status_string.restype = ctypes.c_char_p
         L.convrot_version.argtypes = []
@@ -451,3 +467,10 @@ def linear_lora(x: PackedActivation, ws, adapters, outs=None, gelu: bool = False
     if st != OK:
         raise ConvrotError(st, "convrot_linear_lora")
     return outs
+
+
+# The operators around a block's linears (they use the names above).
+from .block import (  # noqa: E402,F401
+    FP8_BLOCK, MAX_NORM_K, MAX_ROPE_TENSORS, Fp8Activation, Fp8Weights, Norm, RopePlan, block_norm,
+    block_update, fp8_linear, fp8_linear_grouped, fp8_pack_activations, fp8_quantize_weights, rope,
+    rope_plan)

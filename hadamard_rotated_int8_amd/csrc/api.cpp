@@ -6,13 +6,14 @@
 #include <stdint.h>
 
 #include "../../include/convrot.h"
+#include "checks.h"
 #include "kernels.h"
 
+using convrot::aligned16;
+using convrot::from_hip;
+using convrot::kMaxRows;
+
 namespace {
-
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // log4 of a valid group size (1, 4, ..., 4^7), or -1.
 int log4_of(int32_t g) {
@@ -29,8 +30,6 @@ convrot_status check_k_group(int64_t k, int32_t group_size, int* log4g) {
   *log4g = n;
   return CONVROT_OK;
 }
-
-convrot_status from_hip(hipError_t e) { return e == hipSuccess ? CONVROT_OK : CONVROT_ERR_HIP; }
 
 }  // namespace
 

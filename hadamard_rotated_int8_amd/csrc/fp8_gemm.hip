@@ -1,0 +1,350 @@
+// FP8 linear on CDNA4 matrix cores: E4M3 codes, a scale for each block of 128
+// features.
+//
+//   Y[r, o] = act( sum_b sx[r, b] sw[o / 128, b] sum_{i in b} qx[r, i] qw[o, i] + bias[o] )
+//
+// with float32 sums.  v_mfma_scale_f32_32x32x64_f8f6f4 multiplies the products
+// of a lane's 32 features by 2^(ea + eb) as it adds them, so power-of-two
+// (E8M0) scales cost no vector work: a block is two such instructions with
+// the same scale bytes.  float32 weight scales (checkpoints that hold max /
+// 448) cannot go through the instruction: the block's sum starts from zero
+// with the activation's scale applied by the matrix core, and is added to
+// the running sum with one fused multiply-add per value.
+//
+// The FP8 instructions line up the products of a few features before they add
+// them and drop what falls some 14 bits below the largest: the result is off
+// by 1.5e-5 of its size for normal data and 4e-5 where features differ much
+// (measured, with and without scales, the same for every K).  That is far
+// inside a bfloat16 output's rounding (2^-9), but not inside what a float32
+// output promises.  Outputs in float32 therefore convert the codes to
+// bfloat16 (exact) with their scales as they leave LDS and use the bfloat16
+// instruction, which adds in full float32, at half the matrix rate.
+//
+// The weights are the instruction's first operand: a lane then holds 4
+// consecutive columns of one output row per accumulator quad and stores them
+// as one vector.  Which 32 features of a 64-wide slice a lane holds does not
+// matter as long as both operands agree (the sum runs over all of them and
+// the scale is the block's).
+#include "fp8.h"
+#include "kernels.h"
+
+namespace convrot {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kBK = 128;  // features (bytes) per step: one scale block
+constexpr int kGroupM = 4;
+
+struct Fp8Params {
+  const uint8_t* qx;
+  const uint8_t* sx;
+  int64_t lds;
+  int M, K, kb;
+  int nseg;
+  int tiles_m, tiles_n;
+  int y_bf16, gelu;
+  struct Seg {
+    const uint8_t* qw;
+    const void* sw;
+    const float* bias;
+    void* y;
+    int64_t ldy;
+    int n, tn0;
+  } seg[kMaxGemmGroup];
+};
+
+CR_DEVICE int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+CR_DEVICE unsigned bf16_pair(float a, float b) {  // two values to nearest even
+  return unsigned(__builtin_bit_cast(uint16_t, (__bf16)a)) |
+         unsigned(__builtin_bit_cast(uint16_t, (__bf16)b)) << 16;
+}
+
+// Four consecutive columns of one output row; `whole` when all four exist and
+// the row allows a vector store.
+CR_DEVICE void store4(void* y, int64_t at, const float* v, int left, bool bf16, bool whole) {
+  if (bf16) {
+    uint16_t* p = static_cast<uint16_t*>(y) + at;
+    const u32x2 w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    if (whole) {
+      *reinterpret_cast<u32x2*>(p) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) p[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    float* p = static_cast<float*>(y) + at;
+    if (whole) {
+      *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  }
+}
+
+// The float32 value of an E8M0 byte (255 is NaN; 0 is 2^-127, a subnormal).
+CR_DEVICE float e8m0_value(unsigned s) {
+  return __uint_as_float(s == 0 ? 0x400000u : s == kFp8ScaleNan ? 0x7FC00000u : s << 23);
+}
+
+// 32 E4M3 codes times a power of two, as four bfloat16 operands.
+struct Bf16Frag {
+  bf16x8 v[4];
+};
+CR_DEVICE Bf16Frag to_bf16(v8i q, float scale) {
+  Bf16Frag r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(q[i]), scale, false);
+    const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(q[i]), scale, true);
+    r.v[i / 2][4 * (i & 1)] = lo[0];
+    r.v[i / 2][4 * (i & 1) + 1] = lo[1];
+    r.v[i / 2][4 * (i & 1) + 2] = hi[0];
+    r.v[i / 2][4 * (i & 1) + 3] = hi[1];
+  }
+  return r;
+}
+CR_DEVICE f32x16 mfma_bf16(const Bf16Frag& a, const Bf16Frag& b, f32x16 c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+
+// One workgroup of WM x WN waves per output tile; a wave owns FM x FN blocks
+// of 32 x 32.  Operands reach LDS by direct-to-LDS loads of whole 128-byte
+// lines (16-byte chunk c of stage row r at slot c ^ swz(r), so 16 lanes that
+// read 16 consecutive rows touch 16 different groups of 4 banks), in two
+// stages.  Rows past M or n and bytes past K read as zero (range check of the
+// buffer resource).  The activation's scale bytes of a step's block lie side
+// by side and come along as one load; the weights' scales of the whole tile
+// are laid out in LDS as 32-bit values first.
+// EXACT: bfloat16 instructions (float32 outputs).
+template <int FM, int FN, int WM, int WN, bool F32SCALE, bool EXACT>
+__global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p) {
+  constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN, WAVES = WM * WN;
+  constexpr int XB = BM * kBK, WB = BN * kBK;
+  constexpr int STAGE = XB + WB + 256;  // + the rows' scales
+  constexpr int PIECES = (XB + WB) / 1024;  // 1 KB: 8 rows
+  constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;  // weight scale rows of a tile
+  static_assert(BM <= 256 && PIECES % WAVES == 0, "one load of scales, the others split evenly");
+  static_assert(kFp8Block % (32 * FN) == 0 || (32 * FN) % kFp8Block == 0, "blocks in one scale row");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  unsigned* wscale = reinterpret_cast<unsigned*>(smem + 2 * STAGE);  // [NBW][kb]
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int K = p.K, kb = p.kb;
+  // Tiles in groups of kGroupM tile rows, walked column by column and dealt
+  // XCD by XCD, so that neighbours share an L2.
+  const int t = xcd_slot(blockIdx.x, gridDim.x);
+  const int per_group = kGroupM * p.tiles_n;
+  const int first = t / per_group * kGroupM;
+  const int gm = p.tiles_m - first < kGroupM ? p.tiles_m - first : kGroupM;
+  const int in = t % per_group;
+  const int tm = first + in % gm, tn = in / gm;
+  int s = 0;
+  for (int i = 1; i < p.nseg; ++i)
+    if (tn >= p.seg[i].tn0) s = i;
+  const Fp8Params::Seg& sg = p.seg[s];
+  const int m0 = tm * BM, n0 = (tn - sg.tn0) * BN;
+  const int rows = p.M - m0 < BM ? p.M - m0 : BM;
+  const int cols = sg.n - n0 < BN ? sg.n - n0 : BN;
+  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(p.qx + (int64_t)m0 * K, rows * K);
+  const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(sg.qw + (int64_t)n0 * K, cols * K);
+
+  {  // the tile's weight scales (rows past n: a scale of one)
+    const int first_row = n0 / kFp8Block, nrows = (sg.n + kFp8Block - 1) / kFp8Block;
+    for (int i = threadIdx.x; i < NBW * kb; i += WAVES * 64) {
+      const int r = first_row + i / kb;
+      const int64_t at = (int64_t)r * kb + i % kb;
+      unsigned v = F32SCALE ? __float_as_uint(1.f) : 127u;
+      if (r < nrows)
+        v = F32SCALE ? static_cast<const unsigned*>(sg.sw)[at] : static_cast<const uint8_t*>(sg.sw)[at];
+      wscale[i] = v;
+    }
+  }
+
+  auto issue = [&](int step) {
+    uint8_t* st = smem + (step & 1) * STAGE;
+    const int k0 = step * kBK;
+#pragma unroll
+    for (int i = 0; i < PIECES / WAVES; ++i) {
+      const int q = wave + WAVES * i;
+      const bool is_x = q < XB / 1024;
+      const int row = (is_x ? q : q - XB / 1024) * 8 + lane / 8;
+      const int kc = k0 + ((lane & 7) ^ swz(row)) * 16;
+      const unsigned off = kc < K ? unsigned(row * K + kc) : kOutOfRange;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? xr : wr, (lds_void*)(st + q * 1024), 16, off,
+                                               0, 0, 0);
+    }
+    if (wave == 0)  // (the scales' rows are padded to a multiple of 4)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(p.sx + step * p.lds + m0, (rows + 3) & ~3),
+                                               (lds_void*)(st + XB + WB), 4, lane * 4, 0, 0, 0);
+  };
+
+  const int fr = lane & 31, fh = lane >> 5;
+  f32x16 acc[FM][FN] = {};
+  auto frag = [&](const uint8_t* base, int row, int t2) -> v8i {
+    const v4i a = *reinterpret_cast<const v4i*>(base + row * kBK + (((4 * t2 + fh) ^ swz(row)) << 4));
+    const v4i b = *reinterpret_cast<const v4i*>(base + row * kBK + (((4 * t2 + 2 + fh) ^ swz(row)) << 4));
+    return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  };
+  issue(0);
+  for (int step = 0; step < kb; ++step) {
+    waitvm<0>();
+    __syncthreads();  // the stage is whole and the other one free
+    if (step + 1 < kb) issue(step + 1);
+    const uint8_t* st = smem + (step & 1) * STAGE;
+    int sx[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      sx[i] = st[XB + WB + wm * FM * 32 + i * 32 + fr];
+    unsigned sw[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      sw[j] = wscale[(wn * FN * 32 + j * 32) / kFp8Block * kb + step];
+    if constexpr (EXACT) {
+      // Power-of-two scales ride on the conversion; a float32 weight scale is
+      // applied to the block's sum.
+      f32x16 part[FM][FN];
+      if constexpr (F32SCALE) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) part[i][j] = f32x16{};
+      }
+#pragma unroll
+      for (int t2 = 0; t2 < 2; ++t2) {
+        Bf16Frag xf[FM], wf[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          xf[i] = to_bf16(frag(st, wm * FM * 32 + i * 32 + fr, t2), e8m0_value(sx[i]));
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          wf[j] = to_bf16(frag(st + XB, wn * FN * 32 + j * 32 + fr, t2),
+                          F32SCALE ? 1.f : e8m0_value(sw[j]));
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            f32x16& c = F32SCALE ? part[i][j] : acc[i][j];
+            c = mfma_bf16(wf[j], xf[i], c);
+          }
+      }
+      if constexpr (F32SCALE) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              acc[i][j][e] = __builtin_fmaf(part[i][j][e], __uint_as_float(sw[j]), acc[i][j][e]);
+      }
+    } else if constexpr (F32SCALE) {
+      v8i xf[2][FM], wf[2][FN];
+#pragma unroll
+      for (int t2 = 0; t2 < 2; ++t2) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) xf[t2][i] = frag(st, wm * FM * 32 + i * 32 + fr, t2);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) wf[t2][j] = frag(st + XB, wn * FN * 32 + j * 32 + fr, t2);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          f32x16 part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[0][j], xf[0][i], f32x16{}, 0,
+                                                                        0, 0, 127, 0, sx[i]);
+          part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[1][j], xf[1][i], part, 0, 0, 0, 127,
+                                                                 0, sx[i]);
+          const float f = __uint_as_float(sw[j]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(part[e], f, acc[i][j][e]);
+        }
+    } else {
+#pragma unroll
+      for (int t2 = 0; t2 < 2; ++t2) {
+        v8i xf[FM], wf[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) xf[i] = frag(st, wm * FM * 32 + i * 32 + fr, t2);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) wf[j] = frag(st + XB, wn * FN * 32 + j * 32 + fr, t2);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[j], xf[i], acc[i][j], 0, 0, 0,
+                                                                        int(sw[j]), 0, sx[i]);
+      }
+    }
+  }
+  // Register e of block (i, j): column 8 (e / 4) + 4 (lane / 32) + e % 4, row lane % 32.
+  const int64_t ldy = sg.ldy;
+  const bool vec = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(sg.y) & (p.y_bf16 ? 7 : 15)) == 0;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int m = m0 + wm * FM * 32 + i * 32 + fr;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + wn * FN * 32 + j * 32 + 8 * q + 4 * fh;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[i][j][4 * q + e];
+          if (sg.bias && n + e < sg.n) v[e] += sg.bias[n + e];
+          if (p.gelu) v[e] = gelu_erf(v[e]);
+        }
+        if (m < p.M && n < sg.n)
+          store4(sg.y, (int64_t)m * ldy + n, v, sg.n - n, p.y_bf16, vec && n + 4 <= sg.n);
+      }
+  }
+}
+
+template <int FM, int FN, int WM, int WN, bool F32SCALE, bool EXACT>
+hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
+  constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
+  constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;
+  Fp8Params p{};
+  p.qx = a.qx;
+  p.sx = a.sx;
+  p.lds = a.lds;
+  p.M = int(a.m);
+  p.K = int(a.k);
+  p.kb = int((a.k + kFp8Block - 1) / kFp8Block);
+  p.nseg = a.count;
+  p.y_bf16 = a.y_bf16;
+  p.gelu = a.gelu;
+  p.tiles_m = int((a.m + BM - 1) / BM);
+  for (int i = 0; i < a.count; ++i) {
+    p.seg[i] = {a.w[i].q, a.w[i].scale, a.w[i].bias, a.w[i].y, a.w[i].ldy, int(a.w[i].n), p.tiles_n};
+    p.tiles_n += int((a.w[i].n + BN - 1) / BN);
+  }
+  const size_t lds = 2 * ((BM + BN) * kBK + 256) + size_t(NBW) * p.kb * 4;
+  const dim3 grid(unsigned(p.tiles_m) * unsigned(p.tiles_n));
+  hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, F32SCALE, EXACT>), grid, dim3(WM * WN * 64), lds,
+                     stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
+  if (!a.y_bf16)
+    return a.f32_scale ? launch_t<2, 2, 2, 2, true, true>(a, stream)
+                       : launch_t<2, 2, 2, 2, false, true>(a, stream);
+  return a.f32_scale ? launch_t<2, 2, 2, 2, true, false>(a, stream)
+                     : launch_t<2, 2, 2, 2, false, false>(a, stream);
+}
+
+}  // namespace convrot

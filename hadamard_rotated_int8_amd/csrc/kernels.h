@@ -70,4 +70,86 @@ hipError_t launch_lora_down(const void* x, bool bf16, int64_t ldx, int64_t m, in
 hipError_t launch_lora_up_add(const uint16_t* u, int64_t ldu, const uint16_t* b, int64_t m,
                               int64_t n, int r, float* y, int64_t ldy, hipStream_t stream);
 
+// FP8 (E4M3) blocks of 128: q [m, k] and E8M0 scales [ceil(k / 128), lds] of X; q [n, k]
+// and scales [ceil(n / 128), ceil(k / 128)] of W.
+hipError_t launch_fp8_pack(const void* x, bool bf16, int64_t ldx, int64_t m, int64_t k,
+                           uint8_t* q, uint8_t* scale, int64_t lds, hipStream_t stream);
+hipError_t launch_fp8_wquant(const void* w, bool bf16, int64_t ldw, int64_t n, int64_t k,
+                             uint8_t* q, uint8_t* scale, hipStream_t stream);
+
+struct Fp8Weight {
+  const uint8_t* q;
+  const void* scale;  // E8M0 bytes or float32 (Fp8GemmArgs::f32_scale)
+  const float* bias;  // or nullptr
+  void* y;
+  int64_t n, ldy;
+};
+
+struct Fp8GemmArgs {
+  const uint8_t* qx;
+  const uint8_t* sx;
+  int64_t lds, m, k;
+  int count;
+  Fp8Weight w[kMaxGemmGroup];
+  bool f32_scale, y_bf16, gelu;
+};
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream);
+
+// The norms around a block (block_norm.hip).
+constexpr int64_t kMaxNormK = 32768;
+enum { kNormNone = 0, kNormLayer = 1, kNormRms = 2 };
+
+struct VectorArgs {  // a vector of k values for each `rows` consecutive rows, or absent
+  const void* p;
+  int64_t stride, rows;
+  bool bf16;
+};
+
+struct NormArgs {
+  int kind;
+  float eps;
+  VectorArgs weight, bias;
+};
+
+struct BlockNormArgs {
+  const void* x;
+  const void* branch;  // or nullptr
+  void* h;             // of x's type, or nullptr
+  void* y;             // or nullptr
+  uint8_t* q;          // the FP8 packed y, or nullptr
+  uint8_t* q_scale;
+  int64_t m, k, ldx, ldb, ldh, ldy, lds;
+  float residual_scale;
+  bool x_bf16, branch_bf16, y_bf16;
+  VectorArgs gate, scale, shift;
+  NormArgs post, pre;
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
+
+// Rotary positions (rope.hip).
+constexpr int kMaxRopeTensors = 4;
+enum { kPosI32 = 0, kPosI64 = 1, kPosF32 = 2 };
+
+struct RopeTensor {
+  const void* x;
+  void* y;
+  int64_t xs[3], ys[3];  // element strides of batch, token and head
+  int heads;
+  bool copy_rest;  // the features outside the rotated part are copied (not in place)
+};
+
+struct RopeArgs {
+  const void* positions;
+  const double* inv_freq;  // [rot / 2]
+  const int32_t* axis;     // [rot / 2] or nullptr
+  int64_t batch, tokens, pos_batch, pos_token;
+  int count;
+  int d, rot, start;
+  float factor;
+  int pos_type;
+  bool half, inverse, x_bf16, y_bf16;
+  RopeTensor t[kMaxRopeTensors];
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+
 }  // namespace convrot

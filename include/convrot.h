@@ -67,7 +67,8 @@ typedef enum convrot_status {
 typedef enum convrot_dtype {
   CONVROT_F32 = 0,
   CONVROT_BF16 = 1,
-  CONVROT_I32 = 2
+  CONVROT_I32 = 2,
+  CONVROT_E8M0 = 3                /* a power of two as its exponent's byte; scales only */
 } convrot_dtype;
 
 typedef enum convrot_act {
@@ -251,6 +252,227 @@ typedef struct convrot_lora {
 convrot_status convrot_linear_lora(const convrot_packed* x, const convrot_weights* w,
                                    const convrot_lora* lora, int32_t count, void* const* y,
                                    const int64_t* ldy, int32_t act, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * FP8 linears: E4M3 codes with a scale for each block of 128 features.
+ *
+ * Activations have one scale per row and block, weights one per 128 x 128
+ * block:
+ *   Y[r, o] = act( sum_b sx[r, b] sw[o / 128, b] sum_{i in b} qx[r, i] qw[o, i] + bias[o] )
+ * with float32 sums.  No rotation is applied.  E4M3 is the OCP "fn" format
+ * (largest value 448, no infinity).  The library writes power-of-two scales
+ * (E8M0: the byte e + 127 stands for 2^e, 255 for NaN): the least e in
+ * [-126, 127] for which the block's largest magnitude is at most 448 2^e,
+ * and 0 for a block of zeros.  A code is then the E4M3 value nearest to
+ * x 2^-e, ties to even.  A block that holds an infinity or a NaN becomes NaN
+ * throughout.  k need not be a multiple of 128 (the last block is shorter),
+ * but k % 16 == 0 and k <= CONVROT_MAX_K.
+ * ---------------------------------------------------------------------------
+ */
+
+#define CONVROT_FP8_BLOCK 128 /* features (and weight rows) per scale */
+
+/*
+ * An FP8 activation.
+ *   q     : device E4M3 [m, k], row stride exactly k bytes, 16-byte aligned
+ *   scale : device E8M0 [ceil(k / 128), lds] bytes: the scales of one block
+ *           of features side by side, row r's at [b * lds + r]; lds >= m,
+ *           lds % 4 == 0, 4-byte aligned (bytes m .. are padding, whatever
+ *           they hold)
+ */
+typedef struct convrot_fp8_packed {
+  void* q;
+  void* scale;
+  int64_t m;
+  int64_t k;
+  int64_t lds;
+} convrot_fp8_packed;
+
+/*
+ * FP8 weights of one linear layer.
+ *   q     : device E4M3 [n, k], row stride exactly k bytes, 16-byte aligned
+ *   scale : device [ceil(n / 128), ceil(k / 128)], contiguous, of scale_dtype
+ *           (CONVROT_E8M0, or CONVROT_F32 for checkpoints with any scales)
+ *   bias  : device float32 [n], or NULL for no bias
+ */
+typedef struct convrot_fp8_weights {
+  const void* q;
+  const void* scale;
+  const float* bias;
+  int64_t n;
+  int64_t k;
+  int32_t scale_dtype;
+} convrot_fp8_weights;
+
+/*
+ * Offline weight quantisation in blocks of 128 x 128 with E8M0 scales.
+ *   w         : device [n, k] of w_dtype (CONVROT_F32 or CONVROT_BF16), row stride ldw >= k
+ *   q_out     : device E4M3 [n, k], row stride k, 16-byte aligned
+ *   scale_out : device E8M0 [ceil(n / 128), ceil(k / 128)]
+ * Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP.
+ */
+convrot_status convrot_fp8_quantize_weights(const void* w, int32_t w_dtype, int64_t n, int64_t k,
+                                            int64_t ldw, void* q_out, void* scale_out,
+                                            void* stream);
+
+/*
+ * Activation quantisation in blocks of 1 x 128 with E8M0 scales.
+ *   x   : device [m, k] of x_dtype (CONVROT_F32 or CONVROT_BF16), row stride ldx >= k, 16-byte
+ *         aligned rows
+ *   out : q, scale and lds are the caller's; the call sets m and k
+ * Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP.
+ */
+convrot_status convrot_fp8_pack_activations(const void* x, int32_t x_dtype, int64_t m, int64_t k,
+                                            int64_t ldx, convrot_fp8_packed* out, void* stream);
+
+/*
+ * One or several FP8 linears on one packed activation, in one launch.
+ * Weight i writes y[i] (row stride ldy[i] >= w[i].n) as y_dtype (CONVROT_F32
+ * or CONVROT_BF16, rounded once), after act.  All weights have the same
+ * scale_dtype.  The outputs must not overlap one another or any input; y
+ * needs its element's alignment only.
+ *   1 <= count <= CONVROT_MAX_GROUPED
+ * Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP.
+ */
+convrot_status convrot_fp8_linear_grouped(const convrot_fp8_packed* x,
+                                          const convrot_fp8_weights* w, int32_t count,
+                                          void* const* y, const int64_t* ldy, int32_t y_dtype,
+                                          int32_t act, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The norms around a transformer block, with its gate and residual.
+ *   h = residual_scale * x + gate * post(branch)       (with a branch; else h = x)
+ *   y = pre(h) * (1 + scale) + shift
+ * post and pre are
+ *   CONVROT_NORM_LAYER  (v - mean) / sqrt(mean (v - mean)^2 + eps) * weight + bias
+ *   CONVROT_NORM_RMS    v / sqrt(mean v^2 + eps) * weight + bias
+ *   CONVROT_NORM_NONE   v
+ * in float32 throughout; y is computed from h before h is rounded to its
+ * type.  gate, scale, shift, weight and bias may each be absent (data NULL):
+ * a factor of one, an addend of zero.
+ * ---------------------------------------------------------------------------
+ */
+#define CONVROT_MAX_NORM_K 32768
+
+typedef enum convrot_norm_kind {
+  CONVROT_NORM_NONE = 0,
+  CONVROT_NORM_LAYER = 1,
+  CONVROT_NORM_RMS = 2
+} convrot_norm_kind;
+
+/*
+ * Vectors of k values (CONVROT_F32 or CONVROT_BF16), `stride` elements apart,
+ * each shared by `rows` >= 1 consecutive rows: row r takes vector r / rows.
+ * data NULL: absent.  A norm's weight and bias are one vector for all rows
+ * (their stride and rows are not read).
+ */
+typedef struct convrot_vector {
+  const void* data;
+  int64_t stride;
+  int64_t rows;
+  int32_t dtype;
+} convrot_vector;
+
+typedef struct convrot_norm {
+  int32_t kind; /* convrot_norm_kind */
+  float eps;    /* >= 0 */
+  convrot_vector weight, bias;
+} convrot_norm;
+
+/*
+ *   x      : [m, k] of x_dtype, row stride ldx
+ *   branch : [m, k] of branch_dtype, row stride ldb, or NULL (then h, gate and
+ *            post are absent too, and residual_scale is 1)
+ *   h      : [m, k] of x_dtype, row stride ldh, or NULL when not wanted
+ *   y      : [m, k] of y_dtype, row stride ldy, or NULL when not wanted
+ *   packed : y as an FP8 activation (see convrot_fp8_packed; k % 16 == 0)
+ *            instead of y, or NULL; the call sets its m and k
+ * At least one output is wanted.  h or y may be x itself (same pointer, type
+ * and stride); no other output may overlap an input or another output.
+ * Pointers need their element's alignment only.  1 <= k <= CONVROT_MAX_NORM_K.
+ */
+typedef struct convrot_block {
+  const void* x;
+  const void* branch;
+  void* h;
+  void* y;
+  convrot_fp8_packed* packed;
+  int64_t m, k;
+  int64_t ldx, ldb, ldh, ldy;
+  int32_t x_dtype, branch_dtype, y_dtype;
+  float residual_scale;
+  convrot_vector gate, scale, shift;
+  convrot_norm post, pre;
+} convrot_block;
+
+/* Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP. */
+convrot_status convrot_block_norm(const convrot_block* b, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Rotary positions.  In each head of d features the pairs of the slice
+ * [start, start + rot) turn by angle = positions[token, axis[j]] * inv_freq[j]:
+ *   (a, b) -> (a c - b s, b c + a s),   c = factor cos(angle), s = factor sin(angle)
+ * (s of the opposite sign with `inverse`).  Pair j is features (2j, 2j + 1)
+ * of the slice (interleaved) or (j, j + rot / 2) (half).  The other features
+ * pass through.  Angles are formed in float64, turned in float32.
+ * ---------------------------------------------------------------------------
+ */
+#define CONVROT_MAX_ROPE_TENSORS 4
+
+typedef enum convrot_rope_layout {
+  CONVROT_ROPE_INTERLEAVED = 0,
+  CONVROT_ROPE_HALF = 1
+} convrot_rope_layout;
+
+typedef enum convrot_position_type {
+  CONVROT_POS_I32 = 0,
+  CONVROT_POS_I64 = 1,
+  CONVROT_POS_F32 = 2
+} convrot_position_type;
+
+/*
+ * One tensor [batch, tokens, heads, d] with any element strides of the first
+ * three axes (stride 1 along d).  y may be x itself with the same strides and
+ * type; otherwise they must not overlap.
+ */
+typedef struct convrot_rope_tensor {
+  const void* x;
+  void* y;
+  int64_t x_stride[3];
+  int64_t y_stride[3];
+  int64_t heads;
+} convrot_rope_tensor;
+
+/*
+ *   inv_freq  : device float64 [rot / 2]
+ *   axis      : device int32 [rot / 2], values in 0 .. axes - 1, or NULL (axis
+ *               0).  The caller answers for the values.
+ *   positions : device, of position_type: [batch, tokens, axes] with element
+ *               strides pos_stride[0] (0: the same for every batch entry) and
+ *               pos_stride[1]; the axes of a token are consecutive
+ *   x_dtype, y_dtype : CONVROT_F32 or CONVROT_BF16, the same for all tensors
+ *   rot even, 2 <= rot, 0 <= start, start + rot <= d <= 4096
+ */
+typedef struct convrot_rope {
+  const double* inv_freq;
+  const int32_t* axis;
+  const void* positions;
+  int64_t pos_stride[2];
+  int64_t batch, tokens;
+  int32_t position_type;
+  int32_t d, rot, start;
+  int32_t layout, inverse;
+  int32_t x_dtype, y_dtype;
+  float factor;
+  int32_t count; /* 1 .. CONVROT_MAX_ROPE_TENSORS */
+  convrot_rope_tensor t[CONVROT_MAX_ROPE_TENSORS];
+} convrot_rope;
+
+/* Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP. */
+convrot_status convrot_rope_apply(const convrot_rope* r, void* stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 const char* convrot_status_string(convrot_status status);
