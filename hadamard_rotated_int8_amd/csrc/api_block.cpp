@@ -234,7 +234,7 @@ convrot_status convrot_rope_apply(const convrot_rope* r, void* stream) {
   const bool empty = r->batch == 0 || r->tokens == 0;
   for (int32_t i = 0; i < r->count; ++i) {
     const convrot_rope_tensor& t = r->t[i];
-    if (t.heads < 0 || t.heads > (int64_t(1) << 20)) return CONVROT_ERR_SHAPE;
+    if (t.heads < 0 || t.heads > 4096 || t.heads * r->d > (1 << 18)) return CONVROT_ERR_SHAPE;
     for (int j = 0; j < 3; ++j)
       if (t.x_stride[j] < 0 || t.x_stride[j] > kMaxStride || t.y_stride[j] < 0 ||
           t.y_stride[j] > kMaxStride)

@@ -123,6 +123,7 @@ struct BlockNormArgs {
   bool x_bf16, branch_bf16, y_bf16;
   VectorArgs gate, scale, shift;
   NormArgs post, pre;
+  int waves;  // of a row; the launcher's choice
 };
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
 

@@ -454,7 +454,8 @@ typedef struct convrot_rope_tensor {
  *               strides pos_stride[0] (0: the same for every batch entry) and
  *               pos_stride[1]; the axes of a token are consecutive
  *   x_dtype, y_dtype : CONVROT_F32 or CONVROT_BF16, the same for all tensors
- *   rot even, 2 <= rot, 0 <= start, start + rot <= d <= 4096
+ *   rot even, 2 <= rot, 0 <= start, start + rot <= d <= 4096; heads <= 4096
+ *   and heads * d <= 2^18 in each tensor; batch * tokens < 2^31
  */
 typedef struct convrot_rope {
   const double* inv_freq;

@@ -173,7 +173,8 @@ def _rope(inv=FAKE, axis=0, pos=FAKE, ps=(0, 1), batch=1, tokens=4, pdt=0, d=64,
     (SHAPE, dict(batch=1 << 16, tokens=1 << 16)), (SHAPE, dict(rot=63)), (SHAPE, dict(rot=0)),
     (SHAPE, dict(rot=66)), (SHAPE, dict(rot=32, start=33)), (SHAPE, dict(rot=32, start=-1)),
     (SHAPE, dict(d=4098, rot=64)), (SHAPE, dict(d=1)), (SHAPE, dict(ps=(-1, 1))), (SHAPE, dict(ps=(0, 1 << 41))),
-    (SHAPE, dict(t=[dict(heads=-1)])), (SHAPE, dict(t=[dict(xs=(0, -1, 64))])),
+    (SHAPE, dict(t=[dict(heads=-1)])), (SHAPE, dict(t=[dict(heads=4097)])),
+    (SHAPE, dict(d=128, t=[dict(heads=2049)])), (SHAPE, dict(t=[dict(xs=(0, -1, 64))])),
     (SHAPE, dict(t=[dict(ys=(1 << 41, 1, 64))])),
     (DTYPE, dict(xdt=2)), (DTYPE, dict(ydt=3)), (DTYPE, dict(pdt=3)), (DTYPE, dict(pdt=-1)),
     (DTYPE, dict(layout=2)),
