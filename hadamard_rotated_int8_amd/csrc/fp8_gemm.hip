@@ -25,71 +25,12 @@
 // as one vector.  Which 32 features of a 64-wide slice a lane holds does not
 // matter as long as both operands agree (the sum runs over all of them and
 // the scale is the block's).
-#include "fp8.h"
-#include "kernels.h"
+#include "fp8_gemm.h"
 
 namespace convrot {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kBK = 128;  // features (bytes) per step: one scale block
-constexpr int kGroupM = 4;
-
-struct Fp8Params {
-  const uint8_t* qx;
-  const uint8_t* sx;
-  int64_t lds;
-  int M, K, kb;
-  int nseg;
-  int tiles_m, tiles_n;
-  int y_bf16, gelu;
-  struct Seg {
-    const uint8_t* qw;
-    const void* sw;
-    const float* bias;
-    void* y;
-    int64_t ldy;
-    int n, tn0;
-  } seg[kMaxGemmGroup];
-};
-
 CR_DEVICE int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
-
-CR_DEVICE unsigned bf16_pair(float a, float b) {  // two values to nearest even
-  return unsigned(__builtin_bit_cast(uint16_t, (__bf16)a)) |
-         unsigned(__builtin_bit_cast(uint16_t, (__bf16)b)) << 16;
-}
-
-// Four consecutive columns of one output row; `whole` when all four exist and
-// the row allows a vector store.
-CR_DEVICE void store4(void* y, int64_t at, const float* v, int left, bool bf16, bool whole) {
-  if (bf16) {
-    uint16_t* p = static_cast<uint16_t*>(y) + at;
-    const u32x2 w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-    if (whole) {
-      *reinterpret_cast<u32x2*>(p) = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) p[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
-    }
-  } else {
-    float* p = static_cast<float*>(y) + at;
-    if (whole) {
-      *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) p[i] = v[i];
-    }
-  }
-}
 
 // The float32 value of an E8M0 byte (255 is NaN; 0 is 2^-127, a subnormal).
 CR_DEVICE float e8m0_value(unsigned s) {
@@ -143,19 +84,9 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int K = p.K, kb = p.kb;
-  // Tiles in groups of kGroupM tile rows, walked column by column and dealt
-  // XCD by XCD, so that neighbours share an L2.
-  const int t = xcd_slot(blockIdx.x, gridDim.x);
-  const int per_group = kGroupM * p.tiles_n;
-  const int first = t / per_group * kGroupM;
-  const int gm = p.tiles_m - first < kGroupM ? p.tiles_m - first : kGroupM;
-  const int in = t % per_group;
-  const int tm = first + in % gm, tn = in / gm;
-  int s = 0;
-  for (int i = 1; i < p.nseg; ++i)
-    if (tn >= p.seg[i].tn0) s = i;
-  const Fp8Params::Seg& sg = p.seg[s];
-  const int m0 = tm * BM, n0 = (tn - sg.tn0) * BN;
+  const Fp8Tile tile = fp8_tile<BM, BN>(p, xcd_slot(blockIdx.x, gridDim.x));
+  const Fp8Params::Seg& sg = p.seg[tile.seg];
+  const int m0 = tile.m0, n0 = tile.n0;
   const int rows = p.M - m0 < BM ? p.M - m0 : BM;
   const int cols = sg.n - n0 < BN ? sg.n - n0 : BN;
   const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(p.qx + (int64_t)m0 * K, rows * K);
@@ -315,21 +246,7 @@ template <int FM, int FN, int WM, int WN, bool F32SCALE, bool EXACT>
 hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
   constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
   constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;
-  Fp8Params p{};
-  p.qx = a.qx;
-  p.sx = a.sx;
-  p.lds = a.lds;
-  p.M = int(a.m);
-  p.K = int(a.k);
-  p.kb = int((a.k + kFp8Block - 1) / kFp8Block);
-  p.nseg = a.count;
-  p.y_bf16 = a.y_bf16;
-  p.gelu = a.gelu;
-  p.tiles_m = int((a.m + BM - 1) / BM);
-  for (int i = 0; i < a.count; ++i) {
-    p.seg[i] = {a.w[i].q, a.w[i].scale, a.w[i].bias, a.w[i].y, a.w[i].ldy, int(a.w[i].n), p.tiles_n};
-    p.tiles_n += int((a.w[i].n + BN - 1) / BN);
-  }
+  const Fp8Params p = fp8_params<BM, BN>(a);
   const size_t lds = 2 * ((BM + BN) * kBK + 256) + size_t(NBW) * p.kb * 4;
   const dim3 grid(unsigned(p.tiles_m) * unsigned(p.tiles_n));
   hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, F32SCALE, EXACT>), grid, dim3(WM * WN * 64), lds,
@@ -340,6 +257,7 @@ hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
+  if (fp8_wide_wanted(a)) return launch_fp8_gemm_wide(a, stream);
   if (!a.y_bf16)
     return a.f32_scale ? launch_t<2, 2, 2, 2, true, true>(a, stream)
                        : launch_t<2, 2, 2, 2, false, true>(a, stream);

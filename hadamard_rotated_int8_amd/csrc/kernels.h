@@ -94,6 +94,9 @@ struct Fp8GemmArgs {
   bool f32_scale, y_bf16, gelu;
 };
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream);
+// Outputs with many tiles of 256 x 256 (fp8_gemm_wide.hip).
+bool fp8_wide_wanted(const Fp8GemmArgs& a);
+hipError_t launch_fp8_gemm_wide(const Fp8GemmArgs& a, hipStream_t stream);
 
 // The norms around a block (block_norm.hip).
 constexpr int64_t kMaxNormK = 32768;

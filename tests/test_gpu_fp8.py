@@ -239,3 +239,48 @@ def test_results_do_not_vary():
         first = cr.fp8_linear(x, w)
         for _ in range(5):
             assert torch.equal(cr.fp8_linear(x, w), first)
+
+
+def _on_gpu(d, w):
+    """d W^T in float64 (large references)."""
+    return (d.cuda() @ w.cuda().t()).cpu()
+
+
+WIDE = [(4096, 4096, 384), (4099, 4200, 400), (8200, 2050, 1040), (300, 33000, 656), (33000, 250, 528),
+        (4096, 4096, 2064)]
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
+@pytest.mark.parametrize("m,n,k", WIDE)
+def test_large_outputs_small_integers(m, n, k, f32):
+    """Outputs with tiles for every CU, whole and ragged."""
+    print(f"[gpu] fp8 linear large integers {m}x{n}x{k} f32scale={f32}", flush=True)
+    x, w = _integers(m, n, k, f32, m + n + k)
+    want = _on_gpu(ref.dequantised_rows(x.q, x.scale), ref.dequantised_weights(w.q, w.scale))
+    want += w.bias.cpu().double()
+    y = cr.fp8_linear(x, w, out_dtype=torch.bfloat16)
+    assert torch.equal(y.cpu(), want.float().to(torch.bfloat16))
+    # rows that allow no wide stores, nothing beside them written
+    wide = torch.full((m, n + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    cr.fp8_linear(x, w, out=wide[:, 1:n + 1])
+    assert torch.equal(wide[:, 1:n + 1], y)
+    assert (wide[:, 0] == 7).all() and (wide[:, n + 1:] == 7).all()
+
+
+@pytest.mark.parametrize("gelu", [False, True], ids=["", "gelu"])
+def test_large_grouped_random(gelu):
+    m, k = 4100, 1296
+    print(f"[gpu] fp8 grouped large gelu={gelu}", flush=True)
+    g = torch.Generator().manual_seed(9)
+    x = _inputs(m, k, torch.bfloat16, 3)
+    ws = [cr.fp8_quantize_weights((torch.randn(n, k, generator=g) * 0.02).cuda(),
+                                  torch.randn(n, generator=g).cuda() if n != 1000 else None)
+          for n in (2000, 1000, 1552)]
+    d, _ = ref.pack(x)
+    for y, w in zip(cr.fp8_linear_grouped(x.cuda(), ws, out_dtype=torch.bfloat16, gelu=gelu), ws):
+        linear = _on_gpu(d, ref.dequantised_weights(w.q, w.scale))
+        if w.bias is not None:
+            linear += w.bias.cpu().double()
+        want = ref.gelu(linear) if gelu else linear
+        off = (y.cpu().double() - want).norm()
+        assert off <= 2.0 ** -8 * want.norm() + (1.13 if gelu else 1.0) * 2.0 ** -13 * linear.norm()
