@@ -21,8 +21,10 @@
 //   * The scale bytes of a block's 256 rows are one load per wave (each wave
 //     has a copy of its own); the weight scales of a tile are fetched a tile
 //     ahead.
-//   * The load stream does not stop at a tile's end: the next tile's first
-//     half-stages arrive while this tile is stored.
+//   * Neither the loads nor the reads stop at a tile's end: the next tile's
+//     first half-stages arrive, and its first fragments are read, before this
+//     tile is stored, and its first three half-blocks wait for no store.
+//   * A tile's bias and weight scales come into LDS a tile ahead.
 //   * LDS rows are 128 bytes; 16-byte chunk c of row r sits at slot
 //     c ^ (r & 7) ^ ((r >> 3) & 1), so 16 lanes that read 16 consecutive rows
 //     touch 16 different groups of 4 banks.
@@ -43,32 +45,36 @@ constexpr int kPieces = kHalfStage / 1024 / 4; // loads per wave and half-stage 
 constexpr int kScales = 4 * kHalfStage;        // LDS offset of the scale ring: 4 blocks x 4 waves x 256 rows
 constexpr int kWScales = kScales + 4 * 4 * 256;
 constexpr int kMaxBlocks = 1042;               // CONVROT_MAX_K / 128, rounded up to pairs
-constexpr int kOut = (kWScales + 2 * 2 * kMaxBlocks + 1023) / 1024 * 1024;  // 4 KB per wave
+constexpr int kBias = (kWScales + 2 * 2 * kMaxBlocks + 1023) / 1024 * 1024;  // 2 tiles x 256 floats
+constexpr int kOut = kBias + 2048;             // 4 KB per wave
 constexpr int kLds = kOut + 4 * 4096;
 static_assert(kLds <= 160 * 1024, "LDS");
+constexpr int kStores = 32;                    // a wave's stores of a whole tile (an edge tile has more)
 constexpr int kMinBlocks = 3;
 constexpr int64_t kMaxLdy = 1 << 21;           // a tile's rows of Y lie in 31 bits
 
 CR_DEVICE int swz128(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-// One 16 x 16 x 128 product onto (FIRST: into) its accumulators.  As inline
-// assembly, since all 256 accumulation registers hold the tile: the sum has to
-// stay in its registers, and the compiler, free to choose others, spills.  It
-// also keeps the instructions where they are written (the compiler would sink
-// a tile's last ones past the next branch).  The s_nop covers a vector
-// instruction that writes an operand right before; the end of a tile waits
-// for the last results (mfma_settle).
+// One 16 x 16 x 128 product onto (FIRST: into) its accumulators.  As inline assembly, since
+// all 256 accumulation registers hold the tile: the sum has to stay in its
+// registers, and the compiler, free to choose others, spills.  It also keeps
+// the instructions where they are written (the compiler would sink a tile's
+// last ones past the next branch).  The compiler does not see that it is a
+// matrix instruction: mfma_ready goes between a vector instruction that
+// writes an operand and the first use, mfma_settle before results are read.
 template <bool FIRST>
 CR_DEVICE void mfma(f32x4& c, v8i w, v8i x, int sw, int sx) {
   if constexpr (FIRST)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "=a"(c) : "v"(w), "v"(x), "v"(sw), "v"(sx));
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]"
+                 : "=a"(c)
+                 : "v"(w), "v"(x), "v"(sw), "v"(sx));
   else
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "+a"(c) : "v"(w), "v"(x), "v"(sw), "v"(sx));
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                 : "+a"(c)
+                 : "v"(w), "v"(x), "v"(sw), "v"(sx));
 }
-// The results of 8-pass matrix instructions may be read 18 wait states later.
-CR_DEVICE void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 3" ::: "memory"); }
+CR_DEVICE void mfma_ready() { asm volatile("s_nop 3" ::: "memory"); }
+CR_DEVICE void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 3" ::: "memory"); }  // 8 passes: 18 states
 
 template <bool GELU>
 __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p, int total) {
@@ -84,19 +90,28 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
 
   // ---------------------------------------------------------------- loading
   struct Operands {  // of one tile
-    const uint8_t *x, *w;
+    __amdgpu_buffer_rsrc_t x, w;
     const uint8_t* sx;  // the tile's first row in block 0 of the scales
-    int xbytes, wbytes;
     int srows;          // scale bytes per block, padded
   };
+  // The bias of tile `it` (zeros without one and past n): 64 floats per wave.
+  auto load_bias = [&](int it) {
+    const Fp8Tile t = fp8_tile<kTile, kTile>(p, slot + it * G);
+    const Fp8Params::Seg& sg = p.seg[t.seg];
+    const int cols = sg.n - t.n0 < kTile ? sg.n - t.n0 : kTile;
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(sg.bias + (sg.bias ? t.n0 : 0), sg.bias ? cols * 4 : 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (lds_void*)(smem + kBias + (it & 1) * 1024 + wave * 256), 4, (wave * 64 + lane) * 4, 0, 0, 0);
+  };
   auto operands = [&](int it) {
-    if (it >= ntiles) return Operands{p.qx, p.qx, p.sx, 0, 0, 0};  // past the end: nothing is fetched
+    if (it >= ntiles)  // past the end: nothing is fetched
+      return Operands{buffer_rsrc(nullptr, 0), buffer_rsrc(nullptr, 0), p.sx, 0};
     const Fp8Tile t = fp8_tile<kTile, kTile>(p, slot + it * G);
     const Fp8Params::Seg& sg = p.seg[t.seg];
     const int rows = p.M - t.m0 < kTile ? p.M - t.m0 : kTile;
     const int cols = sg.n - t.n0 < kTile ? sg.n - t.n0 : kTile;
-    return Operands{p.qx + (int64_t)t.m0 * K, sg.qw + (int64_t)t.n0 * K, p.sx + t.m0,
-                    rows * K, cols * K, (rows + 3) & ~3};
+    return Operands{buffer_rsrc(p.qx + (int64_t)t.m0 * K, rows * K),
+                    buffer_rsrc(sg.qw + (int64_t)t.n0 * K, cols * K), p.sx + t.m0, (rows + 3) & ~3};
   };
   // Piece q (0 .. 15) of an operand in half-stage h: LDS rows 8 q .. +7, which
   // are rows 64 h + 8 q .. of the first wave's 128 (q < 8) or of the second's.
@@ -107,18 +122,13 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
   // The half-stage being loaded: its block, half and slot, and its scales' place.
   int lb = 0, lhalf = 0, lslot = 0, lring = 0;
   unsigned voff = 0;
-  __amdgpu_buffer_rsrc_t xr = buffer_rsrc(nullptr, 0), wr = buffer_rsrc(nullptr, 0);
-  auto begin_load = [&]() {
-    voff = lb * kBK + chunk * 16 < K ? lane_off : kOutOfRange;
-    xr = buffer_rsrc(cur.x, cur.xbytes);
-    wr = buffer_rsrc(cur.w, cur.wbytes);
-  };
+  auto begin_load = [&]() { voff = lb * kBK + chunk * 16 < K ? lane_off : kOutOfRange; };
   auto piece = [&](int i) {
     const bool is_x = i < kPieces / 2;
     const int q = wave + 4 * (is_x ? i : i - kPieces / 2);
     const int row = lhalf * 64 + (q & 7) * 8 + (q >> 3) * 128;
     uint8_t* dst = smem + lslot * kHalfStage + (is_x ? 0 : kHalfStage / 2) + q * 1024;
-    const __amdgpu_buffer_rsrc_t rs = is_x ? xr : wr;
+    const __amdgpu_buffer_rsrc_t rs = is_x ? cur.x : cur.w;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)dst, 16, voff, row * K + lb * kBK, 0, 0);
   };
   auto scale_piece = [&]() {  // (first halves) the rows' scales of the block
@@ -126,21 +136,15 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(cur.sx + lb * p.lds, lb < kb ? cur.srows : 0),
                                              (lds_void*)dst, 4, lane * 4, 0, 0, 0);
   };
-  // (No branch: the compiler would move the surrounding matrix instructions
-  // across it.)
   auto end_load = [&](bool second) {
     lslot = (lslot + 1) & 3;
     lhalf ^= 1;
     if (second) {
       lring = (lring + 1) & 3;
-      const bool last = lb + 1 == nb;
-      lb = last ? 0 : lb + 1;
-      cur.x = last ? next.x : cur.x;
-      cur.w = last ? next.w : cur.w;
-      cur.sx = last ? next.sx : cur.sx;
-      cur.xbytes = last ? next.xbytes : cur.xbytes;
-      cur.wbytes = last ? next.wbytes : cur.wbytes;
-      cur.srows = last ? next.srows : cur.srows;
+      if (++lb == nb) {
+        lb = 0;
+        cur = next;
+      }
     }
   };
   // The weight scales of tile `it`: entry e = (row e / nb, block e % nb); one
@@ -187,6 +191,7 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
     for (int i = 0; i < kPieces; ++i) piece(i);
     end_load(second);
   };
+  load_bias(0);
   load_all(false);
   load_all(true);
   load_all(false);
@@ -194,38 +199,50 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
   waitvm<2 * kPieces + 1>();  // half-stages 0 and 1
   wait_lgkm0();
   barrier();
+  // The first fragments, and the loads that wait for their slot.
+#pragma unroll
+  for (int i = 0; i < 8; ++i) read_x(smem + (i / 4) * kHalfStage, 0, i);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) read_w(smem + (j / 4) * kHalfStage, 0, j);
+  sw = wsc[wn * nb];
+  wait_lgkm0();
+  barrier();
+  load_all(false);
 
   int st = 0, ring = 0;  // of the block being computed: the slot of its first half, its scales
-  // Half H of block b, with W set S.  FIRST: the tile's first block; LAST: its
-  // last, which reads no fragments ahead (they would have to live through the
-  // stores) and whose second half loads nothing (the slot is not read yet).
-  auto half = [&](auto first_t, auto last_t, auto s_t, auto h_t, int it, int b) __attribute__((always_inline)) {
-    constexpr bool FIRST = decltype(first_t)::value, LAST = decltype(last_t)::value;
+  // Half H of a block, with W set S, while the fragments of the next block
+  // (block nblk of tile nit) are read.  EARLY: one of the tile's first three,
+  // which read half-stages loaded before the last tile's stores.
+  // FIRST: the tile's first block.
+  auto half = [&](auto first_t, auto s_t, auto h_t, auto early_t, int it, int nit, int nblk) __attribute__((always_inline)) {
+    constexpr bool FIRST = decltype(first_t)::value;
+    constexpr bool EARLY = decltype(early_t)::value;
     constexpr int S = decltype(s_t)::value, H = decltype(h_t)::value;
-    constexpr bool LOAD = !(LAST && H == 1);
     const uint8_t* nx = smem + ((st + 2 + H) & 3) * kHalfStage;
     const int nring = (ring + 1) & 3;
 #pragma unroll
     for (int idx = 0; idx < 32; ++idx) {
       const int i = 4 * H + idx / 8, j = i == 7 ? (idx + 4) % 8 : idx % 8;
+      if (idx == 0) mfma_ready();
       mfma<FIRST>(acc[i][j], j < 4 ? wf[S][j & 3] : wl[j & 3], xf[i], sw, sx[i]);
       __builtin_amdgcn_sched_barrier(0);
       if (idx == 3) {
-        // The half-stage read next has landed once only the loads of the two
-        // after it may be in flight (one of them brings a block's scales);
-        // every wave has read the one before it.
-        waitvm<2 * kPieces + 1>();
+        // The half-stage read here has landed once only the loads of the two
+        // after it (one of them brings a block's scales) and stores behind them
+        // may be in flight; every wave has read the one before it.
+        if (EARLY && it > 0)
+          waitvm<2 * kPieces + 1 + kStores>();
+        else
+          waitvm<2 * kPieces + 1>();
         wait_lgkm0();
         barrier();
-        if (LOAD) begin_load();
+        begin_load();
       }
-      if (!LAST) {
-        if (idx % 8 == 7) read_x(nx, nring, i);
-        if (H == 0 && idx % 8 == 4) read_w(nx, 1 - S, idx / 8);
-        if (H == 1 && idx >= 24 && idx < 28) read_w(nx, 0, j);
-        if (H == 1 && idx == 10) nsw = wsc[((it & 1) * 2 + wn) * nb + b + 1];
-      }
-      if (LOAD && idx > 3) {
+      if (idx % 8 == 7) read_x(nx, nring, i);
+      if (H == 0 && idx % 8 == 4) read_w(nx, 1 - S, idx / 8);
+      if (H == 1 && idx >= 24 && idx < 28) read_w(nx, 0, j);
+      if (H == 1 && idx == 10) nsw = wsc[((nit & 1) * 2 + wn) * nb + nblk];
+      if (idx > 3) {
         constexpr int slots = 28;
 #pragma unroll
         for (int d = 0; d < kPieces; ++d)
@@ -234,11 +251,11 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (LOAD) end_load(H == 0);
+    end_load(H == 0);
     if (H == 1) {
       st = (st + 2) & 3;
       ring = nring;
-      if (!LAST) sw = nsw;
+      sw = nsw;
     }
   };
   using Yes = std::true_type;
@@ -254,40 +271,24 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
     const int e0 = threadIdx.x;
     unsigned ws0 = 127;
     if (more && e0 < 2 * nb) ws0 = wscale_at(it + 1, e0);
-    // The tile's first fragments (both half-stages have landed), and the loads
-    // that wait for their slot.
-    {
-      const uint8_t* s0 = smem + st * kHalfStage;
-      const uint8_t* s1 = smem + ((st + 1) & 3) * kHalfStage;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) read_x(i < 4 ? s0 : s1, ring, i);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) read_w(j < 4 ? s0 : s1, 0, j);
-      sw = wsc[((it & 1) * 2 + wn) * nb];
-      wait_lgkm0();
-      barrier();
-      load_all(false);
-    }
-    half(Yes{}, No{}, I0{}, I0{}, it, 0);
-    half(Yes{}, No{}, I0{}, I1{}, it, 0);
-    half(No{}, No{}, I1{}, I0{}, it, 1);
-    half(No{}, No{}, I1{}, I1{}, it, 1);
+    half(Yes{}, I0{}, I0{}, Yes{}, it, it, 1);
+    if (more) load_bias(it + 1);  // (behind a barrier: every wave has stored the tile before)
+    half(Yes{}, I0{}, I1{}, Yes{}, it, it, 1);
+    half(No{}, I1{}, I0{}, Yes{}, it, it, 2);
+    half(No{}, I1{}, I1{}, No{}, it, it, 2);
     if (more) {
       uint8_t* d = wsc + ((it + 1) & 1) * 2 * nb;
       if (e0 < 2 * nb) d[e0] = uint8_t(ws0);
 #pragma unroll 1
       for (int e = e0 + 256; e < 2 * nb; e += 256) d[e] = uint8_t(wscale_at(it + 1, e));
     }
-    for (int b = 2; b < nb - 2; b += 2) {
-      half(No{}, No{}, I0{}, I0{}, it, b);
-      half(No{}, No{}, I0{}, I1{}, it, b);
-      half(No{}, No{}, I1{}, I0{}, it, b + 1);
-      half(No{}, No{}, I1{}, I1{}, it, b + 1);
+    for (int b = 2; b < nb; b += 2) {
+      const bool end = b + 2 == nb;  // (past the last tile: scales that nobody uses)
+      half(No{}, I0{}, I0{}, No{}, it, it, b + 1);
+      half(No{}, I0{}, I1{}, No{}, it, it, b + 1);
+      half(No{}, I1{}, I0{}, No{}, it, it, b + 2);
+      half(No{}, I1{}, I1{}, No{}, it, end ? it + 1 : it, end ? 0 : b + 2);
     }
-    half(No{}, No{}, I0{}, I0{}, it, nb - 2);
-    half(No{}, No{}, I0{}, I1{}, it, nb - 2);
-    half(No{}, Yes{}, I1{}, I0{}, it, nb - 1);
-    half(No{}, Yes{}, I1{}, I1{}, it, nb - 1);
     mfma_settle();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -307,8 +308,6 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
     const int cols = sg.n - t.n0;
     const int ldy = int(sg.ldy);
     uint16_t* y = static_cast<uint16_t*>(sg.y);
-    const __amdgpu_buffer_rsrc_t br =
-        buffer_rsrc(sg.bias ? sg.bias + t.n0 : nullptr, sg.bias ? (cols < kTile ? cols : kTile) * 4 : 0);
     // A resource over the tile's rows (those past M are outside it); row
     // blocks go into the scalar offset.  (ldy < kMaxLdy: see fp8_wide_wanted.)
     const int rows = p.M - t.m0 < kTile ? p.M - t.m0 : kTile;
@@ -318,11 +317,7 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
     const int c = wn * 128 + 8 * fr;  // the lane's first column when it stores
     const unsigned yoff = unsigned((wm * 128 + fg) * ldy + c) * 2;
     uint8_t* out = smem + kOut + wave * 4096;
-    f32x4 bias[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      bias[j] = __builtin_bit_cast(
-          f32x4, __builtin_amdgcn_raw_buffer_load_b128(br, unsigned(wn * 128 + 16 * j + 4 * fg) * 4, 0, 0));
+    const uint8_t* bias = smem + kBias + (it & 1) * 1024;
     auto store = [&](auto whole_t) __attribute__((always_inline)) {
       constexpr bool WHOLE = decltype(whole_t)::value;
 #pragma unroll
@@ -332,7 +327,7 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
         for (int j = 0; j < 8; ++j) {
           f32x4 v = acc[i][j];
           asm volatile("" : "+v"(v));  // (leaves the accumulators' half of the registers here, not earlier)
-          v += bias[j];
+          v += *reinterpret_cast<const f32x4*>(bias + (wn * 128 + 16 * j + 4 * fg) * 4);
           if constexpr (GELU) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = gelu_erf(v[e]);
