@@ -30,8 +30,8 @@
 //     touch 16 different groups of 4 banks.
 //   * Bytes past K and rows past M or n read as zero, in both operands (a
 //     NaN code of another row must not meet even a zero).
-//   * A tile is stored 16 rows at a time through 4 KB of LDS per wave, as
-//     whole 256-byte row pieces.
+//   * A tile is stored 16 rows x 64 columns at a time through LDS, as whole
+//     128-byte lines, non-temporal (Y should not push operands out of L2).
 #include <type_traits>
 
 #include "fp8_gemm.h"
@@ -297,9 +297,11 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
       for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));  // (not read before here)
 
     // Store.  Register e of block (i, j): column 16 j + 4 (lane / 16) + e, row
-    // 16 i + lane % 16.  Sixteen rows at a time go through the wave's LDS
-    // area (256-byte rows, chunk c of row r at slot c ^ r) and leave as
-    // pieces of 256 bytes, 4 rows to a store.
+    // 16 i + lane % 16.  Step s: 16 rows x 64 columns go through the wave's LDS
+    // area (one of two of 2 KB: 128-byte rows, chunk c of row r at slot
+    // c ^ (r & 7)) and leave as whole 128-byte lines, 8 rows to a store, one
+    // step later, under the next one's conversions.  (The area is the wave's
+    // own: its LDS accesses stay in order.)
     // (Lane numbers are re-formed here rather than kept through the K loop.)
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
@@ -314,40 +316,56 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
     const bool whole = cols >= kTile && (ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const __amdgpu_buffer_rsrc_t yr = buffer_rsrc(
         y + (int64_t)t.m0 * ldy + t.n0, ((rows - 1) * ldy + (cols < kTile ? cols : kTile)) * 2);
-    const int c = wn * 128 + 8 * fr;  // the lane's first column when it stores
-    const unsigned yoff = unsigned((wm * 128 + fg) * ldy + c) * 2;
+    const int sr = lane >> 3, sc = (lane & 7) * 8;  // the lane's row and first column when it stores
+    const unsigned yoff = unsigned((wm * 128 + sr) * ldy + wn * 128 + sc) * 2;
     uint8_t* out = smem + kOut + wave * 4096;
-    const uint8_t* bias = smem + kBias + (it & 1) * 1024;
+    f32x4 bias[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      bias[j] = *reinterpret_cast<const f32x4*>(smem + kBias + (it & 1) * 1024 + (wn * 128 + 16 * j + 4 * fg) * 4);
     auto store = [&](auto whole_t) __attribute__((always_inline)) {
       constexpr bool WHOLE = decltype(whole_t)::value;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int s = 0; s <= 16; ++s) {
         __builtin_amdgcn_sched_barrier(0);
+        u32x4 w[2] = {};
+        if (s > 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f32x4 v = acc[i][j];
-          asm volatile("" : "+v"(v));  // (leaves the accumulators' half of the registers here, not earlier)
-          v += *reinterpret_cast<const f32x4*>(bias + (wn * 128 + 16 * j + 4 * fg) * 4);
-          if constexpr (GELU) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = gelu_erf(v[e]);
-          }
-          const int ch = 2 * j + (fg >> 1);
-          *reinterpret_cast<u32x2*>(out + fr * 256 + ((ch ^ fr) << 4) + (fg & 1) * 8) =
-              u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+          for (int k = 0; k < 2; ++k)
+            w[k] = *reinterpret_cast<const u32x4*>(out + ((s - 1) & 1) * 2048 + (8 * k + sr) * 128 +
+                                                   (((lane & 7) ^ sr) << 4));
         }
+        if (s < 16) {
+          const int i = s >> 1;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {  // (the wave's own area: its LDS accesses stay in order)
-          const int r = 4 * s + fg;
-          const u32x4 w = *reinterpret_cast<const u32x4*>(out + r * 256 + ((fr ^ r) << 4));
-          const int soff = (16 * i + 4 * s) * ldy * 2;
-          if constexpr (WHOLE) {
-            __builtin_amdgcn_raw_buffer_store_b128(w, yr, yoff, soff, 0);
-          } else {
+          for (int jj = 0; jj < 4; ++jj) {
+            const int j = 4 * (s & 1) + jj;
+            f32x4 v = acc[i][j];
+            asm volatile("" : "+v"(v));  // (leaves the accumulators' half of the registers here, not earlier)
+            v += bias[j];
+            if constexpr (GELU) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              __builtin_amdgcn_raw_buffer_store_b16(uint16_t(w[e / 2] >> (16 * (e & 1))), yr,
-                                                    c + e < cols ? yoff + e * 2 : kOutOfRange, soff, 0);
+              for (int e = 0; e < 4; ++e) v[e] = gelu_erf(v[e]);
+            }
+            *reinterpret_cast<u32x2*>(out + (s & 1) * 2048 + fr * 128 +
+                                      (((2 * jj + (fg >> 1)) ^ (fr & 7)) << 4) + (fg & 1) * 8) =
+                u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+          }
+        }
+        if (s > 0) {
+          const int i = (s - 1) >> 1, col = ((s - 1) & 1) * 64;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int soff = (16 * i + 8 * k) * ldy * 2;
+            if constexpr (WHOLE) {
+              __builtin_amdgcn_raw_buffer_store_b128(w[k], yr, yoff + col * 2, soff, kNonTemporal);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                __builtin_amdgcn_raw_buffer_store_b16(
+                    uint16_t(w[k][e / 2] >> (16 * (e & 1))), yr,
+                    wn * 128 + col + sc + e < cols ? yoff + (col + e) * 2 : kOutOfRange, soff, 0);
+            }
           }
         }
       }
