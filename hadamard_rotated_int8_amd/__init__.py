@@ -52,6 +52,7 @@ EXPORTED = (
     "convrot_fp8_quantize_weights",
     "convrot_fp8_pack_activations",
     "convrot_fp8_linear_grouped",
+    "convrot_fp8_linear_rows",
     "convrot_block_norm",
     "convrot_rope_apply",
     "convrot_status_string",
@@ -136,6 +137,8 @@ def lib() -> ctypes.CDLL:
         L.convrot_fp8_pack_activations.restype = ctypes.c_int
         L.convrot_fp8_linear_grouped.argtypes = [vp, vp, i32, vp, vp, i32, i32, vp]
         L.convrot_fp8_linear_grouped.restype = ctypes.c_int
+        L.convrot_fp8_linear_rows.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, i32, i32, vp]
+        L.convrot_fp8_linear_rows.restype = ctypes.c_int
         L.convrot_block_norm.argtypes = [vp, vp]
         L.convrot_block_norm.restype = ctypes.c_int
         L.convrot_rope_apply.argtypes = [vp, vp]

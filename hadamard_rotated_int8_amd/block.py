@@ -26,6 +26,7 @@ import torch
 from . import ACT_GELU, ACT_NONE, BF16, E8M0, F32, MAX_GROUPED, OK, ConvrotError, lib
 
 FP8_BLOCK = 128
+FP8_MAX_ROWS = 16  # rows that are quantised inside the linear
 MAX_NORM_K = 32768
 MAX_ROPE_TENSORS = 4
 
@@ -203,12 +204,16 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
     """
     if not ws or len(ws) > MAX_GROUPED:
         raise ValueError(f"1 to {MAX_GROUPED} weights")
-    if not isinstance(x, Fp8Activation):
-        x = fp8_pack_activations(x)
-        dev = x.q.device
-    else:
+    rows = None
+    if isinstance(x, Fp8Activation):
         dev = _check_activation(x)
-    m, k = x.q.shape
+        m, k = x.q.shape
+    else:
+        dev = _device(x, "x")
+        rows = _rows(x, "x")
+        m, k = x.shape
+        if m > FP8_MAX_ROWS:
+            x, rows = fp8_pack_activations(x), None
     dt = _DTYPE.get(out_dtype)
     if dt is None:
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
@@ -239,10 +244,14 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
             _rows(o, "an output", dev, (m, w.q.shape[0]))
             _writable_rows(o, "an output")
     count = len(ws)
-    _launch(lib().convrot_fp8_linear_grouped, "convrot_fp8_linear_grouped", dev, _pack_args(x),
-            b"".join(packed), count, struct.pack(f"={count}Q", *[o.data_ptr() for o in outs]),
+    args = (b"".join(packed), count, struct.pack(f"={count}Q", *[o.data_ptr() for o in outs]),
             struct.pack(f"={count}q", *[_row_stride(o) for o in outs]), dt,
             ACT_GELU if gelu else ACT_NONE)
+    if rows is None:
+        _launch(lib().convrot_fp8_linear_grouped, "convrot_fp8_linear_grouped", dev, _pack_args(x), *args)
+    else:
+        _launch(lib().convrot_fp8_linear_rows, "convrot_fp8_linear_rows", dev, x.data_ptr(), rows, m, k,
+                _row_stride(x), *args)
     return outs
 
 

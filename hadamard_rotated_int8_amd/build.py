@@ -26,7 +26,7 @@ CEILING_LIB_PATH = os.path.join(PKG_DIR, "libconvrot_ceiling.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "pack.hip", "wprep.hip", "gemm.hip", "gemm_small.hip", "lora.hip",
-           "api_block.cpp", "fp8_pack.hip", "fp8_gemm.hip", "fp8_gemm_wide.hip", "block_norm.hip", "rope.hip"]
+           "api_block.cpp", "fp8_pack.hip", "fp8_gemm.hip", "fp8_gemm_wide.hip", "fp8_gemm_rows.hip", "block_norm.hip", "rope.hip"]
 CEILING_SOURCES = ["ceiling.hip"]
 
 # Packed-FP32 instructions are kept out of generated code on purpose.

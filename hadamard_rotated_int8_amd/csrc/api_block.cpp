@@ -70,6 +70,41 @@ convrot_status check_matrix(const void* p, int32_t dtype, int64_t ld, int64_t k)
   return aligned(p, size_of(dtype)) ? CONVROT_OK : CONVROT_ERR_UNSUPPORTED;
 }
 
+// The weights and outputs of an FP8 linear whose m and k are filled in; fills
+// the launch's weights (those with rows) and modes.
+convrot_status check_fp8_linear(const convrot_fp8_weights* w, int32_t count, void* const* y,
+                                const int64_t* ldy, int32_t y_dtype, int32_t act,
+                                convrot::Fp8GemmArgs* a) {
+  if (!w || !y || !ldy) return CONVROT_ERR_NULL;
+  if (count < 1 || count > CONVROT_MAX_GROUPED) return CONVROT_ERR_SHAPE;
+  const convrot_status st = check_k(a->k);
+  if (st != CONVROT_OK) return st;
+  if (a->m < 0 || a->m > kMaxRows) return CONVROT_ERR_SHAPE;
+  if (!float_type(y_dtype)) return CONVROT_ERR_DTYPE;
+  if (act != CONVROT_ACT_NONE && act != CONVROT_ACT_GELU) return CONVROT_ERR_DTYPE;
+  a->f32_scale = w[0].scale_dtype == CONVROT_F32;
+  a->y_bf16 = y_dtype == CONVROT_BF16;
+  a->gelu = act == CONVROT_ACT_GELU;
+  int64_t tiles = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const convrot_fp8_weights& wi = w[i];
+    if (wi.k != a->k || wi.n < 0 || wi.n > kMaxRows || ldy[i] < wi.n || ldy[i] > kMaxStride)
+      return CONVROT_ERR_SHAPE;
+    if ((wi.scale_dtype != CONVROT_F32 && wi.scale_dtype != CONVROT_E8M0) ||
+        wi.scale_dtype != w[0].scale_dtype)
+      return CONVROT_ERR_DTYPE;
+    if (wi.n == 0 || a->m == 0) continue;  // empty weights launch nothing
+    if (!wi.q || !wi.scale || !y[i]) return CONVROT_ERR_NULL;
+    if (!aligned16(wi.q) || (a->f32_scale && !aligned(wi.scale, 4)) ||
+        (wi.bias && !aligned(wi.bias, 4)) || !aligned(y[i], size_of(y_dtype)))
+      return CONVROT_ERR_UNSUPPORTED;
+    a->w[a->count++] = {static_cast<const uint8_t*>(wi.q), wi.scale, wi.bias, y[i], wi.n, ldy[i]};
+    tiles += (wi.n + 31) / 32;
+  }
+  // (32 x 32 tiles, smaller than any kernel's, are counted in 32 bits)
+  return tiles * ((a->m + 31) / 32) > int64_t(INT32_MAX) ? CONVROT_ERR_SHAPE : CONVROT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -119,46 +154,42 @@ convrot_status convrot_fp8_linear_grouped(const convrot_fp8_packed* x,
                                           const convrot_fp8_weights* w, int32_t count,
                                           void* const* y, const int64_t* ldy, int32_t y_dtype,
                                           int32_t act, void* stream) {
-  if (!x || !w || !y || !ldy) return CONVROT_ERR_NULL;
-  if (count < 1 || count > CONVROT_MAX_GROUPED) return CONVROT_ERR_SHAPE;
-  convrot_status st = check_k(x->k);
-  if (st != CONVROT_OK) return st;
-  if (x->m < 0 || x->m > kMaxRows) return CONVROT_ERR_SHAPE;
-  st = check_fp8_stride(x->lds, x->m);
-  if (st != CONVROT_OK) return st;
-  if (!float_type(y_dtype)) return CONVROT_ERR_DTYPE;
-  if (act != CONVROT_ACT_NONE && act != CONVROT_ACT_GELU) return CONVROT_ERR_DTYPE;
+  if (!x) return CONVROT_ERR_NULL;
   convrot::Fp8GemmArgs a{};
   a.qx = static_cast<const uint8_t*>(x->q);
   a.sx = static_cast<const uint8_t*>(x->scale);
   a.lds = x->lds;
   a.m = x->m;
   a.k = x->k;
-  a.f32_scale = w[0].scale_dtype == CONVROT_F32;
-  a.y_bf16 = y_dtype == CONVROT_BF16;
-  a.gelu = act == CONVROT_ACT_GELU;
-  int64_t tiles = 0;
-  for (int32_t i = 0; i < count; ++i) {
-    const convrot_fp8_weights& wi = w[i];
-    if (wi.k != x->k || wi.n < 0 || wi.n > kMaxRows || ldy[i] < wi.n || ldy[i] > kMaxStride)
-      return CONVROT_ERR_SHAPE;
-    if ((wi.scale_dtype != CONVROT_F32 && wi.scale_dtype != CONVROT_E8M0) ||
-        wi.scale_dtype != w[0].scale_dtype)
-      return CONVROT_ERR_DTYPE;
-    if (wi.n == 0 || x->m == 0) continue;  // empty weights launch nothing
-    if (!wi.q || !wi.scale || !y[i]) return CONVROT_ERR_NULL;
-    if (!aligned16(wi.q) || (a.f32_scale && !aligned(wi.scale, 4)) ||
-        (wi.bias && !aligned(wi.bias, 4)) || !aligned(y[i], size_of(y_dtype)))
-      return CONVROT_ERR_UNSUPPORTED;
-    a.w[a.count++] = {static_cast<const uint8_t*>(wi.q), wi.scale, wi.bias, y[i], wi.n, ldy[i]};
-    tiles += (wi.n + 63) / 64;
-  }
-  // (64 x 64 tiles, the smallest, are counted in 32 bits)
-  if (tiles * ((x->m + 63) / 64) > int64_t(INT32_MAX)) return CONVROT_ERR_SHAPE;
+  convrot_status st = check_fp8_linear(w, count, y, ldy, y_dtype, act, &a);
+  if (st != CONVROT_OK) return st;
+  st = check_fp8_stride(x->lds, x->m);
+  if (st != CONVROT_OK) return st;
   if (x->m == 0 || a.count == 0) return CONVROT_OK;
   st = check_fp8_buffers(x);
   if (st != CONVROT_OK) return st;
   return from_hip(convrot::launch_fp8_gemm(a, static_cast<hipStream_t>(stream)));
+}
+
+convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m, int64_t k,
+                                       int64_t ldx, const convrot_fp8_weights* w, int32_t count,
+                                       void* const* y, const int64_t* ldy, int32_t y_dtype,
+                                       int32_t act, void* stream) {
+  if (m > CONVROT_FP8_MAX_ROWS) return CONVROT_ERR_SHAPE;
+  convrot::Fp8GemmArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.x_bf16 = x_dtype == CONVROT_BF16;
+  a.m = m;
+  a.k = k;
+  const convrot_status st = check_fp8_linear(w, count, y, ldy, y_dtype, act, &a);
+  if (st != CONVROT_OK) return st;
+  if (ldx < k || ldx > kMaxStride) return CONVROT_ERR_SHAPE;
+  if (!float_type(x_dtype)) return CONVROT_ERR_DTYPE;
+  if (m == 0 || a.count == 0) return CONVROT_OK;
+  if (!x) return CONVROT_ERR_NULL;
+  if (!aligned16(x) || (ldx * size_of(x_dtype)) % 16 != 0) return CONVROT_ERR_UNSUPPORTED;
+  return from_hip(convrot::launch_fp8_gemm_rows(a, static_cast<hipStream_t>(stream)));
 }
 
 convrot_status convrot_block_norm(const convrot_block* b, void* stream) {

@@ -109,4 +109,26 @@ CR_DEVICE void store4(void* y, int64_t at, const float* v, int left, bool bf16, 
   }
 }
 
+// The float32 value of an E8M0 byte (255 is NaN; 0 is 2^-127, a subnormal).
+CR_DEVICE float e8m0_value(unsigned s) {
+  return __uint_as_float(s == 0 ? 0x400000u : s == kFp8ScaleNan ? 0x7FC00000u : s << 23);
+}
+
+// 32 E4M3 codes times a power of two, as four bfloat16 operands.
+struct Bf16Frag {
+  bf16x8 v[4];
+};
+CR_DEVICE Bf16Frag to_bf16(v8i q, float scale) {
+  Bf16Frag r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(q[i]), scale, false);
+    const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(q[i]), scale, true);
+    r.v[i / 2][4 * (i & 1)] = lo[0];
+    r.v[i / 2][4 * (i & 1) + 1] = lo[1];
+    r.v[i / 2][4 * (i & 1) + 2] = hi[0];
+    r.v[i / 2][4 * (i & 1) + 3] = hi[1];
+  }
+  return r;
+}
 }  // namespace convrot

@@ -32,28 +32,6 @@ namespace {
 
 CR_DEVICE int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-// The float32 value of an E8M0 byte (255 is NaN; 0 is 2^-127, a subnormal).
-CR_DEVICE float e8m0_value(unsigned s) {
-  return __uint_as_float(s == 0 ? 0x400000u : s == kFp8ScaleNan ? 0x7FC00000u : s << 23);
-}
-
-// 32 E4M3 codes times a power of two, as four bfloat16 operands.
-struct Bf16Frag {
-  bf16x8 v[4];
-};
-CR_DEVICE Bf16Frag to_bf16(v8i q, float scale) {
-  Bf16Frag r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(q[i]), scale, false);
-    const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(q[i]), scale, true);
-    r.v[i / 2][4 * (i & 1)] = lo[0];
-    r.v[i / 2][4 * (i & 1) + 1] = lo[1];
-    r.v[i / 2][4 * (i & 1) + 2] = hi[0];
-    r.v[i / 2][4 * (i & 1) + 3] = hi[1];
-  }
-  return r;
-}
 CR_DEVICE f32x16 mfma_bf16(const Bf16Frag& a, const Bf16Frag& b, f32x16 c) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v[i], b.v[i], c, 0, 0, 0);
@@ -257,6 +235,7 @@ hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
+  if (a.m <= kFp8FewRows) return launch_fp8_gemm_rows(a, stream);
   if (fp8_wide_wanted(a)) return launch_fp8_gemm_wide(a, stream);
   if (!a.y_bf16)
     return a.f32_scale ? launch_t<2, 2, 2, 2, true, true>(a, stream)

@@ -341,6 +341,20 @@ convrot_status convrot_fp8_linear_grouped(const convrot_fp8_packed* x,
                                           int32_t act, void* stream);
 
 /*
+ * The same on X itself (at most CONVROT_FP8_MAX_ROWS rows), which is quantised
+ * on the way as convrot_fp8_pack_activations does, in one launch: for single
+ * tokens.
+ *   x : device [m, k] of x_dtype (CONVROT_F32 or CONVROT_BF16), row stride ldx >= k, 16-byte
+ *       aligned rows
+ * Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP.
+ */
+#define CONVROT_FP8_MAX_ROWS 16
+convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m, int64_t k,
+                                       int64_t ldx, const convrot_fp8_weights* w, int32_t count,
+                                       void* const* y, const int64_t* ldy, int32_t y_dtype,
+                                       int32_t act, void* stream);
+
+/*
  * ---------------------------------------------------------------------------
  * The norms around a transformer block, with its gate and residual.
  *   h = residual_scale * x + gate * post(branch)       (with a branch; else h = x)

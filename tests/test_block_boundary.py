@@ -90,8 +90,26 @@ def test_fp8_linear_refusals(want, args):
     assert _linear(**args) == want
 
 
+def _linear_rows(x=FAKE, dt=cr.BF16, m=4, k=256, ldx=256, n=64, wk=256, q=FAKE, y=FAKE, ldy=64, ydt=cr.F32,
+                 act=cr.ACT_NONE, count=1):
+    return cr.lib().convrot_fp8_linear_rows(
+        x, dt, m, k, ldx, block._FP8_WEIGHTS.pack(q, FAKE, 0, n, wk, cr.E8M0), count, struct.pack("=Q", y),
+        struct.pack("=q", ldy), ydt, act, None)
+
+
+@cpu_only
+@pytest.mark.parametrize("want,args", [
+    (NULL, dict(x=None)), (NULL, dict(q=0)), (NULL, dict(y=0)), (SHAPE, dict(m=17)), (SHAPE, dict(m=-1)),
+    (SHAPE, dict(ldx=255)), (SHAPE, dict(wk=128)), (SHAPE, dict(ldy=63)), (SHAPE, dict(count=0)),
+    (DTYPE, dict(dt=cr.I32)), (DTYPE, dict(ydt=cr.I32)), (DTYPE, dict(act=3)),
+    (UNSUPPORTED, dict(x=FAKE + 8)), (UNSUPPORTED, dict(ldx=260)), (UNSUPPORTED, dict(k=264, wk=264, ldx=264))])
+def test_fp8_linear_rows_refusals(want, args):
+    assert _linear_rows(**args) == want
+
+
 @cpu_only
 def test_fp8_empty_calls_launch_nothing():
+    assert _linear_rows(m=0, x=None, q=0, y=0) == cr.OK
     assert _pack(m=0, x=None, q=0, scale=0) == cr.OK
     assert _linear(m=0, q=0, scale=0, y=(0,), ws=[dict(q=0, s=0)]) == cr.OK
     assert _linear(ws=[dict(n=0, q=0, s=0)], y=(0,), q=0, scale=0) == cr.OK

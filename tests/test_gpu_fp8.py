@@ -151,7 +151,7 @@ def _integers(m, n, k, f32, seed, sign_only=False):
     return cr.Fp8Activation(qx, sx.view(E8M0).t()[:m]), cr.Fp8Weights(qw, sw, bias)
 
 
-SHAPES = [(1, 1, 16), (1, 128, 128), (2, 130, 144), (7, 64, 400), (15, 300, 1040), (16, 640, 2048),
+SHAPES = [(1, 1, 16), (2, 33, 5136), (17, 100, 656), (31, 64, 4112), (32, 31, 128), (40, 257, 1040), (64, 300, 2064), (65, 64, 640), (1, 128, 128), (2, 130, 144), (7, 64, 400), (15, 300, 1040), (16, 640, 2048),
           (17, 96, 128), (33, 257, 272), (64, 128, 640), (100, 1000, 1296), (129, 129, 384),
           (256, 512, 512), (300, 770, 912), (513, 260, 528), (1, 4096, 5120), (5, 1500, 13824)]
 
