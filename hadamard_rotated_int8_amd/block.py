@@ -26,7 +26,7 @@ import torch
 from . import ACT_GELU, ACT_NONE, BF16, E8M0, F32, MAX_GROUPED, OK, ConvrotError, lib
 
 FP8_BLOCK = 128
-FP8_MAX_ROWS = 16  # rows that are quantised inside the linear
+FP8_MAX_ROWS, FP8_MAX_ROWS_BYTES = 16, 49152  # an activation that is quantised inside the linear
 MAX_NORM_K = 32768
 MAX_ROPE_TENSORS = 4
 
@@ -212,7 +212,7 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
         dev = _device(x, "x")
         rows = _rows(x, "x")
         m, k = x.shape
-        if m > FP8_MAX_ROWS:
+        if m > FP8_MAX_ROWS or m * _blocks(k) * FP8_BLOCK > FP8_MAX_ROWS_BYTES:
             x, rows = fp8_pack_activations(x), None
     dt = _DTYPE.get(out_dtype)
     if dt is None:

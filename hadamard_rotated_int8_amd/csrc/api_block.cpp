@@ -175,7 +175,9 @@ convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m
                                        int64_t ldx, const convrot_fp8_weights* w, int32_t count,
                                        void* const* y, const int64_t* ldy, int32_t y_dtype,
                                        int32_t act, void* stream) {
-  if (m > CONVROT_FP8_MAX_ROWS) return CONVROT_ERR_SHAPE;
+  static_assert(convrot::kFp8RawBytes == CONVROT_FP8_MAX_ROWS_BYTES, "header");
+  if (m > CONVROT_FP8_MAX_ROWS || (m > 0 && blocks(k) * 128 > CONVROT_FP8_MAX_ROWS_BYTES / m))
+    return CONVROT_ERR_SHAPE;
   convrot::Fp8GemmArgs a{};
   a.x = x;
   a.ldx = ldx;

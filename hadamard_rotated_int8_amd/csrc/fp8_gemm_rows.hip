@@ -1,17 +1,22 @@
 // FP8 linear for few rows of X (one token, a small batch): the weights are
 // read once, straight into registers, and that is what takes the time.
 //
-// A workgroup owns 32 rows of W; its 8 waves share the blocks of 128 features
-// round robin (so that they read neighbouring lines) and add their sums in
-// LDS in wave order.  Each wave requests kAhead blocks of W at once, two
-// 16-byte loads per lane and 16 rows, each instruction 16 rows x 64 bytes;
-// with 16 waves on a CU that is far more than HBM needs in flight.
+// A workgroup owns 32 rows of W (16 where that leaves CUs without one); its 8
+// waves share the blocks of 128 features round robin (so that they read
+// neighbouring lines) and add their sums in LDS in wave order.  Each wave
+// requests kAhead blocks of W at once, two 16-byte loads per lane and 16 rows,
+// each instruction 16 rows x 64 bytes.
 //
 // One instruction of 16 x 16 x 128 (or, for float32 outputs, four of bfloat16
 // on converted codes, see fp8_gemm.hip) multiplies 16 rows of W with 16 rows
-// of X.  X comes packed, or, for up to 16 rows, as it is: each wave then
-// quantises its own blocks in registers while W is on its way, which is less
-// than a second launch costs.
+// of X.  X comes packed, or as it is: then every workgroup quantises it into
+// LDS while its first W loads are on their way, which is less than a second
+// launch costs.  (Each wave quantising its own blocks in registers took 6 us
+// more for one row of 5120 through 13824.)
+//
+// One row, 5120 -> 13824 (71 MB): 15.3 us, 4.6 TB/s.  With 1, 2 and 4 blocks
+// requested at once instead of 3 it took about the same or spilled; 16 rows
+// of W per workgroup: 16.7; 4096 -> 4096: 8.1 us with 32 rows, 6.5 with 16.
 #include <type_traits>
 
 #include "fp8_gemm.h"
@@ -20,22 +25,37 @@ namespace convrot {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kRows = 32;   // of W per workgroup
-constexpr int kNT = kRows / 16;
-constexpr int kAhead = 4;   // blocks requested at once
-enum { kPacked = 0, kRawBf16 = 1, kRawF32 = 2 };
+constexpr int kAhead = 3;   // blocks requested at once
 
-// The maximum over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
-CR_DEVICE unsigned max_over_groups(unsigned a) {
-  const auto h = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-  a = max(h[0], h[1]);
-  const auto q = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  return max(q[0], q[1]);
+// ROW_HALF_MIRROR: lane i of each group of 8 reads lane 7 - i.
+constexpr int kDppHalfMirror = 0x141;
+
+// Sixteen consecutive features of X, 16-byte aligned.
+CR_DEVICE void load16(float* v, const void* x, bool bf16, int64_t at) {
+  if (bf16) {
+    const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at);
+    const u32x4 a[2] = {src[0], src[1]};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = bf16_lo(a[i / 4][i % 4]);
+      v[2 * i + 1] = bf16_hi(a[i / 4][i % 4]);
+    }
+  } else {
+    const f32x4* src = reinterpret_cast<const f32x4*>(static_cast<const float*>(x) + at);
+    const f32x4 a[4] = {src[0], src[1], src[2], src[3]};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = a[i / 4][i % 4];
+  }
 }
 
-template <int MT, int XSRC, bool F32SCALE, bool EXACT>
-__global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(const Fp8Params p, const void* x, int64_t ldx) {
-  __shared__ float part[kWaves][kNT * MT][64][4];
+// MT: 16-row groups of X; NT: of W; RAW: X itself, quantised here.
+template <int MT, int NT, bool RAW, bool F32SCALE, bool EXACT>
+__global__ __launch_bounds__(kWaves * 64, MT == 1 ? 4 : 2) void fp8_rows_kernel(const Fp8Params p, const void* x,
+                                                                                int64_t ldx, bool x_bf16) {
+  constexpr int kRows = 16 * NT;
+  __shared__ float part[kWaves][NT * MT][64][4];
+  __shared__ __attribute__((aligned(16))) uint8_t xlds[RAW ? kFp8RawBytes : 16];  // codes [M][128 kb]
+  __shared__ uint8_t slds[RAW ? kFp8RawBytes / kBK : 16];                         // scales [M][kb]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
@@ -50,13 +70,13 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(const Fp8Params p
 
   // Lane l: row l % 16 of 16, features 16 g .. +15 and 64 + 16 g .. +15 of a
   // block, g = l / 16 (both operands alike).
-  f32x4 acc[kNT][MT] = {};
-  for (int b0 = wave; b0 < kb; b0 += kWaves * kAhead) {
-    v4i w[kAhead][kNT][2];
+  f32x4 acc[NT][MT] = {};
+  v4i w[kAhead][NT][2];
+  auto load_w = [&](int b0) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-      for (int t = 0; t < kNT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int f = (b0 + kWaves * u) * kBK + 64 * c + 16 * fg;
@@ -64,6 +84,40 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(const Fp8Params p
               v4i, __builtin_amdgcn_raw_buffer_load_b128(
                        wr, f < K ? unsigned((16 * t + fr) * K + f) : kOutOfRange, 0, 0));
         }
+  };
+  load_w(wave);
+  if constexpr (RAW) {  // 8 threads to a block, 16 features each
+    for (int i = threadIdx.x >> 3; i < p.M * kb; i += kWaves * 8) {
+      const int row = i / kb, b = i - row * kb, f = b * kBK + 16 * int(threadIdx.x & 7);
+      float v[16];
+      if (f < K) {
+        load16(v, x, x_bf16, row * ldx + f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      }
+      unsigned top = 0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = max(top, abs_bits(v[e]));
+      top = max(top, dpp_u32<kDppQuadSwap1>(top));
+      top = max(top, dpp_u32<kDppQuadSwap2>(top));
+      top = max(top, dpp_u32<kDppHalfMirror>(top));
+      const unsigned sc = fp8_scale_of(top);
+      const float inv = fp8_inverse_scale(sc);
+      u32x4 q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        q[e] = sc == kFp8ScaleNan ? kFp8CodeNan
+                                  : fp8_codes4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv,
+                                               v[4 * e + 3] * inv);
+      *reinterpret_cast<u32x4*>(xlds + (row * kb + b) * kBK + 16 * (threadIdx.x & 7)) = q;
+      if ((threadIdx.x & 7) == 0) slds[row * kb + b] = uint8_t(sc);
+    }
+    wait_lgkm0();  // (not __syncthreads, which may wait for W)
+    barrier();
+  }
+  for (int b0 = wave; b0 < kb; b0 += kWaves * kAhead) {
+    if (b0 != wave) load_w(b0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int b = b0 + kWaves * u;
@@ -73,62 +127,24 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(const Fp8Params p
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const int row = 16 * t + fr;
-        if constexpr (XSRC == kPacked) {
-          v4i q[2] = {};
+        v4i q[2] = {};
+        sx[t] = 127u;
+        if constexpr (RAW) {
+          if (row < p.M) {
+            const uint8_t* src = xlds + (row * kb + b) * kBK + 16 * fg;
+            q[0] = *reinterpret_cast<const v4i*>(src);
+            q[1] = *reinterpret_cast<const v4i*>(src + 64);
+            sx[t] = slds[row * kb + b];
+          }
+        } else if (row < p.M) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int f = b * kBK + 64 * c + 16 * fg;
-            if (row < p.M && f < K) q[c] = *reinterpret_cast<const v4i*>(p.qx + (int64_t)row * K + f);
+            if (f < K) q[c] = *reinterpret_cast<const v4i*>(p.qx + (int64_t)row * K + f);
           }
-          xq[t] = v8i{q[0][0], q[0][1], q[0][2], q[0][3], q[1][0], q[1][1], q[1][2], q[1][3]};
-          sx[t] = row < p.M ? p.sx[b * p.lds + row] : 127u;
-        } else {
-          float v[2][16];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int f = b * kBK + 64 * c + 16 * fg;
-            if (row < p.M && f < K) {  // K % 16 == 0
-              if constexpr (XSRC == kRawBf16) {
-                const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + row * ldx + f);
-                const u32x4 a0 = src[0], a1 = src[1];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  v[c][2 * i] = bf16_lo(a0[i]);
-                  v[c][2 * i + 1] = bf16_hi(a0[i]);
-                  v[c][8 + 2 * i] = bf16_lo(a1[i]);
-                  v[c][9 + 2 * i] = bf16_hi(a1[i]);
-                }
-              } else {
-                const f32x4* src = reinterpret_cast<const f32x4*>(static_cast<const float*>(x) + row * ldx + f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const f32x4 a = src[i];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) v[c][4 * i + e] = a[e];
-                }
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[c][i] = 0.f;
-            }
-          }
-          unsigned top = 0;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = max(top, abs_bits(v[c][i]));
-          top = max_over_groups(top);
-          sx[t] = fp8_scale_of(top);
-          const float inv = fp8_inverse_scale(sx[t]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              xq[t][4 * c + i] = int(sx[t] == kFp8ScaleNan
-                                         ? kFp8CodeNan
-                                         : fp8_codes4(v[c][4 * i] * inv, v[c][4 * i + 1] * inv,
-                                                      v[c][4 * i + 2] * inv, v[c][4 * i + 3] * inv));
+          sx[t] = p.sx[b * p.lds + row];
         }
+        xq[t] = v8i{q[0][0], q[0][1], q[0][2], q[0][3], q[1][0], q[1][1], q[1][2], q[1][3]};
       }
       const int64_t at = (int64_t)(n0 / kFp8Block) * kb + b;
       float sf = 1.f;
@@ -138,7 +154,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(const Fp8Params p
       else
         se = static_cast<const uint8_t*>(sg.sw)[at];
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) {
+      for (int j = 0; j < NT; ++j) {
         const v4i* q = w[u][j];
         const v8i wq = {q[0][0], q[0][1], q[0][2], q[0][3], q[1][0], q[1][1], q[1][2], q[1][3]};
         if constexpr (EXACT) {
@@ -174,12 +190,12 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(const Fp8Params p
     }
   }
 #pragma unroll
-  for (int j = 0; j < kNT; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4*>(part[wave][j * MT + t][lane]) = acc[j][t];
   __syncthreads();
   // Element e of lane l in group (j, t): column 16 j + 4 (l / 16) + e, row 16 t + l % 16.
-  for (int g = wave; g < kNT * MT; g += kWaves) {
+  for (int g = wave; g < NT * MT; g += kWaves) {
     f32x4 v = *reinterpret_cast<const f32x4*>(part[0][g][lane]);
 #pragma unroll
     for (int i = 1; i < kWaves; ++i) v += *reinterpret_cast<const f32x4*>(part[i][g][lane]);
@@ -198,11 +214,13 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(const Fp8Params p
   }
 }
 
-template <int MT, int XSRC>
-void launch_t(const Fp8GemmArgs& a, const Fp8Params& p, dim3 grid, hipStream_t stream) {
+template <int MT, int NT, bool RAW>
+void launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
+  const Fp8Params p = fp8_params<16, 16 * NT>(a);
+  const dim3 grid(unsigned(p.tiles_n));
   auto go = [&](auto f32, auto exact) {
-    hipLaunchKernelGGL((fp8_rows_kernel<MT, XSRC, decltype(f32)::value, decltype(exact)::value>), grid,
-                       dim3(kWaves * 64), 0, stream, p, a.x, a.ldx);
+    hipLaunchKernelGGL((fp8_rows_kernel<MT, NT, RAW, decltype(f32)::value, decltype(exact)::value>), grid,
+                       dim3(kWaves * 64), 0, stream, p, a.x, a.ldx, a.x_bf16);
   };
   using Yes = std::true_type;
   using No = std::false_type;
@@ -213,19 +231,27 @@ void launch_t(const Fp8GemmArgs& a, const Fp8Params& p, dim3 grid, hipStream_t s
   }
 }
 
+template <int NT>
+void launch_nt(const Fp8GemmArgs& a, hipStream_t stream) {
+  if (a.x)
+    launch_t<1, NT, true>(a, stream);
+  else if (a.m <= 16)
+    launch_t<1, NT, false>(a, stream);
+  else if (a.m <= 32)
+    launch_t<2, NT, false>(a, stream);
+  else
+    launch_t<4, NT, false>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs& a, hipStream_t stream) {
-  const Fp8Params p = fp8_params<16, kRows>(a);
-  const dim3 grid(unsigned(p.tiles_n));
-  if (a.x)
-    a.x_bf16 ? launch_t<1, kRawBf16>(a, p, grid, stream) : launch_t<1, kRawF32>(a, p, grid, stream);
-  else if (a.m <= 16)
-    launch_t<1, kPacked>(a, p, grid, stream);
-  else if (a.m <= 32)
-    launch_t<2, kPacked>(a, p, grid, stream);
+  int64_t groups = 0;
+  for (int i = 0; i < a.count; ++i) groups += (a.w[i].n + 31) / 32;
+  if (groups < device_cu_count())
+    launch_nt<1>(a, stream);
   else
-    launch_t<4, kPacked>(a, p, grid, stream);
+    launch_nt<2>(a, stream);
   return hipGetLastError();
 }
 

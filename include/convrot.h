@@ -341,14 +341,16 @@ convrot_status convrot_fp8_linear_grouped(const convrot_fp8_packed* x,
                                           int32_t act, void* stream);
 
 /*
- * The same on X itself (at most CONVROT_FP8_MAX_ROWS rows), which is quantised
- * on the way as convrot_fp8_pack_activations does, in one launch: for single
- * tokens.
+ * The same on X itself, which is quantised on the way as
+ * convrot_fp8_pack_activations does, in one launch: for single tokens.  At
+ * most CONVROT_FP8_MAX_ROWS rows, and m * 128 * ceil(k / 128) at most
+ * CONVROT_FP8_MAX_ROWS_BYTES (48 KB of codes).
  *   x : device [m, k] of x_dtype (CONVROT_F32 or CONVROT_BF16), row stride ldx >= k, 16-byte
  *       aligned rows
  * Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP.
  */
 #define CONVROT_FP8_MAX_ROWS 16
+#define CONVROT_FP8_MAX_ROWS_BYTES 49152
 convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m, int64_t k,
                                        int64_t ldx, const convrot_fp8_weights* w, int32_t count,
                                        void* const* y, const int64_t* ldy, int32_t y_dtype,

@@ -100,7 +100,7 @@ def _linear_rows(x=FAKE, dt=cr.BF16, m=4, k=256, ldx=256, n=64, wk=256, q=FAKE, 
 @cpu_only
 @pytest.mark.parametrize("want,args", [
     (NULL, dict(x=None)), (NULL, dict(q=0)), (NULL, dict(y=0)), (SHAPE, dict(m=17)), (SHAPE, dict(m=-1)),
-    (SHAPE, dict(ldx=255)), (SHAPE, dict(wk=128)), (SHAPE, dict(ldy=63)), (SHAPE, dict(count=0)),
+    (SHAPE, dict(m=2, k=24592, wk=24592, ldx=24592)), (SHAPE, dict(ldx=255)), (SHAPE, dict(wk=128)), (SHAPE, dict(ldy=63)), (SHAPE, dict(count=0)),
     (DTYPE, dict(dt=cr.I32)), (DTYPE, dict(ydt=cr.I32)), (DTYPE, dict(act=3)),
     (UNSUPPORTED, dict(x=FAKE + 8)), (UNSUPPORTED, dict(ldx=260)), (UNSUPPORTED, dict(k=264, wk=264, ldx=264))])
 def test_fp8_linear_rows_refusals(want, args):

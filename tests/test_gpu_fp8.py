@@ -284,3 +284,19 @@ def test_large_grouped_random(gelu):
         want = ref.gelu(linear) if gelu else linear
         off = (y.cpu().double() - want).norm()
         assert off <= 2.0 ** -8 * want.norm() + (1.13 if gelu else 1.0) * 2.0 ** -13 * linear.norm()
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m,k", [(1, 16), (1, 49152), (2, 24576), (2, 24592), (9, 5120), (16, 2960), (16, 144),
+                                 (3, 13824)])
+def test_unpacked_rows_equal_packed_rows(m, k, out):
+    """Quantised inside the linear or before it, with more and fewer weight rows than CUs take: the
+    same bits."""
+    print(f"[gpu] fp8 rows {m}x{k} {out}", flush=True)
+    for dt in (torch.float32, torch.bfloat16):
+        wide = _inputs(m, 2 * k, dt, k).cuda()
+        x = wide[:, k:]  # rows 2 k apart
+        for n in (50, 8300):
+            w = cr.fp8_quantize_weights(torch.randn(n, k, device="cuda"), torch.randn(n, device="cuda"))
+            p = cr.fp8_pack_activations(x)
+            assert torch.equal(cr.fp8_linear(x, w, out_dtype=out), cr.fp8_linear(p, w, out_dtype=out))
