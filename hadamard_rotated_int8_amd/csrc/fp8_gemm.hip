@@ -15,7 +15,7 @@
 // them and drop what falls some 14 bits below the largest: the result is off
 // by 1.5e-5 of its size for normal data and 4e-5 where features differ much
 // (measured, with and without scales, the same for every K).  That is far
-// inside a bfloat16 output's rounding (2^-9), but not inside what a float32
+// inside a bfloat16 output's rounding (2^-8), but not inside what a float32
 // output promises.  Outputs in float32 therefore convert the codes to
 // bfloat16 (exact) with their scales as they leave LDS and use the bfloat16
 // instruction, which adds in full float32, at half the matrix rate.
@@ -41,23 +41,26 @@ CR_DEVICE f32x16 mfma_bf16(const Bf16Frag& a, const Bf16Frag& b, f32x16 c) {
 // One workgroup of WM x WN waves per output tile; a wave owns FM x FN blocks
 // of 32 x 32.  Operands reach LDS by direct-to-LDS loads of whole 128-byte
 // lines (16-byte chunk c of stage row r at slot c ^ swz(r), so 16 lanes that
-// read 16 consecutive rows touch 16 different groups of 4 banks), in two
-// stages.  Rows past M or n and bytes past K read as zero (range check of the
+// read 16 consecutive rows touch 16 different groups of 4 banks), in STAGES
+// stages, STAGES - 1 of them ahead of the products.  Rows past M or n and bytes past K read as zero (range check of the
 // buffer resource).  The activation's scale bytes of a step's block lie side
-// by side and come along as one load; the weights' scales of the whole tile
+// by side and come along as one load (every wave makes its own copy, so that
+// all have the same number of loads to wait for); the weights' scales of the whole tile
 // are laid out in LDS as 32-bit values first.
 // EXACT: bfloat16 instructions (float32 outputs).
-template <int FM, int FN, int WM, int WN, bool F32SCALE, bool EXACT>
+template <int FM, int FN, int WM, int WN, int STAGES, bool F32SCALE, bool EXACT>
 __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p) {
   constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN, WAVES = WM * WN;
   constexpr int XB = BM * kBK, WB = BN * kBK;
-  constexpr int STAGE = XB + WB + 256;  // + the rows' scales
+  constexpr int STAGE = XB + WB + WAVES * 256;  // + the rows' scales, a copy for each wave
   constexpr int PIECES = (XB + WB) / 1024;  // 1 KB: 8 rows
   constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;  // weight scale rows of a tile
+  constexpr int LOADS = PIECES / WAVES + 1;  // of a wave and stage
+  static_assert(STAGES >= 2 && (STAGES - 2) * LOADS <= kVmMax, "vmcnt range");
   static_assert(BM <= 256 && PIECES % WAVES == 0, "one load of scales, the others split evenly");
   static_assert(kFp8Block % (32 * FN) == 0 || (32 * FN) % kFp8Block == 0, "blocks in one scale row");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  unsigned* wscale = reinterpret_cast<unsigned*>(smem + 2 * STAGE);  // [NBW][kb]
+  unsigned* wscale = reinterpret_cast<unsigned*>(smem + STAGES * STAGE);  // [NBW][kb]
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -82,8 +85,10 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
     }
   }
 
-  auto issue = [&](int step) {
-    uint8_t* st = smem + (step & 1) * STAGE;
+  // Past the last block everything is out of range: the loads keep their
+  // number, for the waits.
+  auto issue = [&](int step, int slot) {
+    uint8_t* st = smem + slot * STAGE;
     const int k0 = step * kBK;
 #pragma unroll
     for (int i = 0; i < PIECES / WAVES; ++i) {
@@ -95,9 +100,10 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
       __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? xr : wr, (lds_void*)(st + q * 1024), 16, off,
                                                0, 0, 0);
     }
-    if (wave == 0)  // (the scales' rows are padded to a multiple of 4)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(p.sx + step * p.lds + m0, (rows + 3) & ~3),
-                                               (lds_void*)(st + XB + WB), 4, lane * 4, 0, 0, 0);
+    // (the scales' rows are padded to a multiple of 4)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        buffer_rsrc(p.sx + step * p.lds + m0, step < kb ? (rows + 3) & ~3 : 0),
+        (lds_void*)(st + XB + WB + wave * 256), 4, lane * 4, 0, 0, 0);
   };
 
   const int fr = lane & 31, fh = lane >> 5;
@@ -107,16 +113,21 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
     const v4i b = *reinterpret_cast<const v4i*>(base + row * kBK + (((4 * t2 + 2 + fh) ^ swz(row)) << 4));
     return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   };
-  issue(0);
-  for (int step = 0; step < kb; ++step) {
-    waitvm<0>();
-    __syncthreads();  // the stage is whole and the other one free
-    if (step + 1 < kb) issue(step + 1);
-    const uint8_t* st = smem + (step & 1) * STAGE;
+#pragma unroll
+  for (int t = 0; t < STAGES - 1; ++t) issue(t, t);
+  for (int step = 0, slot = 0; step < kb; ++step) {
+    // This step's stage has landed once only those behind it may be in
+    // flight; every wave has read the one before it, which is refilled.
+    waitvm<(STAGES - 2) * LOADS>();
+    wait_lgkm0();
+    barrier();
+    issue(step + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+    const uint8_t* st = smem + slot * STAGE;
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
     int sx[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-      sx[i] = st[XB + WB + wm * FM * 32 + i * 32 + fr];
+      sx[i] = st[XB + WB + wave * 256 + wm * FM * 32 + i * 32 + fr];
     unsigned sw[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -196,6 +207,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
       }
     }
   }
+  waitvm<0>();  // no load into LDS may be in flight at the end
   // Register e of block (i, j): column 8 (e / 4) + 4 (lane / 32) + e % 4, row lane % 32.
   const int64_t ldy = sg.ldy;
   const bool vec = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(sg.y) & (p.y_bf16 ? 7 : 15)) == 0;
@@ -220,16 +232,25 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
   }
 }
 
-template <int FM, int FN, int WM, int WN, bool F32SCALE, bool EXACT>
+template <int FM, int FN, int WM, int WN, int STAGES, bool F32SCALE, bool EXACT>
 hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
   constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
   constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;
   const Fp8Params p = fp8_params<BM, BN>(a);
-  const size_t lds = 2 * ((BM + BN) * kBK + 256) + size_t(NBW) * p.kb * 4;
+  const size_t lds = STAGES * ((BM + BN) * kBK + WM * WN * 256) + size_t(NBW) * p.kb * 4;
   const dim3 grid(unsigned(p.tiles_m) * unsigned(p.tiles_n));
-  hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, F32SCALE, EXACT>), grid, dim3(WM * WN * 64), lds,
+  hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, STAGES, F32SCALE, EXACT>), grid, dim3(WM * WN * 64), lds,
                      stream, p);
   return hipGetLastError();
+}
+
+template <int FM, int FN, int WM, int WN, int STAGES>
+hipError_t launch_modes(const Fp8GemmArgs& a, hipStream_t stream) {
+  if (!a.y_bf16)
+    return a.f32_scale ? launch_t<FM, FN, WM, WN, STAGES, true, true>(a, stream)
+                       : launch_t<FM, FN, WM, WN, STAGES, false, true>(a, stream);
+  return a.f32_scale ? launch_t<FM, FN, WM, WN, STAGES, true, false>(a, stream)
+                     : launch_t<FM, FN, WM, WN, STAGES, false, false>(a, stream);
 }
 
 }  // namespace
@@ -237,11 +258,25 @@ hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   if (a.m <= kFp8FewRows) return launch_fp8_gemm_rows(a, stream);
   if (fp8_wide_wanted(a)) return launch_fp8_gemm_wide(a, stream);
-  if (!a.y_bf16)
-    return a.f32_scale ? launch_t<2, 2, 2, 2, true, true>(a, stream)
-                       : launch_t<2, 2, 2, 2, false, true>(a, stream);
-  return a.f32_scale ? launch_t<2, 2, 2, 2, true, false>(a, stream)
-                     : launch_t<2, 2, 2, 2, false, false>(a, stream);
+  // Smaller tiles while the CUs would hold at most two workgroups each of
+  // them, for more of them share the loads' latency and the barriers; larger
+  // ones read the operands less often.  Measured with 64 x 64, 64 x 128 and
+  // 128 x 128 tiles (us, bfloat16 unless said): 300 x 4096 -> 4096 17.4, 21.9,
+  // 25.9; 512 x 4096 -> 4096 17.7, 22.9, 25.8; 333 x 4112 -> 4096 float32
+  // 26.9, 26.6, 39.2; 768 x 4096 -> 4096 23.8, 23.7, 27.3; 256 x 5120 ->
+  // 13824 38.8, 31.0, 36.2; 1300 x 4096 -> 4096 41.3, 34.5, 32.2; 3000 x 4096
+  // -> 4096 float32 124, 102, 93.  A stage more costs as much as it gains
+  // (26.9 against 28.0 us for 333 x 4112 -> 4096): two workgroups on a CU
+  // already cover each other's waits.
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    int64_t t = 0;
+    for (int i = 0; i < a.count; ++i) t += (a.w[i].n + bn - 1) / bn;
+    return t * ((a.m + bm - 1) / bm);
+  };
+  const int64_t two = 2 * int64_t(device_cu_count());
+  if (tiles(64, 64) <= two) return launch_modes<1, 1, 2, 2, 3>(a, stream);
+  if (tiles(64, 128) <= two) return launch_modes<1, 2, 2, 2, 2>(a, stream);
+  return launch_modes<2, 2, 2, 2, 2>(a, stream);
 }
 
 }  // namespace convrot
