@@ -92,6 +92,12 @@ def _writable_rows(x: torch.Tensor, what: str) -> None:
         raise ValueError(f"the rows of {what} must not overlap")
 
 
+def _distinct(outs) -> None:
+    at = [o.data_ptr() for o in outs if o.numel()]
+    if len(set(at)) != len(at):
+        raise ValueError("the outputs of one call must not overlap")
+
+
 # ---------------------------------------------------------------------------
 # FP8 linears
 # ---------------------------------------------------------------------------
@@ -243,6 +249,7 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
                 raise ValueError("the outputs must be of out_dtype")
             _rows(o, "an output", dev, (m, w.q.shape[0]))
             _writable_rows(o, "an output")
+        _distinct(outs)
     count = len(ws)
     args = (b"".join(packed), count, struct.pack(f"={count}Q", *[o.data_ptr() for o in outs]),
             struct.pack(f"={count}q", *[_row_stride(o) for o in outs]), dt,
@@ -551,6 +558,7 @@ def rope(x, plan: RopePlan, positions: torch.Tensor, out=None, out_dtype: torch.
         outs = list(out) if many else [out]
         if len(outs) != len(xs):
             raise ValueError("one output per tensor")
+        _distinct(outs)
         odt = outs[0].dtype
         if out_dtype is not None and odt != out_dtype:
             raise ValueError("out must be of out_dtype")

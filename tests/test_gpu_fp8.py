@@ -300,3 +300,26 @@ def test_unpacked_rows_equal_packed_rows(m, k, out):
             w = cr.fp8_quantize_weights(torch.randn(n, k, device="cuda"), torch.randn(n, device="cuda"))
             p = cr.fp8_pack_activations(x)
             assert torch.equal(cr.fp8_linear(x, w, out_dtype=out), cr.fp8_linear(p, w, out_dtype=out))
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m,n", [(1100, 2000), (2113, 2100)])
+def test_rows_do_not_depend_on_the_others(m, n, out, f32):
+    """Few rows take small output tiles and many take larger ones: the sums are the same, and so are
+    the bits of a row."""
+    print(f"[gpu] fp8 linear rows of {m}x{n} {out} f32scale={f32}", flush=True)
+    x, w = _integers(m, n, 400, f32, m + n)
+    y = cr.fp8_linear(x, w, out_dtype=out)
+    want = _on_gpu(ref.dequantised_rows(x.q, x.scale), ref.dequantised_weights(w.q, w.scale))
+    want += w.bias.cpu().double()
+    assert torch.equal(y.cpu(), want.float().to(out))
+
+    g = torch.Generator().manual_seed(n)
+    W = cr.fp8_quantize_weights((torch.randn(n, 400, generator=g) * 0.02).cuda())
+    if f32:
+        W.scale = W.scale.float() * 1.3
+    x = _inputs(m, 400, torch.bfloat16, m).cuda()
+    y = cr.fp8_linear(x, W, out_dtype=out)
+    for a, b in ((0, 65), (1000, 1100)):
+        assert torch.equal(cr.fp8_linear(x[a:b], W, out_dtype=out), y[a:b])
