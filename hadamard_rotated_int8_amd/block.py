@@ -43,6 +43,8 @@ _BLOCK = struct.Struct("=5Q6q3if" + 3 * _VECTOR + 2 * _NORM)
 _ROPE_TENSOR = "QQ7q"
 _ROPE = struct.Struct("=3Q4q8ifi" + 4 * _ROPE_TENSOR)
 
+_ROPE_PADDING = [(0,) * 9 * (MAX_ROPE_TENSORS - i) for i in range(MAX_ROPE_TENSORS + 1)]
+
 _ABSENT = (0, 0, 1, 0)
 _NO_NORM = (0, 0.0, *_ABSENT, *_ABSENT)
 
@@ -55,7 +57,7 @@ def _writable(b: bytes):
 def _launch(fn, name, dev, *args):
     """fn(*args, stream) on dev's current stream, with dev the current device."""
     i = dev.index
-    if torch.cuda.current_device() == i:
+    if torch._C._cuda_getDevice() == i:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(dev):
@@ -84,12 +86,20 @@ def _rows(x: torch.Tensor, what: str, dev=None, shape=None) -> int:
 
 def _row_stride(x: torch.Tensor) -> int:
     """The row stride of a checked matrix (one row has any, down to its length)."""
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+    stride, k = x.stride(0), x.shape[1]
+    return stride if stride >= k or x.shape[0] > 1 else k
 
 
 def _writable_rows(x: torch.Tensor, what: str) -> None:
     if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
         raise ValueError(f"the rows of {what} must not overlap")
+
+
+def _new_like(x: torch.Tensor, dtype: torch.dtype, dev) -> torch.Tensor:
+    """A contiguous tensor of x's shape (empty_like is the shorter call where it gives one)."""
+    if dtype == x.dtype and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype, device=dev)
 
 
 def _distinct(outs) -> None:
@@ -355,7 +365,7 @@ def _out_rows(out, x, out_dtype, pack, dev):
             raise ValueError("with pack, out must be an Fp8Activation of x's shape on x's device")
         return None, out
     if out is None:
-        return torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev), None
+        return _new_like(x, out_dtype or x.dtype, dev), None
     _rows(out, "out", dev, x.shape)
     _writable_rows(out, "out")
     if out_dtype is not None and out.dtype != out_dtype:
@@ -403,7 +413,7 @@ def block_update(x: torch.Tensor, branch: torch.Tensor, gate: torch.Tensor | Non
     if out_dtype is not None and out_dtype not in _DTYPE:
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
     if out_h is None:
-        out_h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out_h = _new_like(x, x.dtype, dev)
     else:
         if out_h.dtype != x.dtype:
             raise ValueError("out_h must have x's type")
@@ -514,15 +524,6 @@ def rope_plan(rot: int, theta: float = 10000.0, layout: str = "interleaved", axe
 _LAYOUT = {"interleaved": 0, "half": 1}
 
 
-def _heads(x: torch.Tensor, what: str):
-    """(batch, tokens, heads, d) and the first three strides of a 3-D or 4-D tensor."""
-    if x.dim() == 4:
-        return tuple(x.shape), x.stride()[:3]
-    if x.dim() == 3:
-        return (1, *x.shape), (0, *x.stride()[:2])
-    raise ValueError(f"{what} must be [tokens, heads, d] or [batch, tokens, heads, d]")
-
-
 def _no_overlap(x: torch.Tensor) -> bool:
     """Whether every element of x has a place of its own (sizes of one aside, strides that nest)."""
     reach = 1
@@ -546,17 +547,20 @@ def rope(x, plan: RopePlan, positions: torch.Tensor, out=None, out_dtype: torch.
     inverse   : turn back
     """
     many = isinstance(x, (list, tuple))
-    xs = list(x) if many else [x]
-    if not 1 <= len(xs) <= MAX_ROPE_TENSORS:
+    xs = x if many else (x,)
+    count = len(xs)
+    if not 1 <= count <= MAX_ROPE_TENSORS:
         raise ValueError(f"1 to {MAX_ROPE_TENSORS} tensors")
-    dev = _device(xs[0], "x")
-    xdt = _DTYPE.get(xs[0].dtype)
+    first = xs[0]
+    dev = _device(first, "x")
+    dtype = first.dtype
+    xdt = _DTYPE.get(dtype)
     if out is None:
-        odt = xs[0].dtype if out_dtype is None else out_dtype
-        outs = [torch.empty(t.shape, dtype=odt, device=dev) for t in xs]
+        odt = dtype if out_dtype is None else out_dtype
+        outs = [_new_like(t, odt, dev) for t in xs]
     else:
         outs = list(out) if many else [out]
-        if len(outs) != len(xs):
+        if len(outs) != count:
             raise ValueError("one output per tensor")
         _distinct(outs)
         odt = outs[0].dtype
@@ -575,22 +579,30 @@ def rope(x, plan: RopePlan, positions: torch.Tensor, out=None, out_dtype: torch.
     if axis is not None and (axis.dtype != torch.int32 or axis.shape != inv.shape or
                              not axis.is_contiguous() or axis.device != dev):
         raise ValueError("axis must be a contiguous int32 [rot / 2] tensor on x's device")
-    (batch, tokens, _, d), _ = _heads(xs[0], "x")
+    dim = first.dim()
+    if dim not in (3, 4):
+        raise ValueError("x must be [tokens, heads, d] or [batch, tokens, heads, d]")
+    batch = first.shape[0] if dim == 4 else 1
+    tokens, _, d = first.shape[-3:]
     args = []
     for t, o in zip(xs, outs):
-        (b, n, h, dd), st = _heads(t, "x")
-        if t.dim() != xs[0].dim() or (b, n, dd) != (batch, tokens, d) or t.dtype != xs[0].dtype \
-                or t.device != dev or (t.stride(-1) != 1 and dd != 1):
+        shape, st = t.shape, t.stride()
+        if len(shape) != dim or shape[-3] != tokens or shape[-1] != d or shape[0] != first.shape[0] or \
+                t.dtype != dtype or t.device != dev or (st[-1] != 1 and d != 1):
             raise ValueError("the tensors must share type, device, batch, tokens and d, with unit "
                              "stride along d")
+        to = o.stride()
         if out is not None:
-            if o.shape != t.shape or o.dtype != odt or o.device != dev or o.stride(-1) != 1:
+            if o.shape != shape or o.dtype != odt or o.device != dev or to[-1] != 1:
                 raise ValueError("an output must have its tensor's shape, with unit stride along d")
             if not _no_overlap(o):
                 raise ValueError("an output's elements must not overlap")
-            if o.data_ptr() == t.data_ptr() and (o.stride() != t.stride() or xdt != ydt):
+            if o.data_ptr() == t.data_ptr() and (to != st or xdt != ydt):
                 raise ValueError("in place, out must be x itself")
-        args += (t.data_ptr(), o.data_ptr(), *st, *_heads(o, "out")[1], h)
+        if dim == 4:
+            args += (t.data_ptr(), o.data_ptr(), *st[:3], *to[:3], shape[2])
+        else:
+            args += (t.data_ptr(), o.data_ptr(), 0, st[0], st[1], 0, to[0], to[1], shape[1])
     pdt = _POSITION.get(positions.dtype)
     lead = positions.dim() - (axis is not None)
     if pdt is None or positions.device != dev or lead not in (1, 2) or \
@@ -600,10 +612,9 @@ def rope(x, plan: RopePlan, positions: torch.Tensor, out=None, out_dtype: torch.
     if axis is not None and positions.stride(-1) != 1 and positions.shape[-1] != 1:
         raise ValueError("the axes of a token's position must be consecutive")
     ps = positions.stride()
-    pad = MAX_ROPE_TENSORS - len(xs)
     _launch(lib().convrot_rope_apply, "convrot_rope_apply", dev,
             _ROPE.pack(inv.data_ptr(), 0 if axis is None else axis.data_ptr(), positions.data_ptr(),
                        ps[0] if lead == 2 else 0, ps[lead - 1], batch, tokens, pdt, d, rot,
-                       plan.start, layout, 1 if inverse else 0, xdt, ydt, plan.factor, len(xs),
-                       *args, *([0] * (9 * pad))))
+                       plan.start, layout, 1 if inverse else 0, xdt, ydt, plan.factor, count,
+                       *args, *_ROPE_PADDING[count]))
     return outs if many else outs[0]
