@@ -256,7 +256,7 @@ hipError_t launch_modes(const Fp8GemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
-  if (a.m <= kFp8FewRows) return launch_fp8_gemm_rows(a, stream);
+  if (fp8_rows_wanted(a)) return launch_fp8_gemm_rows(a, stream);
   if (fp8_wide_wanted(a)) return launch_fp8_gemm_wide(a, stream);
   // Smaller tiles while the CUs would hold at most two workgroups each of
   // them, for more of them share the loads' latency and the barriers; larger

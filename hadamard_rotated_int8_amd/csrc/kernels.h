@@ -97,8 +97,8 @@ struct Fp8GemmArgs {
   bool f32_scale, y_bf16, gelu;
 };
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream);
-// Up to kFp8FewRows rows (fp8_gemm_rows.hip).
-constexpr int kFp8FewRows = 64;
+// Few rows (fp8_gemm_rows.hip).
+bool fp8_rows_wanted(const Fp8GemmArgs& a);
 constexpr int kFp8RawBytes = 49152;  // codes of an unpacked X (at most 16 rows of whole blocks)
 hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs& a, hipStream_t stream);
 // Outputs with many tiles of 256 x 256 (fp8_gemm_wide.hip).

@@ -153,7 +153,8 @@ def _integers(m, n, k, f32, seed, sign_only=False):
 
 SHAPES = [(1, 1, 16), (2, 33, 5136), (17, 100, 656), (31, 64, 4112), (32, 31, 128), (40, 257, 1040), (64, 300, 2064), (65, 64, 640), (1, 128, 128), (2, 130, 144), (7, 64, 400), (15, 300, 1040), (16, 640, 2048),
           (17, 96, 128), (33, 257, 272), (64, 128, 640), (100, 1000, 1296), (129, 129, 384),
-          (256, 512, 512), (300, 770, 912), (513, 260, 528), (1, 4096, 5120), (5, 1500, 13824)]
+          (256, 512, 512), (300, 770, 912), (513, 260, 528), (1, 4096, 5120), (5, 1500, 13824),
+          (17, 8500, 144), (40, 4200, 272), (64, 4096, 400)]
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
@@ -247,13 +248,13 @@ def _on_gpu(d, w):
 
 
 WIDE = [(4096, 4096, 384), (4099, 4200, 400), (8200, 2050, 1040), (300, 33000, 656), (33000, 250, 528),
-        (4096, 4096, 2064)]
+        (4096, 4096, 2064), (2500, 4000, 400), (1700, 3900, 656)]
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
 @pytest.mark.parametrize("m,n,k", WIDE)
 def test_large_outputs_small_integers(m, n, k, f32):
-    """Outputs with tiles for every CU, whole and ragged."""
+    """Outputs with large tiles for every CU or most of them, whole and ragged."""
     print(f"[gpu] fp8 linear large integers {m}x{n}x{k} f32scale={f32}", flush=True)
     x, w = _integers(m, n, k, f32, m + n + k)
     want = _on_gpu(ref.dequantised_rows(x.q, x.scale), ref.dequantised_weights(w.q, w.scale))
