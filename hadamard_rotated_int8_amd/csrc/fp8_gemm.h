@@ -16,6 +16,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = 128;  // features (bytes) per step: one scale block
 constexpr int kGroupM = 4;
+constexpr int kMaxBlocks = 1042;  // CONVROT_MAX_K / 128, rounded up to pairs
 
 struct Fp8Params {
   const uint8_t* qx;

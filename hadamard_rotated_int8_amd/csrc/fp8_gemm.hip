@@ -38,18 +38,20 @@ CR_DEVICE f32x16 mfma_bf16(const Bf16Frag& a, const Bf16Frag& b, f32x16 c) {
   return c;
 }
 
-// One workgroup of WM x WN waves per output tile; a wave owns FM x FN blocks
-// of 32 x 32.  Operands reach LDS by direct-to-LDS loads of whole 128-byte
-// lines (16-byte chunk c of stage row r at slot c ^ swz(r), so 16 lanes that
-// read 16 consecutive rows touch 16 different groups of 4 banks), in STAGES
-// stages, STAGES - 1 of them ahead of the products.  Rows past M or n and bytes past K read as zero (range check of the
-// buffer resource).  The activation's scale bytes of a step's block lie side
-// by side and come along as one load (every wave makes its own copy, so that
-// all have the same number of loads to wait for); the weights' scales of the whole tile
-// are laid out in LDS as 32-bit values first.
+// One workgroup per output tile.  KG groups of WM x WN waves share the blocks
+// of features in turn, each with a ring of stages of its own, and their sums
+// meet in LDS at the end, in the groups' order; a wave owns FM x FN blocks of
+// 32 x 32.  Operands reach LDS by direct-to-LDS loads of whole 128-byte lines
+// (16-byte chunk c of stage row r at slot c ^ swz(r), so 16 lanes that read 16
+// consecutive rows touch 16 different groups of 4 banks), STAGES - 1 stages
+// ahead of the products.  Rows past M or n and bytes past K read as zero
+// (range check of the buffer resource).  The activation's scale bytes of a
+// step's block lie side by side and come along as one load (every wave makes
+// its own copy, so that all have the same number of loads to wait for); the
+// weights' scales of the whole tile are laid out in LDS as 32-bit values first.
 // EXACT: bfloat16 instructions (float32 outputs).
-template <int FM, int FN, int WM, int WN, int STAGES, bool F32SCALE, bool EXACT>
-__global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p) {
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT>
+__global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Params p) {
   constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN, WAVES = WM * WN;
   constexpr int XB = BM * kBK, WB = BN * kBK;
   constexpr int STAGE = XB + WB + WAVES * 256;  // + the rows' scales, a copy for each wave
@@ -57,12 +59,17 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
   constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;  // weight scale rows of a tile
   constexpr int LOADS = PIECES / WAVES + 1;  // of a wave and stage
   static_assert(STAGES >= 2 && (STAGES - 2) * LOADS <= kVmMax, "vmcnt range");
+  static_assert(KG == 1 || (KG - 1) * BM * BN * 4 <= KG * STAGES * STAGE, "the groups' sums fit");
+  static_assert(KG * STAGES * STAGE + BN * 4 + NBW * kMaxBlocks * 4 <= 160 * 1024, "LDS");
   static_assert(BM <= 256 && PIECES % WAVES == 0, "one load of scales, the others split evenly");
   static_assert(kFp8Block % (32 * FN) == 0 || (32 * FN) % kFp8Block == 0, "blocks in one scale row");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  unsigned* wscale = reinterpret_cast<unsigned*>(smem + STAGES * STAGE);  // [NBW][kb]
+  float* bias = reinterpret_cast<float*>(smem + KG * STAGES * STAGE);  // [BN]
+  unsigned* wscale = reinterpret_cast<unsigned*>(bias + BN);              // [NBW][kb]
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wid / WAVES, wave = wid % WAVES;
+  uint8_t* ring = smem + group * STAGES * STAGE;
   const int wm = wave / WN, wn = wave % WN;
   const int K = p.K, kb = p.kb;
   const Fp8Tile tile = fp8_tile<BM, BN>(p, xcd_slot(blockIdx.x, gridDim.x));
@@ -73,22 +80,11 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
   const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(p.qx + (int64_t)m0 * K, rows * K);
   const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(sg.qw + (int64_t)n0 * K, cols * K);
 
-  {  // the tile's weight scales (rows past n: a scale of one)
-    const int first_row = n0 / kFp8Block, nrows = (sg.n + kFp8Block - 1) / kFp8Block;
-    for (int i = threadIdx.x; i < NBW * kb; i += WAVES * 64) {
-      const int r = first_row + i / kb;
-      const int64_t at = (int64_t)r * kb + i % kb;
-      unsigned v = F32SCALE ? __float_as_uint(1.f) : 127u;
-      if (r < nrows)
-        v = F32SCALE ? static_cast<const unsigned*>(sg.sw)[at] : static_cast<const uint8_t*>(sg.sw)[at];
-      wscale[i] = v;
-    }
-  }
-
   // Past the last block everything is out of range: the loads keep their
   // number, for the waits.
-  auto issue = [&](int step, int slot) {
-    uint8_t* st = smem + slot * STAGE;
+  auto issue = [&](int turn, int slot) {
+    uint8_t* st = ring + slot * STAGE;
+    const int step = turn * KG + group;
     const int k0 = step * kBK;
 #pragma unroll
     for (int i = 0; i < PIECES / WAVES; ++i) {
@@ -106,6 +102,22 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
         (lds_void*)(st + XB + WB + wave * 256), 4, lane * 4, 0, 0, 0);
   };
 
+  // (before the first wait: the loads' way is long)
+#pragma unroll
+  for (int t = 0; t < STAGES - 1; ++t) issue(t, t);
+  {  // the tile's weight scales (rows past n: a scale of one) and bias
+    const int first_row = n0 / kFp8Block, nrows = (sg.n + kFp8Block - 1) / kFp8Block;
+    for (int i = threadIdx.x; i < NBW * kb; i += KG * WAVES * 64) {
+      const int r = first_row + i / kb;
+      const int64_t at = (int64_t)r * kb + i % kb;
+      unsigned v = F32SCALE ? __float_as_uint(1.f) : 127u;
+      if (r < nrows)
+        v = F32SCALE ? static_cast<const unsigned*>(sg.sw)[at] : static_cast<const uint8_t*>(sg.sw)[at];
+      wscale[i] = v;
+    }
+    for (int i = threadIdx.x; i < BN; i += KG * WAVES * 64) bias[i] = sg.bias && i < cols ? sg.bias[n0 + i] : 0.f;
+  }
+
   const int fr = lane & 31, fh = lane >> 5;
   f32x16 acc[FM][FN] = {};
   auto frag = [&](const uint8_t* base, int row, int t2) -> v8i {
@@ -113,16 +125,15 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
     const v4i b = *reinterpret_cast<const v4i*>(base + row * kBK + (((4 * t2 + 2 + fh) ^ swz(row)) << 4));
     return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   };
-#pragma unroll
-  for (int t = 0; t < STAGES - 1; ++t) issue(t, t);
-  for (int step = 0, slot = 0; step < kb; ++step) {
+  for (int turn = 0, slot = 0; turn * KG < kb; ++turn) {
+    const int step = turn * KG + group;
     // This step's stage has landed once only those behind it may be in
     // flight; every wave has read the one before it, which is refilled.
     waitvm<(STAGES - 2) * LOADS>();
     wait_lgkm0();
     barrier();
-    issue(step + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
-    const uint8_t* st = smem + slot * STAGE;
+    issue(turn + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+    const uint8_t* st = ring + slot * STAGE;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
     int sx[FM];
 #pragma unroll
@@ -131,7 +142,8 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
     unsigned sw[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      sw[j] = wscale[(wn * FN * 32 + j * 32) / kFp8Block * kb + step];
+      sw[j] = KG == 1 || step < kb ? wscale[(wn * FN * 32 + j * 32) / kFp8Block * kb + step]
+                                   : F32SCALE ? 0 : 127;
     if constexpr (EXACT) {
       // Power-of-two scales ride on the conversion; a float32 weight scale is
       // applied to the block's sum.
@@ -208,6 +220,36 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
     }
   }
   waitvm<0>();  // no load into LDS may be in flight at the end
+  if constexpr (KG > 1) {  // the groups' sums, in their order
+    wait_lgkm0();
+    barrier();
+    f32x4* sums = reinterpret_cast<f32x4*>(smem);
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            sums[(((group - 1) * WAVES + wave) * FM * FN * 4 + (i * FN + j) * 4 + q) * 64 + lane] =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    }
+    wait_lgkm0();
+    barrier();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < KG; ++g)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 v = sums[(((g - 1) * WAVES + wave) * FM * FN * 4 + (i * FN + j) * 4 + q) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+          }
+  }
   // Register e of block (i, j): column 8 (e / 4) + 4 (lane / 32) + e % 4, row lane % 32.
   const int64_t ldy = sg.ldy;
   const bool vec = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(sg.y) & (p.y_bf16 ? 7 : 15)) == 0;
@@ -222,8 +264,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[e] = acc[i][j][4 * q + e];
-          if (sg.bias && n + e < sg.n) v[e] += sg.bias[n + e];
+          v[e] = acc[i][j][4 * q + e] + bias[n - n0 + e];
           if (p.gelu) v[e] = gelu_erf(v[e]);
         }
         if (m < p.M && n < sg.n)
@@ -232,51 +273,69 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_gemm_kernel(const Fp8Params p
   }
 }
 
-template <int FM, int FN, int WM, int WN, int STAGES, bool F32SCALE, bool EXACT>
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT>
 hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
   constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
   constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;
   const Fp8Params p = fp8_params<BM, BN>(a);
-  const size_t lds = STAGES * ((BM + BN) * kBK + WM * WN * 256) + size_t(NBW) * p.kb * 4;
+  const size_t lds = KG * STAGES * ((BM + BN) * kBK + WM * WN * 256) + BN * 4 + size_t(NBW) * p.kb * 4;
   const dim3 grid(unsigned(p.tiles_m) * unsigned(p.tiles_n));
-  hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, STAGES, F32SCALE, EXACT>), grid, dim3(WM * WN * 64), lds,
+  hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT>), grid, dim3(WM * WN * KG * 64), lds,
                      stream, p);
   return hipGetLastError();
 }
 
-template <int FM, int FN, int WM, int WN, int STAGES>
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool EXACT>
+hipError_t launch_type(const Fp8GemmArgs& a, hipStream_t stream) {
+  return a.f32_scale ? launch_t<FM, FN, WM, WN, KG, STAGES, true, EXACT>(a, stream)
+                     : launch_t<FM, FN, WM, WN, KG, STAGES, false, EXACT>(a, stream);
+}
+
+template <int FM, int FN, int WM, int WN, int KG, int STAGES>
 hipError_t launch_modes(const Fp8GemmArgs& a, hipStream_t stream) {
-  if (!a.y_bf16)
-    return a.f32_scale ? launch_t<FM, FN, WM, WN, STAGES, true, true>(a, stream)
-                       : launch_t<FM, FN, WM, WN, STAGES, false, true>(a, stream);
-  return a.f32_scale ? launch_t<FM, FN, WM, WN, STAGES, true, false>(a, stream)
-                     : launch_t<FM, FN, WM, WN, STAGES, false, false>(a, stream);
+  return a.y_bf16 ? launch_type<FM, FN, WM, WN, KG, STAGES, false>(a, stream)
+                  : launch_type<FM, FN, WM, WN, KG, STAGES, true>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
-  if (fp8_rows_wanted(a)) return launch_fp8_gemm_rows(a, stream);
   if (fp8_wide_wanted(a)) return launch_fp8_gemm_wide(a, stream);
-  // Smaller tiles while the CUs would hold at most two workgroups each of
-  // them, for more of them share the loads' latency and the barriers; larger
-  // ones read the operands less often.  Measured with 64 x 64, 64 x 128 and
-  // 128 x 128 tiles (us, bfloat16 unless said): 300 x 4096 -> 4096 17.4, 21.9,
-  // 25.9; 512 x 4096 -> 4096 17.7, 22.9, 25.8; 333 x 4112 -> 4096 float32
-  // 26.9, 26.6, 39.2; 768 x 4096 -> 4096 23.8, 23.7, 27.3; 256 x 5120 ->
-  // 13824 38.8, 31.0, 36.2; 1300 x 4096 -> 4096 41.3, 34.5, 32.2; 3000 x 4096
-  // -> 4096 float32 124, 102, 93.  A stage more costs as much as it gains
-  // (26.9 against 28.0 us for 333 x 4112 -> 4096): two workgroups on a CU
-  // already cover each other's waits.
+  // What bounds few tiles is the latency of a step's loads, barrier and
+  // fragments, some 0.3 us however little they bring, and that a CU has only
+  // so many loads under way: so tiles as small as the CUs still take one of
+  // each, with the blocks of features shared among groups of waves.  Beyond
+  // one tile for each CU, the operands' way through L2 counts: larger tiles,
+  // two workgroups to a CU (which cover each other's waits), no groups.
+  // Measured (us, in a graph; bfloat16 outputs, then float32) with tiles of
+  //   32 x 32 in 4 (float32: 8) groups, 32 x 64 in 4, 64 x 64 in 2, 64 x 64:
+  //   33 x 4096 -> 4096     7.3  8.3 10.1 11.7;   8.1 10.3 15.0 17.3
+  //   16 x 13824 -> 5120   15.0 18.2 25.0 31.6;  19.0 24.8 41.4 49.7
+  //   64 x 13824 -> 5120   27.3 19.7 25.2 30.7;  34.0 25.8 41.6 48.7
+  //   64 x 5120 -> 13824   28.9 20.6 15.5 16.0;  32.3 25.0 20.1 22.2
+  //   512 x 4096 -> 4096      -    - 20.5 18.7;     -    - 31.8 27.5
+  // (8 groups of 32 x 32 with bfloat16 outputs: 7.6, 18.8 in the first two
+  // lines, 4 with float32: 9.0, 20.6) and (eager) with tiles of
+  //   64 x 64, 64 x 128, 128 x 128:
+  //   300 x 4096 -> 4096 17.4 21.9 25.9; 333 x 4112 -> 4096 float32 26.9 26.6
+  //   39.2; 768 x 4096 -> 4096 23.8 23.7 27.3; 256 x 5120 -> 13824 38.8 31.0
+  //   36.2; 1300 x 4096 -> 4096 41.3 34.5 32.2; 3000 x 4096 -> 4096 float32
+  //   124 102 93.
   auto tiles = [&](int64_t bm, int64_t bn) {
     int64_t t = 0;
     for (int i = 0; i < a.count; ++i) t += (a.w[i].n + bn - 1) / bn;
     return t * ((a.m + bm - 1) / bm);
   };
-  const int64_t two = 2 * int64_t(device_cu_count());
-  if (tiles(64, 64) <= two) return launch_modes<1, 1, 2, 2, 3>(a, stream);
-  if (tiles(64, 128) <= two) return launch_modes<1, 2, 2, 2, 2>(a, stream);
-  return launch_modes<2, 2, 2, 2, 2>(a, stream);
+  const int64_t cus = device_cu_count();
+  if (tiles(32, 32) <= cus) {
+    if (a.y_bf16) return launch_type<1, 1, 1, 1, 4, 3, false>(a, stream);
+    return launch_type<1, 1, 1, 1, 8, 2, true>(a, stream);
+  }
+  if (tiles(32, 64) <= cus) return launch_modes<1, 1, 1, 2, 4, 3>(a, stream);
+  if (tiles(64, 64) <= cus) return launch_modes<1, 1, 2, 2, 2, 3>(a, stream);
+  if (tiles(64, 64) <= 2 * cus) return launch_modes<1, 1, 2, 2, 1, 3>(a, stream);
+  if (tiles(64, 128) <= 2 * cus) return launch_modes<1, 2, 2, 2, 1, 2>(a, stream);
+  return launch_modes<2, 2, 2, 2, 1, 2>(a, stream);
 }
 
 }  // namespace convrot

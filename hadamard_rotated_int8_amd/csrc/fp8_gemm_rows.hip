@@ -1,5 +1,6 @@
-// FP8 linear for few rows of X (one token, a small batch): the weights are
-// read once, straight into registers, and that is what takes the time.
+// FP8 linear for a few rows of X as they are (one token, a small batch), in one
+// launch: the weights are read once, straight into registers, and that is what
+// takes the time.
 //
 // A workgroup owns 32 rows of W (16 where that leaves CUs without one); its 8
 // waves share the blocks of 128 features round robin (so that they read
@@ -7,12 +8,12 @@
 // requests kAhead blocks of W at once, two 16-byte loads per lane and 16 rows,
 // each instruction 16 rows x 64 bytes.
 //
+// Every workgroup quantises X into LDS while its first W loads are on their
+// way, which is less than a second launch costs.  (Each wave quantising its
+// own blocks in registers took 6 us more for one row of 5120 through 13824.)
 // One instruction of 16 x 16 x 128 (or, for float32 outputs, four of bfloat16
-// on converted codes, see fp8_gemm.hip) multiplies 16 rows of W with 16 rows
-// of X.  X comes packed, or as it is: then every workgroup quantises it into
-// LDS while its first W loads are on their way, which is less than a second
-// launch costs.  (Each wave quantising its own blocks in registers took 6 us
-// more for one row of 5120 through 13824.)
+// on converted codes, see fp8_gemm.hip) multiplies 16 rows of W with up to 16
+// rows of X.
 //
 // One row, 5120 -> 13824 (71 MB): 15.3 us, 4.6 TB/s.  With 1, 2 and 4 blocks
 // requested at once instead of 3 it took about the same or spilled; 16 rows
@@ -48,14 +49,14 @@ CR_DEVICE void load16(float* v, const void* x, bool bf16, int64_t at) {
   }
 }
 
-// MT: 16-row groups of X; NT: of W; RAW: X itself, quantised here.
-template <int MT, int NT, bool RAW, bool F32SCALE, bool EXACT>
-__global__ __launch_bounds__(kWaves * 64, MT == 1 ? 4 : 2) void fp8_rows_kernel(const Fp8Params p, const void* x,
-                                                                                int64_t ldx, bool x_bf16) {
+// NT: 16-row groups of W.
+template <int NT, bool F32SCALE, bool EXACT>
+__global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Params p, const void* x, int64_t ldx,
+                                                                  bool x_bf16) {
   constexpr int kRows = 16 * NT;
-  __shared__ float part[kWaves][NT * MT][64][4];
-  __shared__ __attribute__((aligned(16))) uint8_t xlds[RAW ? kFp8RawBytes : 16];  // codes [M][128 kb]
-  __shared__ uint8_t slds[RAW ? kFp8RawBytes / kBK : 16];                         // scales [M][kb]
+  __shared__ float part[kWaves][NT][64][4];
+  __shared__ __attribute__((aligned(16))) uint8_t xlds[kFp8RawBytes];  // codes [M][128 kb]
+  __shared__ uint8_t slds[kFp8RawBytes / kBK];                         // scales [M][kb]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
@@ -70,7 +71,7 @@ __global__ __launch_bounds__(kWaves * 64, MT == 1 ? 4 : 2) void fp8_rows_kernel(
 
   // Lane l: row l % 16 of 16, features 16 g .. +15 and 64 + 16 g .. +15 of a
   // block, g = l / 16 (both operands alike).
-  f32x4 acc[NT][MT] = {};
+  f32x4 acc[NT] = {};
   v4i w[kAhead][NT][2];
   auto load_w = [&](int b0) {
 #pragma unroll
@@ -86,66 +87,50 @@ __global__ __launch_bounds__(kWaves * 64, MT == 1 ? 4 : 2) void fp8_rows_kernel(
         }
   };
   load_w(wave);
-  if constexpr (RAW) {  // 8 threads to a block, 16 features each
-    for (int i = threadIdx.x >> 3; i < p.M * kb; i += kWaves * 8) {
-      const int row = i / kb, b = i - row * kb, f = b * kBK + 16 * int(threadIdx.x & 7);
-      float v[16];
-      if (f < K) {
-        load16(v, x, x_bf16, row * ldx + f);
-      } else {
+  // X: 8 threads to a block, 16 features each.
+  for (int i = threadIdx.x >> 3; i < p.M * kb; i += kWaves * 8) {
+    const int row = i / kb, b = i - row * kb, f = b * kBK + 16 * int(threadIdx.x & 7);
+    float v[16];
+    if (f < K) {
+      load16(v, x, x_bf16, row * ldx + f);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-      }
-      unsigned top = 0;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = max(top, abs_bits(v[e]));
-      top = max(top, dpp_u32<kDppQuadSwap1>(top));
-      top = max(top, dpp_u32<kDppQuadSwap2>(top));
-      top = max(top, dpp_u32<kDppHalfMirror>(top));
-      const unsigned sc = fp8_scale_of(top);
-      const float inv = fp8_inverse_scale(sc);
-      u32x4 q;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        q[e] = sc == kFp8ScaleNan ? kFp8CodeNan
-                                  : fp8_codes4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv,
-                                               v[4 * e + 3] * inv);
-      *reinterpret_cast<u32x4*>(xlds + (row * kb + b) * kBK + 16 * (threadIdx.x & 7)) = q;
-      if ((threadIdx.x & 7) == 0) slds[row * kb + b] = uint8_t(sc);
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
     }
-    wait_lgkm0();  // (not __syncthreads, which may wait for W)
-    barrier();
+    unsigned top = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = max(top, abs_bits(v[e]));
+    top = max(top, dpp_u32<kDppQuadSwap1>(top));
+    top = max(top, dpp_u32<kDppQuadSwap2>(top));
+    top = max(top, dpp_u32<kDppHalfMirror>(top));
+    const unsigned sc = fp8_scale_of(top);
+    const float inv = fp8_inverse_scale(sc);
+    u32x4 q;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      q[e] = sc == kFp8ScaleNan ? kFp8CodeNan
+                                : fp8_codes4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv,
+                                             v[4 * e + 3] * inv);
+    *reinterpret_cast<u32x4*>(xlds + (row * kb + b) * kBK + 16 * (threadIdx.x & 7)) = q;
+    if ((threadIdx.x & 7) == 0) slds[row * kb + b] = uint8_t(sc);
   }
+  wait_lgkm0();  // (not __syncthreads, which may wait for W)
+  barrier();
   for (int b0 = wave; b0 < kb; b0 += kWaves * kAhead) {
     if (b0 != wave) load_w(b0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int b = b0 + kWaves * u;
       if (b >= kb) break;
-      v8i xq[MT];
-      unsigned sx[MT];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int row = 16 * t + fr;
-        v4i q[2] = {};
-        sx[t] = 127u;
-        if constexpr (RAW) {
-          if (row < p.M) {
-            const uint8_t* src = xlds + (row * kb + b) * kBK + 16 * fg;
-            q[0] = *reinterpret_cast<const v4i*>(src);
-            q[1] = *reinterpret_cast<const v4i*>(src + 64);
-            sx[t] = slds[row * kb + b];
-          }
-        } else if (row < p.M) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int f = b * kBK + 64 * c + 16 * fg;
-            if (f < K) q[c] = *reinterpret_cast<const v4i*>(p.qx + (int64_t)row * K + f);
-          }
-          sx[t] = p.sx[b * p.lds + row];
-        }
-        xq[t] = v8i{q[0][0], q[0][1], q[0][2], q[0][3], q[1][0], q[1][1], q[1][2], q[1][3]};
+      v4i x0 = {}, x1 = {};
+      int sx = 127;
+      if (fr < p.M) {
+        const uint8_t* src = xlds + (fr * kb + b) * kBK + 16 * fg;
+        x0 = *reinterpret_cast<const v4i*>(src);
+        x1 = *reinterpret_cast<const v4i*>(src + 64);
+        sx = slds[fr * kb + b];
       }
+      const v8i xq = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
       const int64_t at = (int64_t)(n0 / kFp8Block) * kb + b;
       float sf = 1.f;
       int se = 127;
@@ -159,47 +144,34 @@ __global__ __launch_bounds__(kWaves * 64, MT == 1 ? 4 : 2) void fp8_rows_kernel(
         const v8i wq = {q[0][0], q[0][1], q[0][2], q[0][3], q[1][0], q[1][1], q[1][2], q[1][3]};
         if constexpr (EXACT) {
           const Bf16Frag wf = to_bf16(wq, F32SCALE ? 1.f : e8m0_value(se));
+          const Bf16Frag xf = to_bf16(xq, e8m0_value(sx));
+          f32x4 c = F32SCALE ? f32x4{} : acc[j];
 #pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            const Bf16Frag xf = to_bf16(xq[t], e8m0_value(sx[t]));
-            f32x4 c = F32SCALE ? f32x4{} : acc[j][t];
+          for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf.v[i], xf.v[i], c, 0, 0, 0);
+          if constexpr (F32SCALE) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf.v[i], xf.v[i], c, 0, 0, 0);
-            if constexpr (F32SCALE) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(c[e], sf, acc[j][t][e]);
-            }
-            acc[j][t] = c;
+            for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(c[e], sf, acc[j][e]);
           }
+          acc[j] = c;
+        } else if constexpr (F32SCALE) {
+          const f32x4 c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq, f32x4{}, 0, 0, 0, 127, 0, sx);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(c[e], sf, acc[j][e]);
         } else {
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            if constexpr (F32SCALE) {
-              const f32x4 c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq[t], f32x4{}, 0, 0, 0, 127,
-                                                                               0, int(sx[t]));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[j][t][e] = __builtin_fmaf(c[e], sf, acc[j][t][e]);
-            } else {
-              acc[j][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq[t], acc[j][t], 0, 0, 0, se, 0,
-                                                                           int(sx[t]));
-            }
-          }
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq, acc[j], 0, 0, 0, se, 0, sx);
         }
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4*>(part[wave][j * MT + t][lane]) = acc[j][t];
+  for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4*>(part[wave][j][lane]) = acc[j];
   __syncthreads();
-  // Element e of lane l in group (j, t): column 16 j + 4 (l / 16) + e, row 16 t + l % 16.
-  for (int g = wave; g < NT * MT; g += kWaves) {
-    f32x4 v = *reinterpret_cast<const f32x4*>(part[0][g][lane]);
+  // Element e of lane l in group j: column 16 j + 4 (l / 16) + e, row l % 16.
+  if (wave < NT) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(part[0][wave][lane]);
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) v += *reinterpret_cast<const f32x4*>(part[i][g][lane]);
-    const int n = n0 + 16 * (g / MT) + 4 * fg, row = 16 * (g % MT) + fr;
+    for (int i = 1; i < kWaves; ++i) v += *reinterpret_cast<const f32x4*>(part[i][wave][lane]);
+    const int n = n0 + 16 * wave + 4 * fg, row = fr;
     if (row < p.M && n < sg.n) {
       float o[4];
 #pragma unroll
@@ -214,12 +186,12 @@ __global__ __launch_bounds__(kWaves * 64, MT == 1 ? 4 : 2) void fp8_rows_kernel(
   }
 }
 
-template <int MT, int NT, bool RAW>
+template <int NT>
 void launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
   const Fp8Params p = fp8_params<16, 16 * NT>(a);
   const dim3 grid(unsigned(p.tiles_n));
   auto go = [&](auto f32, auto exact) {
-    hipLaunchKernelGGL((fp8_rows_kernel<MT, NT, RAW, decltype(f32)::value, decltype(exact)::value>), grid,
+    hipLaunchKernelGGL((fp8_rows_kernel<NT, decltype(f32)::value, decltype(exact)::value>), grid,
                        dim3(kWaves * 64), 0, stream, p, a.x, a.ldx, a.x_bf16);
   };
   using Yes = std::true_type;
@@ -231,45 +203,15 @@ void launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
   }
 }
 
-template <int NT>
-void launch_nt(const Fp8GemmArgs& a, hipStream_t stream) {
-  if (a.x)
-    launch_t<1, NT, true>(a, stream);
-  else if (a.m <= 16)
-    launch_t<1, NT, false>(a, stream);
-  else if (a.m <= 32)
-    launch_t<2, NT, false>(a, stream);
-  else
-    launch_t<4, NT, false>(a, stream);
-}
-
 }  // namespace
-
-// Up to 16 rows, or up to 64 while W's groups of 16 rows, times the groups of
-// 16 rows of X (1, 2 or 4), are at most four to a CU.  A row more costs this
-// kernel time, the tiles of fp8_gemm.hip none; those take 0.3 to 0.5 us a
-// block of features however little there is.  Measured, here and there (us,
-// bfloat16 outputs; calls of 11 us are bound by their submission): 5120 ->
-// 13824 with 16, 32 and 64 rows 17.9, 21.9, 33.1 and 16.1, 16.2, 16.9 (float32
-// outputs 18.5, 24.0, 37.7 and 23.2, 23.2, 24.0); 13824 -> 5120 28.4, 40.1,
-// 64.6 and 34.4, 34.6, 34.9 (float32 30.4, 41.7, 65.7 and 53.2, 53.5, 53.5);
-// 4096 -> 4096 11.3, 11.0, 12.9 and 13.5 (float32 11.1, 11.1, 14.1 and 18.9);
-// 5120 -> 640 11.3, 11.3, 14.4 and 15.8.
-bool fp8_rows_wanted(const Fp8GemmArgs& a) {
-  if (a.m <= 16) return true;
-  if (a.m > 64) return false;
-  int64_t groups = 0;
-  for (int i = 0; i < a.count; ++i) groups += (a.w[i].n + 15) / 16;
-  return groups * (a.m <= 32 ? 2 : 4) <= 4 * int64_t(device_cu_count());
-}
 
 hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs& a, hipStream_t stream) {
   int64_t groups = 0;
   for (int i = 0; i < a.count; ++i) groups += (a.w[i].n + 31) / 32;
   if (groups < device_cu_count())
-    launch_nt<1>(a, stream);
+    launch_t<1>(a, stream);
   else
-    launch_nt<2>(a, stream);
+    launch_t<2>(a, stream);
   return hipGetLastError();
 }
 

@@ -40,7 +40,6 @@ namespace convrot {
 namespace {
 
 constexpr int kBM = 256;
-constexpr int kMaxBlocks = 1042;               // CONVROT_MAX_K / 128, rounded up to pairs
 constexpr int kMinBlocks = 3;
 constexpr int64_t kMaxLdy = 1 << 21;           // a tile's rows of Y lie in 31 bits
 

@@ -88,7 +88,7 @@ struct Fp8Weight {
 struct Fp8GemmArgs {
   const uint8_t* qx;  // the packed activation ...
   const uint8_t* sx;
-  const void* x;      // ... or, where it is short, X itself (row stride ldx)
+  const void* x;      // ... or X itself, a few rows (row stride ldx)
   int64_t ldx;
   bool x_bf16;
   int64_t lds, m, k;
@@ -97,8 +97,7 @@ struct Fp8GemmArgs {
   bool f32_scale, y_bf16, gelu;
 };
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream);
-// Few rows (fp8_gemm_rows.hip).
-bool fp8_rows_wanted(const Fp8GemmArgs& a);
+// A few rows of X itself (fp8_gemm_rows.hip).
 constexpr int kFp8RawBytes = 49152;  // codes of an unpacked X (at most 16 rows of whole blocks)
 hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs& a, hipStream_t stream);
 // Outputs with many tiles of 256 x 256 (fp8_gemm_wide.hip).
