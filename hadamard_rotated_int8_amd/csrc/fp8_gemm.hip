@@ -305,22 +305,28 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   // fragments, some 0.3 us however little they bring, and that a CU has only
   // so many loads under way: so tiles as small as the CUs still take one of
   // each, with the blocks of features shared among groups of waves.  Beyond
-  // one tile for each CU, the operands' way through L2 counts: larger tiles,
-  // two workgroups to a CU (which cover each other's waits), no groups.
-  // Measured (us, in a graph; bfloat16 outputs, then float32) with tiles of
-  //   32 x 32 in 4 (float32: 8) groups, 32 x 64 in 4, 64 x 64 in 2, 64 x 64:
-  //   33 x 4096 -> 4096     7.3  8.3 10.1 11.7;   8.1 10.3 15.0 17.3
-  //   16 x 13824 -> 5120   15.0 18.2 25.0 31.6;  19.0 24.8 41.4 49.7
-  //   64 x 13824 -> 5120   27.3 19.7 25.2 30.7;  34.0 25.8 41.6 48.7
-  //   64 x 5120 -> 13824   28.9 20.6 15.5 16.0;  32.3 25.0 20.1 22.2
-  //   512 x 4096 -> 4096      -    - 20.5 18.7;     -    - 31.8 27.5
-  // (8 groups of 32 x 32 with bfloat16 outputs: 7.6, 18.8 in the first two
-  // lines, 4 with float32: 9.0, 20.6) and (eager) with tiles of
-  //   64 x 64, 64 x 128, 128 x 128:
-  //   300 x 4096 -> 4096 17.4 21.9 25.9; 333 x 4112 -> 4096 float32 26.9 26.6
-  //   39.2; 768 x 4096 -> 4096 23.8 23.7 27.3; 256 x 5120 -> 13824 38.8 31.0
-  //   36.2; 1300 x 4096 -> 4096 41.3 34.5 32.2; 3000 x 4096 -> 4096 float32
-  //   124 102 93.
+  // one tile of 128 x 128 for each CU, and for up to 64 rows beyond one of
+  // 64 x 64, two workgroups to a CU cover each other's waits instead.
+  // Measured (us, in a graph; bfloat16 outputs; float32 outputs), tiles of
+  //                        32x32  32x64  64x64  64x64 | 32x32  32x64  64x64  64x64
+  //   in groups             4, 8    4      2      1   |  4, 8    4      2      1
+  //   33 x  4096 ->  4096  7.3 7.6  8.3   10.1   11.7 | 9.0 8.1  10.3   15.0   17.3
+  //   16 x 13824 ->  5120 15.0 18.8 18.2  25.0   31.6 | 20.6 19  24.8   41.4   49.7
+  //   64 x 13824 ->  5120   27  33  19.7  25.2   30.7 |   38 34  25.8   41.6   48.7
+  //   64 x  5120 -> 13824   29  31  20.6  15.5   16.0 |   37 32  25.0   20.1   22.2
+  //   64 x  5120 -> 20480           29.8  26.9   25.0 |          35.8   35.7   30.7
+  // and
+  //                        64x64 64x128 128x128 128x64 128x128 |
+  //   in groups              1     1       1      2       2    |
+  //   300 x  4096 ->  4096 15.7  22.1    25.1   15.3    19.1
+  //   333 x  4112 ->  4096                                     | 28.6 27.4 38.7 23.8 32.1
+  //   512 x  4096 ->  4096 18.6  23.0    26.3   16.8    20.1   | 27.4 25.8 37.6 24.3 31.4
+  //   256 x  5120 -> 13824 38.2  30.4    35.1   36.8    27.9   | 55.2 46.1 48.3 52.9 42.8
+  //  1000 x  4096 ->  4096 31.8  27.2    29.1   31.6    24.8   | 51.2 41.1 43.2 46.1 37.9
+  //  2048 x  4096 ->  4096 58.2  53.4    41.2   61.2    47.4   | 85.8 73.7 65.6 88.3 74.1
+  //    64 x  4096 -> 100000 103   124     118    124     132   |  110  128  130  158  144
+  // (Eight groups need a stage less, which costs more than they gain where
+  // the products are quick, with bfloat16 outputs.)
   auto tiles = [&](int64_t bm, int64_t bn) {
     int64_t t = 0;
     for (int i = 0; i < a.count; ++i) t += (a.w[i].n + bn - 1) / bn;
@@ -333,8 +339,9 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   }
   if (tiles(32, 64) <= cus) return launch_modes<1, 1, 1, 2, 4, 3>(a, stream);
   if (tiles(64, 64) <= cus) return launch_modes<1, 1, 2, 2, 2, 3>(a, stream);
-  if (tiles(64, 64) <= 2 * cus) return launch_modes<1, 1, 2, 2, 1, 3>(a, stream);
-  if (tiles(64, 128) <= 2 * cus) return launch_modes<1, 2, 2, 2, 1, 2>(a, stream);
+  if (a.m <= 64) return launch_modes<1, 1, 2, 2, 1, 3>(a, stream);
+  if (tiles(128, 64) <= cus) return launch_modes<2, 1, 2, 2, 2, 3>(a, stream);
+  if (tiles(128, 128) <= cus) return launch_modes<1, 2, 4, 2, 2, 2>(a, stream);
   return launch_modes<2, 2, 2, 2, 1, 2>(a, stream);
 }
 

@@ -330,7 +330,7 @@ def test_unpacked_rows_equal_packed_rows(m, k, out):
 
 @pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("m,n", [(1, 100), (33, 4090), (70, 2500), (50, 6000), (130, 5000), (250, 5100),
+@pytest.mark.parametrize("m,n", [(1, 100), (33, 4090), (70, 2500), (50, 6000), (130, 5000), (60, 17000), (250, 5100),
                                  (1100, 2000), (2113, 2100)])
 def test_every_tile_size(m, n, out, f32):
     """Few rows take small output tiles and many take larger ones, with the blocks of features shared
