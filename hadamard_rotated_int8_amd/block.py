@@ -41,7 +41,7 @@ _VECTOR = "Qqqi4x"
 _NORM = "if" + _VECTOR + _VECTOR
 _BLOCK = struct.Struct("=5Q6q3if" + 3 * _VECTOR + 2 * _NORM)
 _ROPE_TENSOR = "QQ7q"
-_ROPE = struct.Struct("=3Q4q8ifi" + 4 * _ROPE_TENSOR)
+_ROPE = struct.Struct("=3Q4q8ifii4x" + 4 * _ROPE_TENSOR)
 
 _ROPE_PADDING = [(0,) * 9 * (MAX_ROPE_TENSORS - i) for i in range(MAX_ROPE_TENSORS + 1)]
 
@@ -442,6 +442,7 @@ class RopePlan:
                pair turns by (time, row, column, ...), or None with one position
     factor   : multiplies cos and sin (long-context scalings use it)
     start    : first feature of the rotated slice
+    axes     : how many positions a token has (0: not stated)
     """
 
     inv_freq: torch.Tensor
@@ -449,6 +450,7 @@ class RopePlan:
     axis: torch.Tensor | None = None
     factor: float = 1.0
     start: int = 0
+    axes: int = 0
 
 
 def rope_plan(rot: int, theta: float = 10000.0, layout: str = "interleaved", axes=None,
@@ -518,7 +520,7 @@ def rope_plan(rot: int, theta: float = 10000.0, layout: str = "interleaved", axe
         axis = torch.tensor([i for i, n in enumerate(parts) for _ in range(n // 2)],
                             dtype=torch.int32, device=device)
     return RopePlan(torch.tensor(freqs, dtype=torch.float64, device=device), layout, axis,
-                    float(factor), start)
+                    float(factor), start, len(parts))
 
 
 _LAYOUT = {"interleaved": 0, "half": 1}
@@ -609,12 +611,17 @@ def rope(x, plan: RopePlan, positions: torch.Tensor, out=None, out_dtype: torch.
             positions.shape[lead - 1] != tokens or (lead == 2 and positions.shape[0] != batch):
         raise ValueError("positions must be int32, int64 or float32 [tokens] or [batch, tokens] "
                          "(with the plan's axes behind) on x's device")
-    if axis is not None and positions.stride(-1) != 1 and positions.shape[-1] != 1:
-        raise ValueError("the axes of a token's position must be consecutive")
+    axes = 1
+    if axis is not None:
+        axes = positions.shape[-1]
+        if axes < max(plan.axes, 1):
+            raise ValueError("positions has fewer axes than the plan")
+        if positions.stride(-1) != 1 and axes != 1:
+            raise ValueError("the axes of a token's position must be consecutive")
     ps = positions.stride()
     _launch(lib().convrot_rope_apply, "convrot_rope_apply", dev,
             _ROPE.pack(inv.data_ptr(), 0 if axis is None else axis.data_ptr(), positions.data_ptr(),
                        ps[0] if lead == 2 else 0, ps[lead - 1], batch, tokens, pdt, d, rot,
-                       plan.start, layout, 1 if inverse else 0, xdt, ydt, plan.factor, count,
+                       plan.start, layout, 1 if inverse else 0, xdt, ydt, plan.factor, count, axes,
                        *args, *_ROPE_PADDING[count]))
     return outs if many else outs[0]

@@ -176,7 +176,8 @@ convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m
                                        void* const* y, const int64_t* ldy, int32_t y_dtype,
                                        int32_t act, void* stream) {
   static_assert(convrot::kFp8RawBytes == CONVROT_FP8_MAX_ROWS_BYTES, "header");
-  if (m > CONVROT_FP8_MAX_ROWS || (m > 0 && blocks(k) * 128 > CONVROT_FP8_MAX_ROWS_BYTES / m))
+  if (k < 1 || k > CONVROT_MAX_K || m > CONVROT_FP8_MAX_ROWS ||
+      (m > 0 && blocks(k) * 128 > CONVROT_FP8_MAX_ROWS_BYTES / m))
     return CONVROT_ERR_SHAPE;
   convrot::Fp8GemmArgs a{};
   a.x = x;
@@ -226,6 +227,11 @@ convrot_status convrot_block_norm(const convrot_block* b, void* stream) {
   if (b->m > 0) {
     if (!b->x || (!b->h && !wants_y)) return CONVROT_ERR_NULL;
     if (b->packed && (st = check_fp8_buffers(b->packed)) != CONVROT_OK) return st;
+    // In place: over x, row by row; nothing else is read and written.
+    if ((b->h && (b->h == b->y || b->h == b->branch || (b->h == b->x && b->ldh != b->ldx))) ||
+        (b->y && (b->y == b->branch ||
+                  (b->y == b->x && (b->ldy != b->ldx || b->y_dtype != b->x_dtype)))))
+      return CONVROT_ERR_UNSUPPORTED;
   }
   if (b->packed) {
     b->packed->m = b->m;
@@ -255,7 +261,7 @@ convrot_status convrot_block_norm(const convrot_block* b, void* stream) {
 convrot_status convrot_rope_apply(const convrot_rope* r, void* stream) {
   if (!r) return CONVROT_ERR_NULL;
   if (r->batch < 0 || r->tokens < 0 || r->batch > kMaxRows || r->tokens > kMaxRows ||
-      r->count < 1 || r->count > CONVROT_MAX_ROPE_TENSORS || r->d < 2 || r->d > 4096 ||
+      r->count < 1 || r->count > CONVROT_MAX_ROPE_TENSORS || r->axes < 1 || r->d < 2 || r->d > 4096 ||
       r->rot < 2 || r->rot % 2 != 0 || r->start < 0 || r->start > r->d - r->rot)
     return CONVROT_ERR_SHAPE;
   if (r->batch * r->tokens > kMaxRows) return CONVROT_ERR_SHAPE;
@@ -303,6 +309,7 @@ convrot_status convrot_rope_apply(const convrot_rope* r, void* stream) {
   a.axis = r->axis;
   a.batch = r->batch;
   a.tokens = r->tokens;
+  a.axes = r->axes;
   a.pos_batch = r->pos_stride[0];
   a.pos_token = r->pos_stride[1];
   a.d = r->d;

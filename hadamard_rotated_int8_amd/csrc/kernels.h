@@ -153,6 +153,7 @@ struct RopeArgs {
   const double* inv_freq;  // [rot / 2]
   const int32_t* axis;     // [rot / 2] or nullptr
   int64_t batch, tokens, pos_batch, pos_token;
+  int axes;
   int count;
   int d, rot, start;
   float factor;

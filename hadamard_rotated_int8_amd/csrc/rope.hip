@@ -96,12 +96,14 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a, const 
       place[tl][0] = b;
       place[tl][1] = tok;
     }
-    const int64_t at = b * a.pos_batch + tok * a.pos_token + (a.axis ? a.axis[j] : 0);
+    const int axis = a.axis ? a.axis[j] : 0;
+    const bool known = unsigned(axis) < unsigned(a.axes);
+    const int64_t at = b * a.pos_batch + tok * a.pos_token + (known ? axis : 0);
     const double pos = a.pos_type == kPosI32   ? double(static_cast<const int32_t*>(a.positions)[at])
                        : a.pos_type == kPosI64 ? double(static_cast<const int64_t*>(a.positions)[at])
                                                : double(static_cast<const float*>(a.positions)[at]);
     double turns = pos * (a.inv_freq[j] * 0.15915494309189533577);  // 1 / (2 pi)
-    turns -= rint(turns);
+    turns = known ? turns - rint(turns) : __builtin_nan("");
     float sn, c;
     sincospif(2.f * float(turns), &sn, &c);
     cs[i] = make_float2(c * a.factor, (a.inverse ? -sn : sn) * a.factor);

@@ -266,7 +266,9 @@ convrot_status convrot_linear_lora(const convrot_packed* x, const convrot_weight
  * [-126, 127] for which the block's largest magnitude is at most 448 2^e,
  * and 0 for a block of zeros.  A code is then the E4M3 value nearest to
  * x 2^-e, ties to even.  A block that holds an infinity or a NaN becomes NaN
- * throughout.  k need not be a multiple of 128 (the last block is shorter),
+ * throughout.  Every code times its scale is a finite float32 number (with
+ * others' scales beyond that, outputs may be infinite where a sum is not).
+ * k need not be a multiple of 128 (the last block is shorter),
  * but k % 16 == 0 and k <= CONVROT_MAX_K.
  * ---------------------------------------------------------------------------
  */
@@ -406,7 +408,8 @@ typedef struct convrot_norm {
  *   packed : y as an FP8 activation (see convrot_fp8_packed; k % 16 == 0)
  *            instead of y, or NULL; the call sets its m and k
  * At least one output is wanted.  h or y may be x itself (same pointer, type
- * and stride); no other output may overlap an input or another output.
+ * and stride), not both; no other output may overlap an input or another
+ * output.
  * Pointers need their element's alignment only.  1 <= k <= CONVROT_MAX_NORM_K.
  */
 typedef struct convrot_block {
@@ -465,7 +468,8 @@ typedef struct convrot_rope_tensor {
 /*
  *   inv_freq  : device float64 [rot / 2]
  *   axis      : device int32 [rot / 2], values in 0 .. axes - 1, or NULL (axis
- *               0).  The caller answers for the values.
+ *               0).  A pair with another value has no position: its results
+ *               are NaN.
  *   positions : device, of position_type: [batch, tokens, axes] with element
  *               strides pos_stride[0] (0: the same for every batch entry) and
  *               pos_stride[1]; the axes of a token are consecutive
@@ -485,6 +489,7 @@ typedef struct convrot_rope {
   int32_t x_dtype, y_dtype;
   float factor;
   int32_t count; /* 1 .. CONVROT_MAX_ROPE_TENSORS */
+  int32_t axes;  /* positions of a token, >= 1 */
   convrot_rope_tensor t[CONVROT_MAX_ROPE_TENSORS];
 } convrot_rope;
 

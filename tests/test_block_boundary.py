@@ -100,6 +100,7 @@ def _linear_rows(x=FAKE, dt=cr.BF16, m=4, k=256, ldx=256, n=64, wk=256, q=FAKE, 
 @cpu_only
 @pytest.mark.parametrize("want,args", [
     (NULL, dict(x=None)), (NULL, dict(q=0)), (NULL, dict(y=0)), (SHAPE, dict(m=17)), (SHAPE, dict(m=-1)),
+    (SHAPE, dict(k=-16)), (SHAPE, dict(k=2 ** 63 - 1)), (SHAPE, dict(k=cr.MAX_K + 16)),
     (SHAPE, dict(m=2, k=24592, wk=24592, ldx=24592)), (SHAPE, dict(ldx=255)), (SHAPE, dict(wk=128)), (SHAPE, dict(ldy=63)), (SHAPE, dict(count=0)),
     (DTYPE, dict(dt=cr.I32)), (DTYPE, dict(ydt=cr.I32)), (DTYPE, dict(act=3)),
     (UNSUPPORTED, dict(x=FAKE + 8)), (UNSUPPORTED, dict(ldx=260)), (UNSUPPORTED, dict(k=264, wk=264, ldx=264))])
@@ -158,6 +159,10 @@ PACKED = (FAKE, FAKE, 0, 0, 4)
     (UNSUPPORTED, dict(x=FAKE + 1)), (UNSUPPORTED, dict(y=FAKE + 2, ydt=cr.F32)),
     (UNSUPPORTED, dict(branch=FAKE + 2)), (UNSUPPORTED, dict(scale=_vec(FAKE + 2))),
     (UNSUPPORTED, dict(y=0, packed=PACKED, k=56)), (UNSUPPORTED, dict(y=0, packed=(FAKE + 8, FAKE, 0, 0, 4))),
+    (UNSUPPORTED, dict(ldy=128)), (UNSUPPORTED, dict(ydt=cr.F32)),   # over x, but not row by row
+    (UNSUPPORTED, dict(y=0, branch=FAKE + 64, h=FAKE, ldh=128, pre=_norm())),
+    (UNSUPPORTED, dict(branch=FAKE + 64, h=FAKE + 128, y=FAKE + 128)), (UNSUPPORTED, dict(branch=FAKE + 64, h=FAKE)),
+    (UNSUPPORTED, dict(branch=FAKE + 64, h=FAKE + 64)), (UNSUPPORTED, dict(branch=FAKE + 64, y=FAKE + 64)),
     (UNSUPPORTED, dict(y=0, packed=(FAKE, FAKE + 1, 0, 0, 4))), (UNSUPPORTED, dict(y=0, packed=(FAKE, FAKE, 0, 0, 5)))])
 def test_block_norm_refusals(want, args):
     assert _block(**args) == want
@@ -172,7 +177,7 @@ def test_block_norm_null_and_empty():
 # ------------------------------------------------------------ rotary positions
 
 def _rope(inv=FAKE, axis=0, pos=FAKE, ps=(0, 1), batch=1, tokens=4, pdt=0, d=64, rot=64, start=0,
-          layout=0, xdt=cr.BF16, ydt=cr.BF16, count=1, t=None):
+          layout=0, xdt=cr.BF16, ydt=cr.BF16, count=1, axes=1, t=None):
     t = t or [{}]
     tensors = []
     for one in t:
@@ -180,14 +185,14 @@ def _rope(inv=FAKE, axis=0, pos=FAKE, ps=(0, 1), batch=1, tokens=4, pdt=0, d=64,
         tensors += [o["x"], o["y"], *o["xs"], *o["ys"], o["heads"]]
     tensors += [0] * (36 - len(tensors))
     return cr.lib().convrot_rope_apply(block._ROPE.pack(
-        inv, axis, pos, *ps, batch, tokens, pdt, d, rot, start, layout, 0, xdt, ydt, 1.0, count, *tensors),
+        inv, axis, pos, *ps, batch, tokens, pdt, d, rot, start, layout, 0, xdt, ydt, 1.0, count, axes, *tensors),
         None)
 
 
 @cpu_only
 @pytest.mark.parametrize("want,args", [
     (NULL, dict(inv=0)), (NULL, dict(pos=0)), (NULL, dict(t=[dict(x=0)])), (NULL, dict(t=[dict(y=0)])),
-    (SHAPE, dict(count=0)), (SHAPE, dict(count=5)), (SHAPE, dict(batch=-1)), (SHAPE, dict(tokens=BIG)),
+    (SHAPE, dict(count=0)), (SHAPE, dict(count=5)), (SHAPE, dict(axes=0)), (SHAPE, dict(batch=-1)), (SHAPE, dict(tokens=BIG)),
     (SHAPE, dict(batch=1 << 16, tokens=1 << 16)), (SHAPE, dict(rot=63)), (SHAPE, dict(rot=0)),
     (SHAPE, dict(rot=66)), (SHAPE, dict(rot=32, start=33)), (SHAPE, dict(rot=32, start=-1)),
     (SHAPE, dict(d=4098, rot=64)), (SHAPE, dict(d=1)), (SHAPE, dict(ps=(-1, 1))), (SHAPE, dict(ps=(0, 1 << 41))),
@@ -284,4 +289,4 @@ def test_struct_formats_have_the_header_s_sizes(tmp_path):
     subprocess.run([cc, "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
     assert got == [block._FP8_PACKED.size, block._FP8_WEIGHTS.size, block._BLOCK.size, block._ROPE.size,
-                   struct.calcsize("=5Q6q3if" + 3 * block._VECTOR), struct.calcsize("=3Q4q8ifi")]
+                   struct.calcsize("=5Q6q3if" + 3 * block._VECTOR), struct.calcsize("=3Q4q8ifii4x")]

@@ -302,6 +302,9 @@ def test_norm_refusals():
     _refused(cr.block_update, x, x, out_h=x.bfloat16())
     _refused(cr.block_update, x, x, pack=True)  # nothing to pack
     _refused(cr.block_update, x, x, out=x)
+    _refused(cr.block_update, x, x.clone(), norm=n, out_h=x, out=x)  # both over x
+    _refused(cr.block_update, x, x.clone(), norm=n, out_h=x, out=x[:, :])
+    _refused(cr.block_norm, x.bfloat16().view(-1)[:2560].view(10, 256), n, out=None, out_dtype=torch.int8)
 
 
 def test_rope_refusals():

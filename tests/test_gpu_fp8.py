@@ -261,6 +261,24 @@ def test_results_do_not_vary():
             assert torch.equal(cr.fp8_linear(x, w), first)
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m", [3, 70, 300])
+def test_scales_at_the_ends_of_their_range(m, out):
+    """Scale bytes from 0 (2^-127) to 254 (2^127) in both operands, each value finite in float32 (7/8 of
+    2^127 at most; 7 times it would not be) and the products within its normal range: exact."""
+    n, k = 640, 128
+    g = torch.Generator().manual_seed(m)
+    qx = torch.randint(1, 8, (m, k), generator=g).float() / 8
+    qw = torch.randint(1, 8, (n, k), generator=g).float() / 8
+    for pair in ((0, 240), (1, 239), (3, 254), (127, 60), (240, 0), (254, 3), (239, 1)):
+        sx = torch.full((1, (m + 3) // 4 * 4), pair[0], dtype=torch.uint8).view(E8M0).cuda().t()[:m]
+        sw = torch.full((5, 1), pair[1], dtype=torch.uint8).view(E8M0).cuda()
+        y = cr.fp8_linear(cr.Fp8Activation(qx.to(E4M3).cuda(), sx), cr.Fp8Weights(qw.to(E4M3).cuda(), sw),
+                          out_dtype=out)
+        want = (qx.double() @ qw.double().t()) * 2.0 ** (sum(pair) - 254)
+        assert torch.equal(y.cpu(), want.float().to(out)), pair
+
+
 def _on_gpu(d, w):
     """d W^T in float64 (large references)."""
     return (d.cuda() @ w.cuda().t()).cpu()

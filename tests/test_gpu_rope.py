@@ -162,3 +162,20 @@ def test_empty_calls():
     q, k = cr.rope([torch.ones(2, 0, 32, device="cuda"), torch.ones(2, 1, 32, device="cuda")], plan,
                    torch.tensor([0, 0], device="cuda"))
     assert q.shape == (2, 0, 32) and (k == 1).all()
+
+
+def test_axes_that_positions_do_not_have():
+    """Too few positions for the plan are refused; a pair that names an axis outside them has no
+    position: its results are NaN, the others stay."""
+    plan = cr.rope_plan(12, axes=(4, 4, 4))
+    x = _x(5, 2, 12).cuda()
+    pos = torch.arange(10, device="cuda").view(5, 2)
+    with pytest.raises(ValueError, match="axes"):
+        cr.rope(x, plan, pos)
+    for bad in (2, -1):
+        own = cr.RopePlan(plan.inv_freq, axis=torch.tensor([0, 0, 1, 1, bad, 0], dtype=torch.int32).cuda())
+        y = cr.rope(x, own, pos)
+        assert torch.isnan(y[..., 8:10]).all()
+        good = cr.RopePlan(plan.inv_freq, axis=torch.tensor([0, 0, 1, 1, 0, 0], dtype=torch.int32).cuda())
+        want = cr.rope(x, good, pos)
+        assert torch.equal(y[..., :8], want[..., :8]) and torch.equal(y[..., 10:], want[..., 10:])
