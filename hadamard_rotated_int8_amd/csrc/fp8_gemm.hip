@@ -296,24 +296,24 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   // each, with the blocks of features shared among groups of waves.  Beyond
   // one tile of 128 x 128 for each CU, and for up to 64 rows beyond one of
   // 64 x 64, two workgroups to a CU cover each other's waits instead.
-  // Measured (us, in a graph; bfloat16 outputs; float32 outputs), tiles of
-  //                        32x32  32x64  64x64  64x64 | 32x32  32x64  64x64  64x64
-  //   in groups             4, 8    4      2      1   |  4, 8    4      2      1
-  //   33 x  4096 ->  4096  7.3 7.6  8.3   10.1   11.7 | 9.0 8.1  10.3   15.0   17.3
-  //   16 x 13824 ->  5120 15.0 18.8 18.2  25.0   31.6 | 20.6 19  24.8   41.4   49.7
-  //   64 x 13824 ->  5120   27  33  19.7  25.2   30.7 |   38 34  25.8   41.6   48.7
-  //   64 x  5120 -> 13824   29  31  20.6  15.5   16.0 |   37 32  25.0   20.1   22.2
-  //   64 x  5120 -> 20480           29.8  26.9   25.0 |          35.8   35.7   30.7
+  // Measured (us, in a graph; bfloat16 outputs | float32 outputs), tiles of
+  //                        32x32     32x64 64x64 64x64 | 32x32     32x64 64x64 64x64
+  //   in groups             4    8    4     2     1    |  4    8    4     2     1
+  //   33 x  4096 ->  4096   7.3  7.6  8.2   9.6  11.8  |  8.5  7.8  9.6  13.4  17.8
+  //   16 x 13824 ->  5120  15.2 18.3 17.7  23.1  32.2  | 18.6 18.4 21.7  36.3  50.0
+  //   64 x 13824 ->  5120  27.1 33.9 19.3  25.8  32.5  | 34.4 34.4 23.4  36.1  50.0
+  //   64 x  5120 -> 13824  29.1 32.4 20.6  15.3  16.8  | 33.2 32.6 22.9  17.8  22.6
+  //   64 x  5120 -> 20480  35.9 40.2 29.8  28.2  25.4  | 40.7 40.6 33.0  32.2  29.6
   // and
-  //                        64x64 64x128 128x128 128x64 128x128 |
-  //   in groups              1     1       1      2       2    |
-  //   300 x  4096 ->  4096 15.7  22.1    25.1   15.3    19.1
-  //   333 x  4112 ->  4096                                     | 28.6 27.4 38.7 23.8 32.1
-  //   512 x  4096 ->  4096 18.6  23.0    26.3   16.8    20.1   | 27.4 25.8 37.6 24.3 31.4
-  //   256 x  5120 -> 13824 38.2  30.4    35.1   36.8    27.9   | 55.2 46.1 48.3 52.9 42.8
-  //  1000 x  4096 ->  4096 31.8  27.2    29.1   31.6    24.8   | 51.2 41.1 43.2 46.1 37.9
-  //  2048 x  4096 ->  4096 58.2  53.4    41.2   61.2    47.4   | 85.8 73.7 65.6 88.3 74.1
-  //    64 x  4096 -> 100000 103   124     118    124     132   |  110  128  130  158  144
+  //                        64x64 64x128 128x128 128x64 128x128 | the same
+  //   in groups             1     1      1       2      2
+  //   300 x  4096 ->  4096 16.2  25.3   24.5    14.4   19.0    | 25.0 26.5 35.1 20.6 29.3
+  //   512 x  4096 ->  4096 17.6  25.2   30.3    15.4   20.2    | 26.5 27.9 40.1 22.0 30.2
+  //   200 x 13824 ->  5120 37.0  67.1   85.3    35.2   52.2    | 69.3 72.7  117 52.2 82.5
+  //   256 x  5120 -> 13824 38.6  32.6   41.0    34.2   28.3    | 54.0 44.4 53.7 45.2 39.3
+  //  1000 x  4096 ->  4096 29.7  27.0   32.3    27.5   22.9    | 44.7 38.0 42.7 39.2 35.4
+  //  2048 x  4096 ->  4096 53.4  53.7   38.2    52.0   42.5    | 82.3 69.3 61.7 76.3 67.1
+  //    64 x  4096 -> 100000 103   129    122     123    130    |  106  114  120  133  129
   // (Eight groups need a stage less, which costs more than they gain where
   // the products are quick, with bfloat16 outputs.)
   auto tiles = [&](int64_t bm, int64_t bn) {
