@@ -25,9 +25,12 @@
 //     first half-stages arrive, and its first fragments are read, before this
 //     tile is stored, and its first three half-blocks wait for no store.
 //   * A tile's bias and weight scales come into LDS a tile ahead.
-//   * LDS rows are 128 bytes; 16-byte chunk c of row r sits at slot
-//     c ^ (r & 7) ^ ((r >> 3) & 1), so 16 lanes that read 16 consecutive rows
-//     touch 16 different groups of 4 banks.
+//   * LDS rows are 128 bytes; 16-byte chunk c of row r sits at slot c ^ (r & 7).
+//     A 16-byte read is served 16 lanes at a time, lanes 0-3, 12-15, 20-23 and
+//     24-27 first; of a fragment these hold rows 0-3 and 12-15 of one chunk
+//     and rows 4-11 of the next, in 16 different groups of 4 banks.  (With
+//     bit 3 of the row in the slot as well, which suits 16 rows of one chunk,
+//     46 % of the LDS' busy cycles were conflicts.)
 //   * Bytes past K and rows past M or n read as zero, in both operands (a
 //     NaN code of another row must not meet even a zero).
 //   * A tile is stored 16 rows x 64 columns at a time through LDS, as whole
@@ -66,7 +69,7 @@ struct WideCfg {
   static_assert(2 * PIECES + 1 + STORES <= kVmMax, "vmcnt range");
 };
 
-CR_DEVICE int swz128(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+CR_DEVICE int swz128(int row) { return row & 7; }
 
 // One 16 x 16 x 128 product onto (FIRST: into) its accumulators.  As inline
 // assembly, since all 256 accumulation registers hold the tile: the sum has to
@@ -157,7 +160,7 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
   // these are rows 64 h + 8 q .. of the first wave's 128 (q < 8) or of the
   // second's; of W likewise, with BN / 2 columns per wave.  Lane l fills slot
   // l % 8 of row l / 8 with global chunk (l % 8) ^ swz128(row).
-  const int chunk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);  // (q & 1 = wave & 1)
+  const int chunk = (lane & 7) ^ (lane >> 3);
   const unsigned lane_off = unsigned((lane >> 3) * K + chunk * 16);
   Operands cur = operands(0), next = operands(1);
   // The half-stage being loaded: its block, half and slot, and its scales' place.
