@@ -371,6 +371,13 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
       half(No{}, I2{}, I0{}, I1{}, No{}, it, it, b + 1);
       half(No{}, I2{}, I1{}, I0{}, No{}, it, it, b + 2);
       half(No{}, I2{}, I1{}, I1{}, No{}, it, end ? it + 1 : it, end ? 0 : b + 2);
+      if constexpr (F32) {
+        // Kept in the half of the registers where the instructions take them;
+        // the compiler would carry half of them round the loop in the other,
+        // at 40 copies more.  (All have arrived; fragment 7 has not.)
+#pragma unroll
+        for (int i = 0; i < 7; ++i) asm volatile("" : "+a"(xf[i]));
+      }
     }
     mfma_settle();
     __builtin_amdgcn_sched_barrier(0);
