@@ -65,7 +65,7 @@ def _hazards(lines):
     return checked, found
 
 
-def test_checker_sees_a_planted_hazard():
+def test_a_planted_hazard_is_seen():
     mfma = "v_mfma_scale_f32_16x16x128_f8f6f4 v[0:3], a[0:7], a[8:15], 0, v9, v8 op_sel_hi:[0,0,0]"
     assert _hazards(["v_and_b32_e32 v8, 0xff, v8", mfma])[1]
     assert not _hazards(["v_and_b32_e32 v8, 0xff, v8", "s_nop 1", mfma])[1]
