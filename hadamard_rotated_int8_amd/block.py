@@ -189,7 +189,10 @@ def fp8_quantize_weights(w: torch.Tensor, bias: torch.Tensor | None = None) -> F
 
 
 def fp8_pack_activations(x: torch.Tensor, out: Fp8Activation | None = None) -> Fp8Activation:
-    """E4M3 codes and E8M0 scales of X (float32 or bfloat16 [m, k]) in blocks of 1 x 128."""
+    """E4M3 codes and E8M0 scales of X in blocks of 1 x 128.
+
+    x: float32 or bfloat16 [m, k], k a multiple of 16, rows at multiples of 16 bytes.
+    """
     dev = _device(x, "x")
     dt = _rows(x, "x")
     m, k = x.shape
@@ -215,7 +218,11 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
     """Several FP8 linears on one activation in one launch; returns the outputs.
 
     x: float32 or bfloat16 [m, k], which is packed on the way, or what
-    ``fp8_pack_activations``, ``block_norm`` or ``block_update`` packed.
+    ``fp8_pack_activations``, ``block_norm`` or ``block_update`` packed.  k is a
+    multiple of 16, and the rows of an unpacked x start at multiples of 16 bytes.
+    How the sums are divided depends on the sizes of the whole call, so a row's
+    last bits may differ between calls of different sizes (the same call gives
+    the same bits).
     Output i is act(X W_i^T + bias_i), float32 or bfloat16 [m, n_i].
     """
     if not ws or len(ws) > MAX_GROUPED:

@@ -509,21 +509,29 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
 
 }  // namespace
 
-// From where the tiles of 128 x 128 (fp8_gemm.hip) no longer fit the CUs at
-// once, two to each, and one round of these is as fast: more than half as many
-// tiles as CUs, three quarters with float32 weight scales.  Measured, here and
-// there (us), 4096 -> 4096 with 2048, 2560, 4096 and 8192 rows: 44.9, 47.1,
-// 54.3, 105.9 and 39.2, 60.9, 77.2, 148.8; float32 weight scales with 1536,
-// 2048, 2304 and 4096 rows: 42.7, 41.4, 73.8, 79.8 and 41.8, 46.2, 69.1, 88.0.
+// Whether these tiles take less time than those of 128 x 128 (fp8_gemm.hip),
+// which the CUs hold two each: a round of all CUs takes 1.4 times as long here
+// (0.9 times with float32 weight scales, whose tiles are half as large, and no
+// less where the others do not fill it).  Measured, here and there (us):
+// 4096 -> 4096 with 2048, 2560, 4096 and 8192 rows (rounds 1, 1, 1, 2 and 1, 2,
+// 2, 4) 44.9, 47.1, 54.3, 105.9 and 39.2, 60.9, 77.2, 148.8; 65536 x 4096 -> 64
+// and 200 (1, 1 and 1, 2) 57.0, 81.3 and 50.3, 99.6; 300 x 5120 -> 40000 (2 and
+// 2) 107.8 and 90.9; 129 x 4096 -> 100000 (2 and 4) 121 and 172.  float32 weight
+// scales: 4096 -> 4096 with 1536, 2048, 2304 and 4096 rows (1, 1, 2, 2 and the
+// same) 42.7, 41.4, 73.8, 79.8 and 41.8, 46.2, 69.1, 88.0; 32768 x 5120 -> 128
+// (1 and half a one) 43.9 and 33.7; 300 x 5120 -> 40000 (3 and 2) 125 and 99.
 bool fp8_wide_wanted(const Fp8GemmArgs& a) {
   if (!a.y_bf16 || (a.k + kFp8Block - 1) / kFp8Block < kMinBlocks) return false;
+  const int64_t cus = device_cu_count();
   const int bn = a.f32_scale ? WideCfg<true>::BN : WideCfg<false>::BN;
-  int64_t tiles = 0;
+  int64_t tiles = 0, small = 0;
   for (int i = 0; i < a.count; ++i) {
     if (a.w[i].ldy >= kMaxLdy) return false;
     tiles += ((a.m + kBM - 1) / kBM) * ((a.w[i].n + bn - 1) / bn);
+    small += ((a.m + 127) / 128) * ((a.w[i].n + 127) / 128);
   }
-  return a.f32_scale ? tiles * 4 > int64_t(device_cu_count()) * 3 : tiles * 2 > device_cu_count();
+  const int64_t here = (tiles + cus - 1) / cus, there = (small + 2 * cus - 1) / (2 * cus);
+  return a.f32_scale ? 9 * here <= 10 * there && 2 * small > 3 * cus : 7 * here < 5 * there;
 }
 
 namespace {

@@ -285,7 +285,7 @@ def _on_gpu(d, w):
 
 
 WIDE = [(4096, 4096, 384), (4099, 4200, 400), (8200, 2050, 1040), (300, 33000, 656), (33000, 250, 528),
-        (4096, 4096, 2064), (2500, 4000, 400), (1700, 3900, 656)]
+        (4096, 4096, 2064), (2500, 4000, 400), (1700, 3900, 656), (520, 17000, 656), (129, 66000, 528)]
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
