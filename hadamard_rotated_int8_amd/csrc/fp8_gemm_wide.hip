@@ -79,7 +79,9 @@ CR_DEVICE int swz128(int row) { return row & 7; }
 // is a matrix instruction.  FRESH: an operand may have been written by the
 // vector instruction before (scale bytes are widened where they are first
 // used), which takes 2 wait states.  mfma_settle comes before results are
-// read.  tests/test_matrix_hazards.py checks the built code for both.
+// read.  tests/test_matrix_registers.py checks the built code for both: that
+// the compiler puts no copy right before an instruction without the wait, and
+// nothing that touches a result too early behind one.
 template <bool FIRST, bool FRESH>
 CR_DEVICE void mfma(f32x4& c, v8i w, v8i x, int sw, int sx) {
   if constexpr (FIRST && FRESH)
@@ -102,17 +104,14 @@ CR_DEVICE void mfma(f32x4& c, v8i w, v8i x, int sw, int sx) {
 // A product by itself, from zero, for float32 weight scales: those are applied
 // by vector instructions, which reach only half of the registers.  The
 // accumulators are kept there and the operands in the other half.  The
-// compiler does not wait for c; kPartLead instructions later it is there.
-template <bool FRESH>
+// compiler may copy any operand there right before the instruction (it does so
+// with W fragments that it carries round the K loop), so the 2 wait states
+// come before every one.  It does not wait for c; kPartLead instructions later
+// it is there.
 CR_DEVICE void mfma_part(f32x4& c, v8i w, v8i x, int one, int sx) {
-  if constexpr (FRESH)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "=&v"(c)
-                 : "a"(w), "a"(x), "v"(one), "v"(sx));
-  else
-    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "=&v"(c)
-                 : "a"(w), "a"(x), "v"(one), "v"(sx));
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]"
+               : "=&v"(c)
+               : "a"(w), "a"(x), "v"(one), "v"(sx));
 }
 constexpr int kPartLead = 3;  // 96 cycles; 11 wait states of 4 are needed
 CR_DEVICE void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 3" ::: "memory"); }  // 8 passes: 18 states
@@ -291,7 +290,7 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
       constexpr int idx = decltype(idx_t)::value;
       if constexpr (F32) {
         constexpr int i = 4 * H + idx / FN, j = idx % FN;
-        mfma_part<idx % FN == 0>(part[idx & 3], wf[S][j], xf[i], one, sx[i]);
+        mfma_part(part[idx & 3], wf[S][j], xf[i], one, sx[i]);
       } else {
         constexpr int i = 4 * H + idx / 8, j = i == 7 ? (idx + 4) % 8 : idx % 8;
         mfma<FIRST, idx % 8 == 0>(acc[i][j], j < 4 ? wf[S][j & 3] : wl[j & 3], xf[i], sw, sx[i]);
