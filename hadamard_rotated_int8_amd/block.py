@@ -223,7 +223,9 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
     How the sums are divided depends on the sizes of the whole call, so a row's
     last bits may differ between calls of different sizes (the same call gives
     the same bits).
-    Output i is act(X W_i^T + bias_i), float32 or bfloat16 [m, n_i].
+    Output i is act(X W_i^T + bias_i), float32 or bfloat16 [m, n_i].  Sums are
+    float32; for bfloat16 outputs products more than 13 bits below the largest
+    of 8 neighbouring features are cut (include/convrot.h states the bound).
     """
     if not ws or len(ws) > MAX_GROUPED:
         raise ValueError(f"1 to {MAX_GROUPED} weights")

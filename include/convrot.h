@@ -260,8 +260,17 @@ convrot_status convrot_linear_lora(const convrot_packed* x, const convrot_weight
  * Activations have one scale per row and block, weights one per 128 x 128
  * block:
  *   Y[r, o] = act( sum_b sx[r, b] sw[o / 128, b] sum_{i in b} qx[r, i] qw[o, i] + bias[o] )
- * with float32 sums.  No rotation is applied.  E4M3 is the OCP "fn" format
- * (largest value 448, no infinity).  The library writes power-of-two scales
+ * with float32 sums of exact products where Y is float32.  Where Y is bfloat16
+ * the products of 8 consecutive features (8 j .. 8 j + 7) are first cut to a
+ * multiple of 2^(e - 13), e the largest sum of two factors' exponents among
+ * them (that of an E4M3 subnormal or zero is -6), and added exactly; these sums
+ * are added in float32.  A bfloat16 output is therefore off by less than
+ * 7 2^-13 times the sum of the groups' largest products (all codes E4M3 normal
+ * numbers), besides the float32 additions and its own rounding of 2^-8: for
+ * ordinary data 1.5e-5 to 4e-5 of its size, but an output that is small because
+ * larger products cancel has that error of the larger ones.
+ * No rotation is applied.  E4M3 is the OCP "fn" format (largest value 448, no
+ * infinity).  The library writes power-of-two scales
  * (E8M0: the byte e + 127 stands for 2^e, 255 for NaN): the least e in
  * [-126, 127] for which the block's largest magnitude is at most 448 2^e,
  * and 0 for a block of zeros.  A code is then the E4M3 value nearest to
