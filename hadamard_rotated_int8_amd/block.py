@@ -31,7 +31,8 @@ MAX_NORM_K = 32768
 MAX_ROPE_TENSORS = 4
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
-_SCALE_DTYPE = {torch.float32: F32, torch.float8_e8m0fnu: E8M0}
+_E8M0 = getattr(torch, "float8_e8m0fnu", None)  # (newer than the rest of what the package needs)
+_SCALE_DTYPE = {torch.float32: F32, _E8M0: E8M0}
 _POSITION = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
 
 # The structs of include/convrot.h, as struct formats.
@@ -143,9 +144,15 @@ def _blocks(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
+def _new_scales(*shape, device) -> torch.Tensor:
+    if _E8M0 is None:
+        raise RuntimeError("FP8 scales need a torch that has float8_e8m0fnu")
+    return torch.empty(shape, dtype=_E8M0, device=device)
+
+
 def _new_activation(m: int, k: int, dev) -> Fp8Activation:
     q = torch.empty((m, k), dtype=torch.float8_e4m3fn, device=dev)
-    scale = torch.empty((_blocks(k), (m + 3) // 4 * 4), dtype=torch.float8_e8m0fnu, device=dev)
+    scale = _new_scales(_blocks(k), (m + 3) // 4 * 4, device=dev)
     return Fp8Activation(q, scale.t()[:m])
 
 
@@ -155,7 +162,7 @@ def _check_activation(x: Fp8Activation) -> torch.device:
     if q.dtype != torch.float8_e4m3fn or q.dim() != 2 or not q.is_contiguous():
         raise ValueError("the FP8 codes must be a contiguous float8_e4m3fn [m, k] tensor")
     m, kb = q.shape[0], _blocks(q.shape[1])
-    if s.dtype != torch.float8_e8m0fnu or s.shape != (m, kb) or (s.stride(0) != 1 and m > 1):
+    if s.dtype != _E8M0 or s.shape != (m, kb) or (s.stride(0) != 1 and m > 1):
         raise ValueError("the FP8 scales must be a float8_e8m0fnu [m, ceil(k / 128)] tensor with "
                          "unit row stride")
     if s.device != dev:
@@ -182,7 +189,7 @@ def fp8_quantize_weights(w: torch.Tensor, bias: torch.Tensor | None = None) -> F
     n, k = w.shape
     _check_bias(bias, n, dev)
     q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=dev)
-    scale = torch.empty((_blocks(n), _blocks(k)), dtype=torch.float8_e8m0fnu, device=dev)
+    scale = _new_scales(_blocks(n), _blocks(k), device=dev)
     _launch(lib().convrot_fp8_quantize_weights, "convrot_fp8_quantize_weights", dev, w.data_ptr(),
             dt, n, k, _row_stride(w), q.data_ptr(), scale.data_ptr())
     return Fp8Weights(q, scale, bias)
