@@ -82,7 +82,8 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const BlockNormArgs a)
   const bool alone = MAXT == 256 && a.waves == 1;
   const int T = 64 * a.waves;
   const int t0 = alone ? int(threadIdx.x & 63) : int(threadIdx.x);
-  const int64_t row = alone ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t block = a.first + blockIdx.x;
+  const int64_t row = alone ? block * 4 + (threadIdx.x >> 6) : block;
   if (row >= a.m) return;  // (whole waves, and with W > 1 none)
   const int k = int(a.k);
   const float inv_k = 1.f / float(k);
@@ -256,11 +257,15 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const BlockNormArgs a)
 template <int CPT, int XT, int BT, int MAXT>
 void launch_t(const BlockNormArgs& a, hipStream_t stream) {
   const bool alone = a.waves == 1;
-  const dim3 grid(unsigned(alone ? (a.m + 3) / 4 : a.m)), threads(alone ? 256 : 64 * a.waves);
-  if (a.k % 8 == 0)
-    hipLaunchKernelGGL((block_norm_kernel<CPT, XT, BT, true, MAXT>), grid, threads, 0, stream, a);
-  else
-    hipLaunchKernelGGL((block_norm_kernel<CPT, XT, BT, false, MAXT>), grid, threads, 0, stream, a);
+  const int threads = alone ? 256 : 64 * a.waves;
+  in_launches(alone ? (a.m + 3) / 4 : a.m, threads, [&](int64_t first, unsigned count) {
+    BlockNormArgs part = a;
+    part.first = first;
+    if (a.k % 8 == 0)
+      hipLaunchKernelGGL((block_norm_kernel<CPT, XT, BT, true, MAXT>), dim3(count), dim3(threads), 0, stream, part);
+    else
+      hipLaunchKernelGGL((block_norm_kernel<CPT, XT, BT, false, MAXT>), dim3(count), dim3(threads), 0, stream, part);
+  });
 }
 
 template <int CPT, int MAXT>

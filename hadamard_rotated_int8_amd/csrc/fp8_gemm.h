@@ -26,6 +26,7 @@ struct Fp8Params {
   int nseg;
   int tiles_m, tiles_n;
   int y_bf16, gelu;
+  int first;  // tile of the launch's first workgroup
   struct Seg {
     const uint8_t* qw;
     const void* sw;

@@ -61,11 +61,12 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
   const int K = p.K, kb = p.kb;
+  const int tile = p.first + int(blockIdx.x);
   int s = 0;
   for (int i = 1; i < p.nseg; ++i)
-    if (int(blockIdx.x) >= p.seg[i].tn0) s = i;
+    if (tile >= p.seg[i].tn0) s = i;
   const Fp8Params::Seg& sg = p.seg[s];
-  const int n0 = (int(blockIdx.x) - sg.tn0) * kRows;
+  const int n0 = (tile - sg.tn0) * kRows;
   const int cols = sg.n - n0 < kRows ? sg.n - n0 : kRows;
   const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(sg.qw + (int64_t)n0 * K, cols * K);
 
@@ -188,11 +189,13 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
 
 template <int NT>
 void launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
-  const Fp8Params p = fp8_params<16, 16 * NT>(a);
-  const dim3 grid(unsigned(p.tiles_n));
+  Fp8Params p = fp8_params<16, 16 * NT>(a);
   auto go = [&](auto f32, auto exact) {
-    hipLaunchKernelGGL((fp8_rows_kernel<NT, decltype(f32)::value, decltype(exact)::value>), grid,
-                       dim3(kWaves * 64), 0, stream, p, a.x, a.ldx, a.x_bf16);
+    in_launches(p.tiles_n, kWaves * 64, [&](int64_t first, unsigned count) {
+      p.first = int(first);
+      hipLaunchKernelGGL((fp8_rows_kernel<NT, decltype(f32)::value, decltype(exact)::value>), dim3(count),
+                         dim3(kWaves * 64), 0, stream, p, a.x, a.ldx, a.x_bf16);
+    });
   };
   using Yes = std::true_type;
   using No = std::false_type;

@@ -85,12 +85,13 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const void* __restrict__ 
 // Weights: one workgroup per 128 x 128 block.  Offline.
 template <bool BF16>
 __global__ __launch_bounds__(256) void fp8_wquant_kernel(const void* __restrict__ w, int64_t ldw,
-                                                         int64_t n, int k, int kb,
+                                                         int64_t n, int k, int kb, int64_t first,
                                                          uint8_t* __restrict__ q,
                                                          uint8_t* __restrict__ scale) {
   __shared__ unsigned top[4];
-  const int bk = blockIdx.x % kb;
-  const int64_t bn = blockIdx.x / kb;
+  const int64_t block = first + blockIdx.x;
+  const int64_t bn = block / kb;
+  const int bk = int(block - bn * kb);
   auto at = [&](int64_t r, int c) -> float {
     if constexpr (BF16)
       return __uint_as_float(unsigned(static_cast<const uint16_t*>(w)[r * ldw + c]) << 16);
@@ -145,13 +146,14 @@ hipError_t launch_fp8_pack(const void* x, bool bf16, int64_t ldx, int64_t m, int
 hipError_t launch_fp8_wquant(const void* w, bool bf16, int64_t ldw, int64_t n, int64_t k,
                              uint8_t* q, uint8_t* scale, hipStream_t stream) {
   const int kb = int((k + kFp8Block - 1) / kFp8Block);
-  const dim3 grid(unsigned(((n + kFp8Block - 1) / kFp8Block) * kb));  // checked: < 2^31
-  if (bf16)
-    hipLaunchKernelGGL(fp8_wquant_kernel<true>, grid, dim3(256), 0, stream, w, ldw, n, int(k), kb,
-                       q, scale);
-  else
-    hipLaunchKernelGGL(fp8_wquant_kernel<false>, grid, dim3(256), 0, stream, w, ldw, n, int(k), kb,
-                       q, scale);
+  in_launches((n + kFp8Block - 1) / kFp8Block * kb, 256, [&](int64_t first, unsigned count) {
+    if (bf16)
+      hipLaunchKernelGGL(fp8_wquant_kernel<true>, dim3(count), dim3(256), 0, stream, w, ldw, n, int(k), kb, first, q,
+                         scale);
+    else
+      hipLaunchKernelGGL(fp8_wquant_kernel<false>, dim3(count), dim3(256), 0, stream, w, ldw, n, int(k), kb, first, q,
+                         scale);
+  });
   return hipGetLastError();
 }
 

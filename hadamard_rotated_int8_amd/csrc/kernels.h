@@ -6,6 +6,17 @@
 
 namespace convrot {
 
+// launch(first, count) for the workgroups first .. first + count - 1 of
+// `blocks`, in as many launches as that takes.  A grid names at most 2^32 - 1
+// threads along an axis; HIP takes a larger one without an error and runs the
+// remainder only.
+template <typename F>
+inline void in_launches(int64_t blocks, int threads, F&& launch) {
+  const int64_t most = ((int64_t(1) << 32) - 1) / threads;
+  for (int64_t first = 0; first < blocks; first += most)
+    launch(first, unsigned(blocks - first < most ? blocks - first : most));
+}
+
 // Compute units of the current device (cached per device).
 int device_cu_count();
 
@@ -132,7 +143,8 @@ struct BlockNormArgs {
   bool x_bf16, branch_bf16, y_bf16;
   VectorArgs gate, scale, shift;
   NormArgs post, pre;
-  int waves;  // of a row; the launcher's choice
+  int waves;      // of a row; the launcher's choice
+  int64_t first;  // workgroup of the launch's first one
 };
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
 

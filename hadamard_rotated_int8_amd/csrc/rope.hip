@@ -28,6 +28,7 @@ CR_DEVICE int quotient(int n, Divisor v) {
 }
 
 struct Shape {
+  int64_t first;  // workgroup of the launch's first one
   int tokens;     // per workgroup
   int pairs;      // rot / 2
   int units;      // work items per head: those that turn, then those that copy
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a, const 
   extern __shared__ __attribute__((aligned(16))) float2 cs[];  // [tokens][pairs]
   __shared__ int64_t place[kMaxTokens][2];                     // batch entry, token
   const int64_t total = a.batch * a.tokens;
-  const int64_t t0 = (int64_t)blockIdx.x * s.tokens;
+  const int64_t t0 = (s.first + blockIdx.x) * s.tokens;
   const int nt = total - t0 < s.tokens ? int(total - t0) : s.tokens;
   for (int i = threadIdx.x; i < nt * s.pairs; i += kThreads) {
     const int tl = quotient(i, s.by_pairs), j = i - tl * s.pairs;
@@ -213,19 +214,22 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
   while (s.tokens < kMaxTokens && s.tokens * least < kThreads && total / (2 * s.tokens) >= 2048 &&
          int64_t(2) * s.tokens * most < 65536 && 2 * s.tokens * s.pairs <= 2048)
     s.tokens *= 2;
-  const dim3 grid(unsigned((total + s.tokens - 1) / s.tokens));
   const size_t lds = size_t(s.tokens) * s.pairs * sizeof(float) * 2;
   const int which = (a.half ? 4 : 0) | (a.x_bf16 ? 2 : 0) | (a.y_bf16 ? 1 : 0);
-  switch (which) {
-    case 0: launch_t<false, false, false>(a, s, vec, grid, lds, stream); break;
-    case 1: launch_t<false, false, true>(a, s, vec, grid, lds, stream); break;
-    case 2: launch_t<false, true, false>(a, s, vec, grid, lds, stream); break;
-    case 3: launch_t<false, true, true>(a, s, vec, grid, lds, stream); break;
-    case 4: launch_t<true, false, false>(a, s, vec, grid, lds, stream); break;
-    case 5: launch_t<true, false, true>(a, s, vec, grid, lds, stream); break;
-    case 6: launch_t<true, true, false>(a, s, vec, grid, lds, stream); break;
-    default: launch_t<true, true, true>(a, s, vec, grid, lds, stream); break;
-  }
+  in_launches((total + s.tokens - 1) / s.tokens, kThreads, [&](int64_t first, unsigned count) {
+    const dim3 grid(count);
+    s.first = first;
+    switch (which) {
+      case 0: launch_t<false, false, false>(a, s, vec, grid, lds, stream); break;
+      case 1: launch_t<false, false, true>(a, s, vec, grid, lds, stream); break;
+      case 2: launch_t<false, true, false>(a, s, vec, grid, lds, stream); break;
+      case 3: launch_t<false, true, true>(a, s, vec, grid, lds, stream); break;
+      case 4: launch_t<true, false, false>(a, s, vec, grid, lds, stream); break;
+      case 5: launch_t<true, false, true>(a, s, vec, grid, lds, stream); break;
+      case 6: launch_t<true, true, false>(a, s, vec, grid, lds, stream); break;
+      default: launch_t<true, true, true>(a, s, vec, grid, lds, stream); break;
+    }
+  });
   return hipGetLastError();
 }
 
