@@ -20,6 +20,10 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;
 
 bool float_type(int32_t t) { return t == CONVROT_F32 || t == CONVROT_BF16; }
 unsigned size_of(int32_t t) { return t == CONVROT_BF16 ? 2 : 4; }
+// Whether every row starts at a multiple of 16 bytes.
+bool rows_at_16(const void* x, int64_t m, int64_t ldx, int32_t type) {
+  return aligned16(x) && (m == 1 || ldx * size_of(type) % 16 == 0);
+}
 int64_t blocks(int64_t n) { return (n + CONVROT_FP8_BLOCK - 1) / CONVROT_FP8_BLOCK; }
 
 convrot_status check_k(int64_t k) {
@@ -139,7 +143,7 @@ convrot_status convrot_fp8_pack_activations(const void* x, int32_t x_dtype, int6
     if (!x) return CONVROT_ERR_NULL;
     st = check_fp8_buffers(out);
     if (st != CONVROT_OK) return st;
-    if (!aligned16(x) || (ldx * size_of(x_dtype)) % 16 != 0) return CONVROT_ERR_UNSUPPORTED;
+    if (!rows_at_16(x, m, ldx, x_dtype)) return CONVROT_ERR_UNSUPPORTED;
   }
   out->m = m;
   out->k = k;
@@ -191,7 +195,7 @@ convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m
   if (!float_type(x_dtype)) return CONVROT_ERR_DTYPE;
   if (m == 0 || a.count == 0) return CONVROT_OK;
   if (!x) return CONVROT_ERR_NULL;
-  if (!aligned16(x) || (ldx * size_of(x_dtype)) % 16 != 0) return CONVROT_ERR_UNSUPPORTED;
+  if (!rows_at_16(x, m, ldx, x_dtype)) return CONVROT_ERR_UNSUPPORTED;
   return from_hip(convrot::launch_fp8_gemm_rows(a, static_cast<hipStream_t>(stream)));
 }
 
