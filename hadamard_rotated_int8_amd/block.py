@@ -103,6 +103,14 @@ def _new_like(x: torch.Tensor, dtype: torch.dtype, dev) -> torch.Tensor:
     return torch.empty(x.shape, dtype=dtype, device=dev)
 
 
+def _span(x: torch.Tensor) -> tuple[int, int]:
+    """The addresses from a matrix's first byte to behind its last."""
+    at = x.data_ptr()
+    if x.numel() == 0:
+        return at, at
+    return at, at + (1 + sum((n - 1) * s for n, s in zip(x.shape, x.stride()))) * x.element_size()
+
+
 def _distinct(outs) -> None:
     at = [o.data_ptr() for o in outs if o.numel()]
     if len(set(at)) != len(at):
@@ -233,6 +241,7 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
     Output i is act(X W_i^T + bias_i), float32 or bfloat16 [m, n_i].  Sums are
     float32; for bfloat16 outputs products more than 13 bits below the largest
     of 8 neighbouring features are cut (include/convrot.h states the bound).
+    ``outs`` may lie over an unpacked x, not over one another.
     """
     if not ws or len(ws) > MAX_GROUPED:
         raise ValueError(f"1 to {MAX_GROUPED} weights")
@@ -276,6 +285,10 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
             _rows(o, "an output", dev, (m, w.q.shape[0]))
             _writable_rows(o, "an output")
         _distinct(outs)
+        if rows is not None:  # a workgroup may write Y while another still reads X
+            lo, hi = _span(x)
+            if any(a < hi and lo < b for a, b in map(_span, outs)):
+                x, rows = fp8_pack_activations(x), None
     count = len(ws)
     args = (b"".join(packed), count, struct.pack(f"={count}Q", *[o.data_ptr() for o in outs]),
             struct.pack(f"={count}q", *[_row_stride(o) for o in outs]), dt,
