@@ -291,6 +291,8 @@ convrot_status convrot_rope_apply(const convrot_rope* r, void* stream) {
       for (int j = 0; j < 3; ++j)
         if (t.x_stride[j] != t.y_stride[j]) return CONVROT_ERR_UNSUPPORTED;
     }
+    for (int j = 0; j < a.count; ++j)  // another tensor's place, before it is read or after
+      if (t.y == a.t[j].y || t.y == a.t[j].x || t.x == a.t[j].y) return CONVROT_ERR_UNSUPPORTED;
     convrot::RopeTensor& o = a.t[a.count++];
     o.x = t.x;
     o.y = t.y;

@@ -464,7 +464,8 @@ typedef enum convrot_position_type {
 /*
  * One tensor [batch, tokens, heads, d] with any element strides of the first
  * three axes (stride 1 along d).  y may be x itself with the same strides and
- * type; otherwise they must not overlap.
+ * type; otherwise they must not overlap, nor may y overlap another tensor of
+ * the call.
  */
 typedef struct convrot_rope_tensor {
   const void* x;
