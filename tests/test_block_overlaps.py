@@ -15,4 +15,4 @@ FAKE = boundary.FAKE
     [dict(x=FAKE, y=FAKE + 0x2000), dict(x=FAKE + 0x1000, y=FAKE + 0x2000)],   # one place for both
     [dict(x=FAKE, y=FAKE), dict(x=FAKE, y=FAKE)]])                             # turned twice, or once
 def test_rope_outputs_over_other_tensors_are_refused(t):
-    assert boundary._rope(t=t) == cr.ERR_UNSUPPORTED
+    assert boundary._rope(t=t, count=2) == cr.ERR_UNSUPPORTED
