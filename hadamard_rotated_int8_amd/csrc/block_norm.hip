@@ -6,8 +6,10 @@
 //
 // Bound by HBM: x (and the branch) are read once, h and y written once.
 // Statistics are float32; a layer norm's variance is taken of the
-// differences from the mean (a second sum over the registers), so a large
-// common offset costs no digits.
+// differences from the mean (a second sum over the registers).  A float32
+// mean is itself off by some 2^-24 of the rows' common part, and so is every
+// difference; the differences' own mean, summed with their squares, takes
+// that off again, so a large common part costs no digits.
 #include <type_traits>
 
 #include "fp8.h"
@@ -21,27 +23,48 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kMaxWaves = 16;
 enum { kBf16 = 0, kF32 = 1, kAbsent = 2 };  // types of x and branch
 
+// ROW_HALF_MIRROR and ROW_MIRROR: lane i of each 8 reads lane 7 - i, of each
+// 16 lane 15 - i.
+constexpr int kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+// Every step adds two sums that both lanes of a pair hold, so all lanes get
+// the same bits.  (A rotation by 4 would add in another order in every lane,
+// and lanes would take off different means.)
 CR_DEVICE float wave_sum(float v) {
   v += dpp_f32<kDppQuadSwap1>(v);
   v += dpp_f32<kDppQuadSwap2>(v);
-  v += dpp_f32<kDppRowRor4>(v);
-  v += dpp_f32<kDppRowRor8>(v);
+  v += dpp_f32<kDppHalfMirror>(v);
+  v += dpp_f32<kDppMirror>(v);
   v += __shfl_xor(v, 16);
   v += __shfl_xor(v, 32);
   return v;
 }
 
-// Sum over the row's waves.  Every sum of a row has a `part` of its own, so
+// Sums over the row's waves.  Every sum of a row has a `part` of its own, so
 // one barrier suffices.
-CR_DEVICE float row_sum(float v, float* part, int waves) {
+CR_DEVICE float row_sum(float v, float2* part, int waves) {
   v = wave_sum(v);
   if (waves > 1) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6].x = v;
     __syncthreads();
     v = 0.f;
-    for (int w = 0; w < waves; ++w) v += part[w];
+    for (int w = 0; w < waves; ++w) v += part[w].x;
   }
   return v;
+}
+CR_DEVICE float2 row_sums(float u, float v, float2* part, int waves) {
+  u = wave_sum(u);
+  v = wave_sum(v);
+  if (waves > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(u, v);
+    __syncthreads();
+    u = v = 0.f;
+    for (int w = 0; w < waves; ++w) {
+      u += part[w].x;
+      v += part[w].y;
+    }
+  }
+  return make_float2(u, v);
 }
 
 // Eight consecutive values; loads need only the type's own alignment.
@@ -78,7 +101,7 @@ CR_DEVICE int64_t vector_at(const VectorArgs& v, int64_t row) { return row / v.r
 // is four rows that never wait for one another.
 template <int CPT, int XT, int BT, bool WHOLE, int MAXT>
 __global__ __launch_bounds__(MAXT) void block_norm_kernel(const BlockNormArgs a) {
-  __shared__ float part[4][kMaxWaves];
+  __shared__ float2 part[4][kMaxWaves];
   const bool alone = MAXT == 256 && a.waves == 1;
   const int T = 64 * a.waves;
   const int t0 = alone ? int(threadIdx.x & 63) : int(threadIdx.x);
@@ -138,8 +161,9 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const BlockNormArgs a)
     }
   };
   auto normalise = [&](float (&v)[CPT][8], const NormArgs& n, int slot) {
+    const bool layer = n.kind == kNormLayer;
     float mean = 0.f;
-    if (n.kind == kNormLayer) {
+    if (layer) {
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < CPT; ++c)
@@ -147,22 +171,26 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const BlockNormArgs a)
         for (int i = 0; i < 8; ++i) sum += v[c][i];
       mean = row_sum(sum, part[slot], a.waves) * inv_k;
     }
-    float sq = 0.f;
+    float sum = 0.f, sq = 0.f;
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
       const int left = k - feature(c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = v[c][i] - mean;
+        float d = v[c][i] - mean;
         v[c][i] = d;
-        sq += (WHOLE ? left > 0 : i < left) ? d * d : 0.f;
+        d = (WHOLE ? left > 0 : i < left) ? d : 0.f;
+        sum += d;
+        sq += d * d;
       }
     }
-    const float r = 1.f / sqrtf(row_sum(sq, part[slot + 1], a.waves) * inv_k + n.eps);
+    const float2 s = row_sums(sum, sq, part[slot + 1], a.waves);
+    const float rest = layer ? s.x * inv_k : 0.f;  // of the mean
+    const float r = 1.f / sqrtf(fmaxf(s.y * inv_k - rest * rest, 0.f) + n.eps);
 #pragma unroll
     for (int c = 0; c < CPT; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] *= r;
+      for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(v[c][i], r, -rest * r);
     if (n.weight.p) {
       float w[CPT][8];
       load(w, n.weight.p, n.weight.bf16, 0);
