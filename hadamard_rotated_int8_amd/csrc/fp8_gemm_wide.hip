@@ -509,16 +509,23 @@ __global__ __launch_bounds__(256, 1) void fp8_gemm_wide_kernel(const Fp8Params p
 }  // namespace
 
 // Whether these tiles take less time than those of 128 x 128 (fp8_gemm.hip),
-// which the CUs hold two each: a round of all CUs takes 1.4 times as long here
-// (0.9 times with float32 weight scales, whose tiles are half as large, and no
-// less where the others do not fill it).  Measured, here and there (us):
-// 4096 -> 4096 with 2048, 2560, 4096 and 8192 rows (rounds 1, 1, 1, 2 and 1, 2,
-// 2, 4) 44.9, 47.1, 54.3, 105.9 and 39.2, 60.9, 77.2, 148.8; 65536 x 4096 -> 64
-// and 200 (1, 1 and 1, 2) 57.0, 81.3 and 50.3, 99.6; 300 x 5120 -> 40000 (2 and
-// 2) 107.8 and 90.9; 129 x 4096 -> 100000 (2 and 4) 121 and 172.  float32 weight
-// scales: 4096 -> 4096 with 1536, 2048, 2304 and 4096 rows (1, 1, 2, 2 and the
-// same) 42.7, 41.4, 73.8, 79.8 and 41.8, 46.2, 69.1, 88.0; 32768 x 5120 -> 128
-// (1 and half a one) 43.9 and 33.7; 300 x 5120 -> 40000 (3 and 2) 125 and 99.
+// which the CUs hold two each.
+//
+// Power-of-two scales: a round of all CUs takes 1.4 times as long here.
+// Measured, here and there (us; 4096 -> 4096 unless stated, rounds in
+// brackets): 2048 rows 44.7 (1), 40.5 (1); 2304 44.7 (1), 65.8 (2); 4096 53.9
+// (1), 78.8 (2); 4608 89.9 (2), 103.8 (3); 8192 104.9 (2), 151.6 (4); 32768 x
+// 5120 -> 128 58.1 (1), 33.8 (1); 65536 x 4096 -> 200 80.5 (1), 97.2 (2); 300 x
+// 5120 -> 40000 108.9 (2), 88.3 (2); 129 x 4096 -> 100000 122.3 (2), 171.6 (4).
+//
+// float32 weight scales: the tiles here are half as large, and a last round
+// there that gives each CU one workgroup takes half of a round that gives each
+// two, so those count as halves: a round here takes 7/4 of a half there.  2048
+// rows 43.2 (1), 47.5 (2); 2304 74.7 (2), 68.9 (3); 2816 76.2 (2), 71.3 (3);
+// 3328 77.2 (2), 81.3 (4); 4096 81.9 (2), 87.3 (4); 4608 110.6 (3), 107.6 (5);
+// 6144 120.8 (3), 128.4 (6); 1024 42.1 (1), 28.8 (1); 1280 41.4 (1), 42.4 (2);
+// 32768 x 5120 -> 128 46.7 (1), 34.6 (1); 300 x 5120 -> 40000 131.8 (3), 98.4
+// (4); 129 x 4096 -> 100000 156.0 (4), 174.0 (7).
 bool fp8_wide_wanted(const Fp8GemmArgs& a) {
   if (!a.y_bf16 || (a.k + kFp8Block - 1) / kFp8Block < kMinBlocks) return false;
   const int64_t cus = device_cu_count();
@@ -530,7 +537,10 @@ bool fp8_wide_wanted(const Fp8GemmArgs& a) {
     small += ((a.m + 127) / 128) * ((a.w[i].n + 127) / 128);
   }
   const int64_t here = (tiles + cus - 1) / cus, there = (small + 2 * cus - 1) / (2 * cus);
-  return a.f32_scale ? 9 * here <= 10 * there && 2 * small > 3 * cus : 7 * here < 5 * there;
+  if (!a.f32_scale) return 7 * here < 5 * there;
+  const int64_t last = small % (2 * cus);
+  const int64_t halves = 2 * there - (last > 0 && last <= cus ? 1 : 0);
+  return 7 * here <= 4 * halves;
 }
 
 namespace {

@@ -96,8 +96,10 @@ def _spiky(m, k, g):
                                                                            device="cuda").float()))
 
 
-# rows as they are, tiles of few rows, of middle sizes, large tiles (256 x 256, or 256 x 128)
-SIZES = [(3, 300, 1296), (40, 200, 1296), (333, 1000, 2064), (2113, 2100, 656), (4100, 3900, 1296)]
+# rows as they are, tiles of few rows, of middle sizes, large tiles (256 x 256, or 256 x 128 with
+# float32 weight scales: sizes for both kinds), whole and ragged, several to a workgroup
+SIZES = [(3, 300, 1296), (40, 200, 1296), (333, 1000, 2064), (2113, 2100, 656), (4100, 3900, 1296),
+         (4000, 3900, 1296), (1700, 3900, 656), (130, 65000, 528)]
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
@@ -119,11 +121,11 @@ def test_every_value_is_within_its_bound(m, n, k, data, gelu, out, f32):
     _check(y, cr.fp8_pack_activations(x), w, gelu, out)
 
 
-@pytest.mark.parametrize("f32,k", [(False, 16640), (True, 33024)], ids=["e8m0", "f32scale"])
-def test_large_outputs_of_very_long_rows(f32, k):
+@pytest.mark.parametrize("f32,m,n,k", [(False, 4200, 4200, 16640), (True, 4000, 4000, 33024)],
+                         ids=["e8m0", "f32scale"])
+def test_large_outputs_of_very_long_rows(f32, m, n, k):
     """More blocks of features than a workgroup has threads to fetch their weight scales at once, several
     tiles to a workgroup: small integers, exact."""
-    m, n = 4200, 4200
     print(f"[gpu] fp8 linear large and long {m}x{n}x{k} f32scale={f32}", flush=True)
     g = torch.Generator(device="cuda").manual_seed(k)
     kb, nb = k // 128, -(-n // 128)
@@ -149,7 +151,7 @@ def test_large_outputs_of_very_long_rows(f32, k):
 
 @pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32scale"])
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("m,n,k", [(3, 300, 5136), (40, 200, 5136), (333, 1000, 5136), (4100, 3900, 5136)])
+@pytest.mark.parametrize("m,n,k", [(3, 300, 5136), (40, 200, 5136), (333, 1000, 5136), (4100, 3900, 5136), (4000, 3900, 5136)])
 def test_large_blocks_that_cancel_leave_the_small_ones(m, n, k, out, f32):
     """The first block holds one product of 2^p, the last one its opposite; small integers between."""
     print(f"[gpu] fp8 linear cancelling blocks {m}x{n}x{k} {out} f32scale={f32}", flush=True)
@@ -169,3 +171,30 @@ def test_large_blocks_that_cancel_leave_the_small_ones(m, n, k, out, f32):
         want = x.double() @ q.double().t().contiguous()
         assert want.abs().max() < 2 ** 14 and want.norm() > 0
         assert torch.equal(cr.fp8_linear(x, w, out_dtype=out), want.float().to(out)), p
+
+
+@pytest.mark.parametrize("m,n,k", [(4000, 3900, 400), (6100, 4090, 400), (8190, 2040, 528), (255, 65000, 400)])
+def test_large_outputs_with_float32_scales(m, n, k):
+    """More ragged edges of the 256 x 128 tiles, with rows that allow wide stores and rows that do not:
+    small integers, exact, and nothing beside the outputs."""
+    print(f"[gpu] fp8 linear large float32 scales {m}x{n}x{k}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    kb, nb = -(-k // 128), -(-n // 128)
+
+    def integers(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, generator=g, device="cuda")
+
+    x = cr.Fp8Activation(integers(-3, 4, m, k).float().to(E4M3),
+                         integers(127, 129, kb, (m + 3) // 4 * 4).to(torch.uint8).view(E8M0).t()[:m])
+    w = cr.Fp8Weights(integers(-2, 3, n, k).float().to(E4M3), 1 + 0.5 * integers(0, 2, nb, kb).float(),
+                      integers(-8, 9, n).float())
+    d = _codes(x.q) * x.scale.float().double().repeat_interleave(128, 1)[:, :k]
+    v = _codes(w.q) * _weight_scales(w, slice(None)).repeat_interleave(128, 1)[:, :k]
+    want = (d @ v.t().contiguous() + w.bias.double()).float().to(torch.bfloat16)
+    assert torch.equal(cr.fp8_linear(x, w, out_dtype=torch.bfloat16), want)
+    wide = torch.full((m, n + 11), 7.0, dtype=torch.bfloat16, device="cuda")
+    for at in (1, 8):
+        cr.fp8_linear(x, w, out=wide[:, at:at + n])
+        assert torch.equal(wide[:, at:at + n], want)
+        assert (wide[:, :at] == 7).all() and (wide[:, at + n:] == 7).all()
+        wide.fill_(7)
