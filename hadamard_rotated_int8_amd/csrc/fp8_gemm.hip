@@ -262,7 +262,7 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
           if (p.gelu) v[e] = gelu_erf(v[e]);
         }
         if (m < p.M && n < sg.n)
-          store4(sg.y, (int64_t)m * ldy + n, v, sg.n - n, p.y_bf16, vec && n + 4 <= sg.n);
+          store4(sg.y, (int64_t)m * ldy + n, v, sg.n - n, p.y_bf16, vec && sg.n - n >= 4);
       }
   }
 }

@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
         if (p.gelu) o[e] = gelu_erf(o[e]);
       }
       const bool vec = (sg.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(sg.y) & (p.y_bf16 ? 7 : 15)) == 0;
-      store4(sg.y, row * sg.ldy + n, o, sg.n - n, p.y_bf16, vec && n + 4 <= sg.n);
+      store4(sg.y, row * sg.ldy + n, o, sg.n - n, p.y_bf16, vec && sg.n - n >= 4);
     }
   }
 }

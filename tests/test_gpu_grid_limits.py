@@ -95,3 +95,28 @@ def test_linear_weight_rows(rows, n):
     want = (x.double() @ codes.float().double().t().contiguous()).to(torch.bfloat16)
     for at in range(0, n, period):
         assert torch.equal(y[:, at:at + period], want[:, :n - at]), at
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows", [True, False], ids=["unpacked", "packed"])
+def test_linear_of_the_most_weight_rows(rows, out):
+    """2^31 - 1 weight rows, outputs with room for a vector store behind the last one: what lies there
+    stays (a column number plus 4 does not fit 32 bits)."""
+    n, k = 2 ** 31 - 1, 16
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    print(f"[gpu] fp8 linear 2x{n}x{k} {out} unpacked={rows}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randint(-3, 4, (2, k), generator=g, device="cuda").float()
+    period = 2 ** 24
+    codes = torch.randint(-2, 3, (period, k), generator=g, device="cuda").float().to(E4M3)
+    q = torch.empty(n, k, dtype=E4M3, device="cuda")
+    for at in range(0, n, period):
+        q.view(torch.uint8)[at:at + period] = codes.view(torch.uint8)[:n - at]
+    scale = torch.full((-(-n // 128), 1), 127, dtype=torch.uint8, device="cuda").view(E8M0)
+    y = torch.full((2, n + 1), 9.0, dtype=out, device="cuda")
+    cr.fp8_linear(x if rows else cr.fp8_pack_activations(x), cr.Fp8Weights(q, scale), out=y[:, :n])
+    want = (x.double() @ codes.float().double().t().contiguous()).to(out)
+    for at in range(0, n, period):
+        assert torch.equal(y[:, at:min(at + period, n)], want[:, :n - at]), at
+    assert (y[:, n] == 9).all()
