@@ -82,7 +82,9 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const void* __restrict__ 
   }
 }
 
-// Weights: one workgroup per 128 x 128 block.  Offline.
+// Weights: one workgroup per 128 x 128 block, which it reads twice, the second
+// time mostly from the caches.  Offline.  13824 x 5120 takes 54 us in bfloat16
+// (3.9 TB/s, each byte counted once) and 100 us in float32 (3.5).
 template <bool BF16>
 __global__ __launch_bounds__(256) void fp8_wquant_kernel(const void* __restrict__ w, int64_t ldw,
                                                          int64_t n, int k, int kb, int64_t first,
