@@ -186,11 +186,13 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const BlockNormArgs a)
     }
     const float2 s = row_sums(sum, sq, part[slot + 1], a.waves);
     const float rest = layer ? s.x * inv_k : 0.f;  // of the mean
-    const float r = 1.f / sqrtf(fmaxf(s.y * inv_k - rest * rest, 0.f) + n.eps);
+    const float var = s.y * inv_k - rest * rest;
+    const float r = 1.f / sqrtf((var < 0.f ? 0.f : var) + n.eps);  // (a NaN stays one)
+    const float back = rest != 0.f ? -rest * r : -0.f;             // (r may be infinite)
 #pragma unroll
     for (int c = 0; c < CPT; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(v[c][i], r, -rest * r);
+      for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(v[c][i], r, back);
     if (n.weight.p) {
       float w[CPT][8];
       load(w, n.weight.p, n.weight.bf16, 0);

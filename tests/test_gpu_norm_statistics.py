@@ -113,3 +113,32 @@ def test_rows_of_equal_values():
         y = cr.block_norm(x.cuda(), cr.Norm("layer", 1e-6)).cpu().double()
         # a mean's rounding, 64 u |v|, less its own mean: 70 u of that, over 1e-3
         assert (y.abs() <= 70 * U * 64 * U * x.double().abs() / 1e-3 + 1e-30).all()
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("k", [5, 384, 2000])
+def test_a_row_with_a_nan_is_nan_and_others_are_not(k, kind):
+    """As the formula has it: the statistics of such a row are NaN.  An infinity makes the root
+    infinite: 0 for the other values of an rms norm, NaN for itself and for all of a layer norm's."""
+    x = torch.randn(9, k)
+    x[1, 3], x[7, 0], x[4, 2] = float("nan"), float("nan"), float("inf")
+    n = cr.Norm(kind, 1e-6)
+    y = cr.block_norm(x.cuda(), n).cpu()
+    _, after = cr.block_update(x.cuda(), torch.zeros(9, k, device="cuda"), norm=n)
+    h, _ = cr.block_update(torch.zeros(9, k, device="cuda"), x.cuda(), post=n)
+    want = ref.norm(x, kind, 1e-6)
+    assert torch.isnan(want[[1, 7]]).all()
+    for got in (y, after.cpu(), h.cpu()):
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got[4].nan_to_num(1.0), want[4].float().nan_to_num(1.0))
+        rest = [0, 2, 3, 5, 6, 8]
+        assert ((got[rest] - want[rest]).abs() <= _tolerance(x[rest].double(), want[rest], kind, 1e-6)).all()
+
+
+def test_signs_of_zero_and_rows_without_eps():
+    x = torch.zeros(3, 16)
+    x[0, 0], x[0, 1] = -0.0, 2.0
+    x[1] = 1e-30  # squares below float32: the root is of zero
+    y = cr.block_norm(x.cuda(), cr.Norm("rms", 0.0)).cpu()
+    assert torch.signbit(y[0, 0]) and not torch.signbit(y[0, 2]) and y[0, 1] == 4.0
+    assert torch.isinf(y[1]).all() and torch.isnan(y[2]).all()
