@@ -14,14 +14,14 @@ pytestmark = pytest.mark.gpu
 E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
-@pytest.fixture(scope="module", autouse=True)
+@pytest.fixture(autouse=True)
 def device():
     if not torch.cuda.is_available():
         pytest.fail("GPU tests need a visible GPU")
     cr.lib()
     yield
     torch.cuda.synchronize()
-    torch.cuda.empty_cache()
+    torch.cuda.empty_cache()  # (tens of GB each)
 
 
 def test_norm_rows_of_one_wave():
