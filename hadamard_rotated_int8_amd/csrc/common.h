@@ -75,6 +75,11 @@ CR_DEVICE float dpp_f32(float v) {
 CR_DEVICE float bf16_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
 CR_DEVICE float bf16_hi(uint32_t pair) { return __uint_as_float(pair & 0xFFFF0000u); }
 
+CR_DEVICE unsigned bf16_pair(float a, float b) {  // two values to nearest even
+  return unsigned(__builtin_bit_cast(uint16_t, (__bf16)a)) |
+         unsigned(__builtin_bit_cast(uint16_t, (__bf16)b)) << 16;
+}
+
 // Activation code of a rotated value x, given r = RN(1/s) for the row scale s:
 // round half away from zero of x r, as trunc(RN(x r + copysign(0.5 - 2^-25, x)))
 // -- one fused multiply-add; the float->int conversion truncates toward zero.

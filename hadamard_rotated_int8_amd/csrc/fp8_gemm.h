@@ -81,11 +81,6 @@ inline Fp8Params fp8_params(const Fp8GemmArgs& a) {
   return p;
 }
 
-CR_DEVICE unsigned bf16_pair(float a, float b) {  // two values to nearest even
-  return unsigned(__builtin_bit_cast(uint16_t, (__bf16)a)) |
-         unsigned(__builtin_bit_cast(uint16_t, (__bf16)b)) << 16;
-}
-
 // Four consecutive columns of one output row; `whole` when all four exist and
 // the row allows a vector store.
 CR_DEVICE void store4(void* y, int64_t at, const float* v, int left, bool bf16, bool whole) {

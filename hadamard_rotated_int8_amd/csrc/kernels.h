@@ -175,4 +175,27 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 
+// Attention (attention.hip).
+struct AttentionArgs {
+  const uint16_t *q, *k, *v;  // bfloat16
+  uint16_t* out;
+  int64_t qs[3], ks[3], vs[3], os[3];  // element strides of batch, token and head
+  int64_t batch, m, l;
+  int kv_heads, ratio, d;  // ratio: query heads that share a key head
+  float scale;
+  const int32_t* lengths;  // [batch] or nullptr
+  const uint8_t* mask;     // [batch] rows of l bytes, or nullptr
+  int64_t mask_stride;
+  float* part;   // [splits][batch][kv_heads][m ratio][d] where the keys are split
+  float* stats;  // ... and the maximum (in powers of two) and sum of each row
+  int tiles, splits;
+  int64_t first;  // workgroup of the launch's first one
+};
+struct AttentionPlan {
+  int64_t tiles;  // of a key head's queries
+  int splits;     // of the keys
+};
+AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d);
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
+
 }  // namespace convrot

@@ -506,6 +506,61 @@ typedef struct convrot_rope {
 /* Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP. */
 convrot_status convrot_rope_apply(const convrot_rope* r, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Attention of m queries to l keys (an encoder's states, or the tokens' own):
+ *   out[r] = sum_j p[r, j] v[j] / sum_j p[r, j],   p[r, j] = exp(scale q[r] . k[j] - max_j)
+ * over the keys that are seen; a query that sees none gives zeros.  Query head
+ * h reads key head h / (heads / kv_heads).  Scores, maxima, sums and the
+ * output's sums are float32; the weights p are rounded to bfloat16 (2^-8 of
+ * each, before their sum is taken) and so is the output.
+ *
+ * Tensors are bfloat16 [batch, m or l, heads, d] with any element strides of
+ * the first three axes (stride 1 along d), 16-byte aligned with strides that
+ * are multiples of 8.  Strides of 0 share keys or values among a batch.
+ * What a hidden key or its value holds does not matter (a NaN neither).
+ * ---------------------------------------------------------------------------
+ */
+#define CONVROT_MAX_HEAD_DIM 256
+
+/*
+ *   q_stride .. out_stride : of batch, token and head, 0 .. 2^40; the tokens'
+ *                 of k and v at most 2^23.  out's elements must not overlap one
+ *                 another nor an input.
+ *   d           : a multiple of 8 in 8 .. CONVROT_MAX_HEAD_DIM
+ *   scale       : > 0 and finite
+ *   lengths     : device int32 [batch]: keys lengths[b] .. l - 1 of batch entry
+ *                 b are hidden; or NULL
+ *   mask        : device bytes [batch, l], row stride mask_stride >= 0: keys
+ *                 with 0 are hidden; or NULL
+ *   workspace   : device, 16-byte aligned, convrot_attention_workspace() bytes,
+ *                 for this call until it has run; NULL where that is 0
+ */
+typedef struct convrot_attention {
+  const void *q, *k, *v;
+  void* out;
+  int64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3];
+  int64_t batch, m, l;
+  int32_t heads, kv_heads, d;
+  float scale;
+  const int32_t* lengths;
+  const uint8_t* mask;
+  int64_t mask_stride;
+  void* workspace;
+  int64_t workspace_bytes;
+} convrot_attention;
+
+/*
+ * The bytes of workspace that a call of these sizes needs on the current
+ * device: few queries over many keys are worked on by several workgroups,
+ * whose parts meet there.  Reads batch, m, l, heads, kv_heads and d only.
+ * Errors: NULL, SHAPE, UNSUPPORTED.
+ */
+convrot_status convrot_attention_workspace(const convrot_attention* a, int64_t* bytes);
+
+/* Errors: NULL, SHAPE (a workspace that is too small, too), UNSUPPORTED, HIP. */
+convrot_status convrot_attention_apply(const convrot_attention* a, void* stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char* convrot_status_string(convrot_status status);
 
