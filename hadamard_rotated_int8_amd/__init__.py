@@ -55,6 +55,8 @@ EXPORTED = (
     "convrot_fp8_linear_rows",
     "convrot_block_norm",
     "convrot_rope_apply",
+    "convrot_group_norm_workspace",
+    "convrot_group_norm_apply",
     "convrot_attention_workspace",
     "convrot_attention_apply",
     "convrot_status_string",
@@ -145,6 +147,10 @@ def lib() -> ctypes.CDLL:
         L.convrot_block_norm.restype = ctypes.c_int
         L.convrot_rope_apply.argtypes = [vp, vp]
         L.convrot_rope_apply.restype = ctypes.c_int
+        L.convrot_group_norm_workspace.argtypes = [vp, vp]
+        L.convrot_group_norm_workspace.restype = ctypes.c_int
+        L.convrot_group_norm_apply.argtypes = [vp, vp]
+        L.convrot_group_norm_apply.restype = ctypes.c_int
         L.convrot_attention_workspace.argtypes = [vp, vp]
         L.convrot_attention_workspace.restype = ctypes.c_int
         L.convrot_attention_apply.argtypes = [vp, vp]
@@ -480,7 +486,7 @@ def linear_lora(x: PackedActivation, ws, adapters, outs=None, gelu: bool = False
 
 # The operators around a block's linears (they use the names above).
 from .block import (  # noqa: E402,F401
-    FP8_BLOCK, MAX_NORM_K, MAX_ROPE_TENSORS, Fp8Activation, Fp8Weights, Norm, RopePlan, block_norm,
-    block_update, fp8_linear, fp8_linear_grouped, fp8_pack_activations, fp8_quantize_weights, rope,
-    rope_plan)
+    FP8_BLOCK, MAX_GROUP_NORM_C, MAX_NORM_K, MAX_ROPE_TENSORS, Fp8Activation, Fp8Weights, Norm, RopePlan,
+    block_norm, block_update, fp8_linear, fp8_linear_grouped, fp8_pack_activations, fp8_quantize_weights,
+    group_norm, rope, rope_plan)
 from .attention import MAX_HEAD_DIM, attention  # noqa: E402,F401

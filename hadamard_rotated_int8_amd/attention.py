@@ -5,13 +5,12 @@ Argument checks and marshalling only, like the package's other helpers.
 
 from __future__ import annotations
 
-import ctypes
 import struct
 
 import torch
 
-from . import OK, ConvrotError, lib
-from .block import _device, _launch, _no_overlap, _span
+from . import lib
+from .block import _device, _launch, _no_overlap, _span, _workspace
 
 MAX_HEAD_DIM = 256
 
@@ -84,14 +83,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | 
             *strides(v), *strides(out), batch, m, l, heads, kv_heads, d, scale,
             0 if lengths is None else lengths.data_ptr(), 0 if mask is None else mask.data_ptr(),
             mask_stride, 0, 0]
-    need = ctypes.c_int64()
-    with torch.cuda.device(dev):
-        st = lib().convrot_attention_workspace(_ATTENTION.pack(*args), ctypes.byref(need))
-    if st != OK:
-        raise ConvrotError(st, "convrot_attention_workspace")
-    if need.value:
-        # (freed behind the call: the stream that it is allocated on runs the call first)
-        space = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        args[-2:] = space.data_ptr(), need.value
-    _launch(lib().convrot_attention_apply, "convrot_attention_apply", dev, _ATTENTION.pack(*args))
+    packed, space = _workspace(lib().convrot_attention_workspace, "convrot_attention_workspace", args,
+                               _ATTENTION, dev)
+    _launch(lib().convrot_attention_apply, "convrot_attention_apply", dev, packed)
     return out

@@ -28,6 +28,7 @@ from . import ACT_GELU, ACT_NONE, BF16, E8M0, F32, MAX_GROUPED, OK, ConvrotError
 FP8_BLOCK = 128
 FP8_MAX_ROWS, FP8_MAX_ROWS_BYTES = 16, 49152  # an activation that is quantised inside the linear
 MAX_NORM_K = 32768
+MAX_GROUP_NORM_C = 4096
 MAX_ROPE_TENSORS = 4
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
@@ -41,6 +42,7 @@ _FP8_WEIGHTS = struct.Struct("=QQQqqi4x")
 _VECTOR = "Qqqi4x"
 _NORM = "if" + _VECTOR + _VECTOR
 _BLOCK = struct.Struct("=5Q6q3if" + 3 * _VECTOR + 2 * _NORM)
+_GROUP_NORM = struct.Struct("=2Q6q4ifi" + 2 * _VECTOR + "Qq")
 _ROPE_TENSOR = "QQ7q"
 _ROPE = struct.Struct("=3Q4q8ifii4x" + 4 * _ROPE_TENSOR)
 
@@ -455,6 +457,85 @@ def block_update(x: torch.Tensor, branch: torch.Tensor, gate: torch.Tensor | Non
         raise ValueError("out and pack need a norm, a scale or a shift")
     _block_call(x, branch, gate, residual_scale, post, norm, scale, shift, out_h, y, packed, dev)
     return out_h, (packed if pack else y)
+
+
+def _workspace(fn, name, args, struct_, dev):
+    """args (whose last two are the workspace and its size) packed with a workspace of the size that
+    the library asks for, and that workspace, which must live until the call is submitted."""
+    need = ctypes.c_int64()
+    if torch._C._cuda_getDevice() == dev.index:
+        st = fn(struct_.pack(*args), ctypes.byref(need))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(struct_.pack(*args), ctypes.byref(need))
+    if st != OK:
+        raise ConvrotError(st, name)
+    space = None
+    if need.value:
+        space = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        args[-2:] = space.data_ptr(), need.value
+    return struct_.pack(*args), space
+
+
+def _positions(x: torch.Tensor, what: str) -> tuple[int, int, int]:
+    """(images, positions, stride of a position) of [batch, ..., c]."""
+    if x.dim() < 3 or (x.stride(-1) != 1 and x.shape[-1] != 1):
+        raise ValueError(f"{what} must be [batch, ..., c] with unit stride along c")
+    count, stride = 1, None
+    for n, st in zip(reversed(x.shape[1:-1]), reversed(x.stride()[1:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * count:
+            raise ValueError(f"the positions of {what} must lie at one distance from one another")
+        count *= n
+    return x.shape[0], count, stride if stride is not None else x.shape[-1]
+
+
+def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, eps: float = 1e-6, silu: bool = False,
+               out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Group norm of channels-last features, with a SiLU behind it if asked:
+    act((x - mean) / sqrt(var + eps) * weight + bias), mean and var over an image's positions and
+    the c / groups neighbouring channels of a group.
+
+    x            : float32 or bfloat16 [batch, ..., c], the positions at one distance from one
+                   another (for [batch, c, height, width] in channels-last memory: x.permute(0, 2, 3, 1))
+    weight, bias : float32 or bfloat16 [c]
+    Returns float32 or bfloat16 in x's shape (x's type by default; ``out`` may be x).
+    """
+    dev = _device(x, "x")
+    if x.dtype not in _DTYPE or (out_dtype is not None and out_dtype not in _DTYPE):
+        raise ValueError("x and out must be float32 or bfloat16")
+    batch, positions, xs = _positions(x, "x")
+    c = x.shape[-1]
+    if not 1 <= c <= MAX_GROUP_NORM_C or groups < 1 or c % groups:
+        raise ValueError(f"groups must divide the channels, which are 1 to {MAX_GROUP_NORM_C}")
+    if 0 in x.shape:
+        positions = 0
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        ys = c
+    else:
+        if out.dtype not in _DTYPE or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must be of out_dtype")
+        if out.shape != x.shape or out.device != dev:
+            raise ValueError("out must have x's shape and device")
+        ys = _positions(out, "out")[2]
+        if not _no_overlap(out):
+            raise ValueError("out's elements must not overlap")
+        if out.data_ptr() != x.data_ptr() or out.stride() != x.stride() or out.dtype != x.dtype:
+            (a, b), (lo, hi) = _span(x), _span(out)
+            if a < hi and lo < b:
+                raise ValueError("out must be x itself or lie in memory of its own")
+    args = [x.data_ptr(), out.data_ptr(), x.stride(0), xs, out.stride(0), ys, batch, positions, c, groups,
+            _DTYPE[x.dtype], _DTYPE[out.dtype], eps, 1 if silu else 0,
+            *_vector_args(weight, c, "weight", dev), *_vector_args(bias, c, "bias", dev), 0, 0]
+    packed, space = _workspace(lib().convrot_group_norm_workspace, "convrot_group_norm_workspace", args,
+                               _GROUP_NORM, dev)
+    _launch(lib().convrot_group_norm_apply, "convrot_group_norm_apply", dev, packed)
+    return out
 
 
 # ---------------------------------------------------------------------------

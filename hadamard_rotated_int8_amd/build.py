@@ -27,7 +27,7 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "pack.hip", "wprep.hip", "gemm.hip", "gemm_small.hip", "lora.hip",
            "api_block.cpp", "fp8_pack.hip", "fp8_gemm.hip", "fp8_gemm_wide.hip", "fp8_gemm_rows.hip", "block_norm.hip", "rope.hip",
-           "api_attention.cpp", "attention.hip"]
+           "group_norm.hip", "api_attention.cpp", "attention.hip"]
 CEILING_SOURCES = ["ceiling.hip"]
 
 # Packed-FP32 instructions are kept out of generated code on purpose.

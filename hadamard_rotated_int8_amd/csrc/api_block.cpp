@@ -1,4 +1,4 @@
-// C ABI of the FP8 linears, the block norms and the rotary positions:
+// C ABI of the FP8 linears, the block and group norms and the rotary positions:
 // argument validation (on the host, before any HIP call) and dispatch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -107,6 +107,21 @@ convrot_status check_fp8_linear(const convrot_fp8_weights* w, int32_t count, voi
   }
   // (32 x 32 tiles, smaller than any kernel's, are counted in 32 bits)
   return tiles * ((a->m + 31) / 32) > int64_t(INT32_MAX) ? CONVROT_ERR_SHAPE : CONVROT_OK;
+}
+
+convrot_status check_group_norm_sizes(const convrot_group_norm& g) {
+  if (g.batch < 0 || g.positions < 0 || g.batch > kMaxRows || g.positions > kMaxRows || g.c < 1 ||
+      g.c > CONVROT_MAX_GROUP_NORM_C || g.groups < 1 || g.c % g.groups != 0 ||
+      g.batch > (int64_t(1) << 40) / CONVROT_MAX_GROUP_NORM_C)
+    return CONVROT_ERR_SHAPE;
+  return CONVROT_OK;
+}
+int64_t group_norm_runs(const convrot_group_norm& g) {
+  return convrot::plan_group_norm(g.batch, g.positions, g.c, g.groups);
+}
+// A mean and a sum of squares for each run, and what becomes of them.
+int64_t group_norm_bytes(const convrot_group_norm& g, int64_t runs) {
+  return runs > 0 ? g.batch * g.groups * (8 * runs + 16) : 0;
 }
 
 }  // namespace
@@ -260,6 +275,59 @@ convrot_status convrot_block_norm(const convrot_block* b, void* stream) {
   a.branch_bf16 = b->branch_dtype == CONVROT_BF16;
   a.y_bf16 = b->y_dtype == CONVROT_BF16;
   return from_hip(convrot::launch_block_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+convrot_status convrot_group_norm_workspace(const convrot_group_norm* g, int64_t* bytes) {
+  if (!g || !bytes) return CONVROT_ERR_NULL;
+  const convrot_status st = check_group_norm_sizes(*g);
+  if (st != CONVROT_OK) return st;
+  *bytes = g->batch == 0 || g->positions == 0 ? 0 : group_norm_bytes(*g, group_norm_runs(*g));
+  return CONVROT_OK;
+}
+
+convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* stream) {
+  if (!g) return CONVROT_ERR_NULL;
+  convrot_status st = check_group_norm_sizes(*g);
+  if (st != CONVROT_OK) return st;
+  if (!float_type(g->x_dtype) || !float_type(g->y_dtype) || (g->silu != 0 && g->silu != 1))
+    return CONVROT_ERR_DTYPE;
+  if (!(g->eps >= 0.f)) return CONVROT_ERR_UNSUPPORTED;  // a NaN too
+  for (int i = 0; i < 2; ++i)
+    if (g->x_stride[i] < 0 || g->x_stride[i] > kMaxStride || g->y_stride[i] < 0 || g->y_stride[i] > kMaxStride)
+      return CONVROT_ERR_SHAPE;
+  convrot::GroupNormArgs a{};
+  if ((st = fill_vector(g->weight, g->c, false, &a.weight)) != CONVROT_OK) return st;
+  if ((st = fill_vector(g->bias, g->c, false, &a.bias)) != CONVROT_OK) return st;
+  if (g->batch == 0 || g->positions == 0) return CONVROT_OK;
+  if (!g->x || !g->y) return CONVROT_ERR_NULL;
+  if (!aligned(g->x, size_of(g->x_dtype)) || !aligned(g->y, size_of(g->y_dtype))) return CONVROT_ERR_UNSUPPORTED;
+  if (g->x == g->y && (g->x_dtype != g->y_dtype || g->x_stride[0] != g->y_stride[0] ||
+                       g->x_stride[1] != g->y_stride[1]))
+    return CONVROT_ERR_UNSUPPORTED;
+  a.runs = group_norm_runs(*g);
+  const int64_t bytes = group_norm_bytes(*g, a.runs);
+  if (bytes > 0) {
+    if (!g->workspace) return CONVROT_ERR_NULL;
+    if (g->workspace_bytes < bytes) return CONVROT_ERR_SHAPE;
+    if (!aligned16(g->workspace)) return CONVROT_ERR_UNSUPPORTED;
+  }
+  a.x = g->x;
+  a.y = g->y;
+  for (int i = 0; i < 2; ++i) {
+    a.xs[i] = g->x_stride[i];
+    a.ys[i] = g->y_stride[i];
+  }
+  a.batch = g->batch;
+  a.positions = g->positions;
+  a.c = g->c;
+  a.groups = g->groups;
+  a.eps = g->eps;
+  a.x_bf16 = g->x_dtype == CONVROT_BF16;
+  a.y_bf16 = g->y_dtype == CONVROT_BF16;
+  a.silu = g->silu != 0;
+  a.stats = static_cast<float*>(g->workspace);
+  a.part = a.stats + 4 * g->batch * g->groups;
+  return from_hip(convrot::launch_group_norm(a, static_cast<hipStream_t>(stream)));
 }
 
 convrot_status convrot_rope_apply(const convrot_rope* r, void* stream) {

@@ -175,6 +175,25 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 
+// Group norm, channels last (group_norm.hip).
+constexpr int kMaxGroupNormC = 4096;
+struct GroupNormArgs {
+  const void* x;
+  void* y;
+  int64_t xs[2], ys[2];  // element strides of image and position
+  int64_t batch, positions;
+  int c, groups;
+  float eps;
+  bool x_bf16, y_bf16, silu;
+  VectorArgs weight, bias;
+  int64_t runs;  // of an image's positions, or 0: a group in one workgroup
+  float* part;   // [batch][runs][groups] mean and squared differences, with runs
+  float* stats;  // [batch][groups] first value, mean from it, 1 / deviation, unused
+  int64_t first;  // workgroup of the launch's first one
+};
+int64_t plan_group_norm(int64_t batch, int64_t positions, int c, int groups);
+hipError_t launch_group_norm(const GroupNormArgs& a, hipStream_t stream);
+
 // Attention (attention.hip).
 struct AttentionArgs {
   const uint16_t *q, *k, *v;  // bfloat16

@@ -508,6 +508,52 @@ convrot_status convrot_rope_apply(const convrot_rope* r, void* stream);
 
 /*
  * ---------------------------------------------------------------------------
+ * Group norm of channels-last features, with an optional SiLU behind it:
+ *   y = act((x - mean) / sqrt(var + eps) * weight + bias)
+ * mean and var (of the differences from the mean) over an image's positions
+ * and a group's c / groups neighbouring channels, in float32.
+ * ---------------------------------------------------------------------------
+ */
+#define CONVROT_MAX_GROUP_NORM_C 4096
+
+/*
+ *   x, y     : device [batch, positions, c] of x_dtype and y_dtype (CONVROT_F32
+ *              or CONVROT_BF16), element strides of image and position at most
+ *              2^40 (stride 1 along c); y may be x itself with the same strides
+ *              and type, and must not overlap it otherwise.  Pointers need
+ *              their element's alignment only.
+ *   weight, bias : c values each, or absent (a norm's: stride and rows are not read)
+ *   c        : at most CONVROT_MAX_GROUP_NORM_C, groups divide it; eps >= 0
+ *   silu     : 1 for v / (1 + exp(-v)) of the result, else 0
+ *   workspace : device, 16-byte aligned, convrot_group_norm_workspace() bytes,
+ *              for this call until it has run; NULL where that is 0
+ */
+typedef struct convrot_group_norm {
+  const void* x;
+  void* y;
+  int64_t x_stride[2], y_stride[2];
+  int64_t batch, positions;
+  int32_t c, groups;
+  int32_t x_dtype, y_dtype;
+  float eps;
+  int32_t silu;
+  convrot_vector weight, bias;
+  void* workspace;
+  int64_t workspace_bytes;
+} convrot_group_norm;
+
+/*
+ * The bytes of workspace that a call of these sizes needs on the current
+ * device.  Reads batch, positions, c and groups only.
+ * Errors: NULL, SHAPE.
+ */
+convrot_status convrot_group_norm_workspace(const convrot_group_norm* g, int64_t* bytes);
+
+/* Errors: NULL, SHAPE (a workspace that is too small, too), DTYPE, UNSUPPORTED, HIP. */
+convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Attention of m queries to l keys (an encoder's states, or the tokens' own):
  *   out[r] = sum_j p[r, j] v[j] / sum_j p[r, j],   p[r, j] = exp(scale q[r] . k[j] - max_j)
  * over the keys that are seen; a query that sees none gives zeros.  Query head
