@@ -36,6 +36,7 @@ I32 = 2
 E8M0 = 3
 ACT_NONE = 0
 ACT_GELU = 1
+ACT_SILU = 2
 MAX_K = 133136
 MAX_LOG4_GROUP = 7
 MAX_GROUPED = 8
@@ -53,6 +54,10 @@ EXPORTED = (
     "convrot_fp8_pack_activations",
     "convrot_fp8_linear_grouped",
     "convrot_fp8_linear_rows",
+    "convrot_fp8_gated",
+    "convrot_fp8_gated_rows",
+    "convrot_fp8_gated_backward",
+    "convrot_fp8_transpose_weights",
     "convrot_block_norm",
     "convrot_rope_apply",
     "convrot_group_norm_workspace",
@@ -143,6 +148,14 @@ def lib() -> ctypes.CDLL:
         L.convrot_fp8_linear_grouped.restype = ctypes.c_int
         L.convrot_fp8_linear_rows.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, i32, i32, vp]
         L.convrot_fp8_linear_rows.restype = ctypes.c_int
+        L.convrot_fp8_gated.argtypes = [vp, vp, vp]
+        L.convrot_fp8_gated.restype = ctypes.c_int
+        L.convrot_fp8_gated_rows.argtypes = [vp, i32, i64, i64, i64, vp, vp]
+        L.convrot_fp8_gated_rows.restype = ctypes.c_int
+        L.convrot_fp8_gated_backward.argtypes = [vp, vp]
+        L.convrot_fp8_gated_backward.restype = ctypes.c_int
+        L.convrot_fp8_transpose_weights.argtypes = [vp, i32, vp, vp, vp]
+        L.convrot_fp8_transpose_weights.restype = ctypes.c_int
         L.convrot_block_norm.argtypes = [vp, vp]
         L.convrot_block_norm.restype = ctypes.c_int
         L.convrot_rope_apply.argtypes = [vp, vp]
@@ -487,6 +500,6 @@ def linear_lora(x: PackedActivation, ws, adapters, outs=None, gelu: bool = False
 # The operators around a block's linears (they use the names above).
 from .block import (  # noqa: E402,F401
     FP8_BLOCK, MAX_GROUP_NORM_C, MAX_NORM_K, MAX_ROPE_TENSORS, Fp8Activation, Fp8Weights, Norm, RopePlan,
-    block_norm, block_update, fp8_linear, fp8_linear_grouped, fp8_pack_activations, fp8_quantize_weights,
-    group_norm, rope, rope_plan)
+    block_norm, block_update, fp8_gated, fp8_gated_backward, fp8_linear, fp8_linear_grouped,
+    fp8_pack_activations, fp8_quantize_weights, fp8_transpose_weights, group_norm, rope, rope_plan)
 from .attention import MAX_HEAD_DIM, attention  # noqa: E402,F401

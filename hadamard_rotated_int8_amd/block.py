@@ -23,7 +23,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import ACT_GELU, ACT_NONE, BF16, E8M0, F32, MAX_GROUPED, OK, ConvrotError, lib
+from . import ACT_GELU, ACT_NONE, ACT_SILU, BF16, E8M0, F32, MAX_GROUPED, MAX_K, OK, ConvrotError, lib
 
 FP8_BLOCK = 128
 FP8_MAX_ROWS, FP8_MAX_ROWS_BYTES = 16, 49152  # an activation that is quantised inside the linear
@@ -39,6 +39,8 @@ _POSITION = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
 # The structs of include/convrot.h, as struct formats.
 _FP8_PACKED = struct.Struct("=QQqqq")
 _FP8_WEIGHTS = struct.Struct("=QQQqqi4x")
+_GATED_TAIL = struct.Struct("=Qq2i2Qq")  # behind the two weights
+_GATED_BACKWARD = struct.Struct("=6Q5q2i")
 _VECTOR = "Qqqi4x"
 _NORM = "if" + _VECTOR + _VECTOR
 _BLOCK = struct.Struct("=5Q6q3if" + 3 * _VECTOR + 2 * _NORM)
@@ -230,6 +232,28 @@ def _check_bias(bias, n, dev):
             raise ValueError("all tensors of one call must be on the same device")
 
 
+def _weight_args(w: Fp8Weights, dev) -> bytes:
+    """Check an FP8 weight; returns its C struct."""
+    q, s = w.q, w.scale
+    if q.dtype != torch.float8_e4m3fn or q.dim() != 2 or not q.is_contiguous():
+        raise ValueError("weight codes must be a contiguous float8_e4m3fn [n, k] tensor")
+    n = q.shape[0]
+    sdt = _SCALE_DTYPE.get(s.dtype)
+    if sdt is None or s.shape != (_blocks(n), _blocks(q.shape[1])) or not s.is_contiguous():
+        raise ValueError("weight scales must be a contiguous float8_e8m0fnu or float32 "
+                         "[ceil(n / 128), ceil(k / 128)] tensor")
+    b = w.bias
+    _check_bias(b, n, dev)
+    if q.device != dev or s.device != dev:
+        raise ValueError("all tensors of one call must be on the same device")
+    return _FP8_WEIGHTS.pack(q.data_ptr(), s.data_ptr(), 0 if b is None else b.data_ptr(), n, q.shape[1], sdt)
+
+
+def _few_rows(m: int, k: int) -> bool:
+    """Whether X is quantised inside the linear."""
+    return m <= FP8_MAX_ROWS and m * _blocks(k) * FP8_BLOCK <= FP8_MAX_ROWS_BYTES
+
+
 def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
                        out_dtype: torch.dtype = torch.float32, gelu: bool = False):
     """Several FP8 linears on one activation in one launch; returns the outputs.
@@ -255,27 +279,12 @@ def fp8_linear_grouped(x: torch.Tensor | Fp8Activation, ws, outs=None,
         dev = _device(x, "x")
         rows = _rows(x, "x")
         m, k = x.shape
-        if m > FP8_MAX_ROWS or m * _blocks(k) * FP8_BLOCK > FP8_MAX_ROWS_BYTES:
+        if not _few_rows(m, k):
             x, rows = fp8_pack_activations(x), None
     dt = _DTYPE.get(out_dtype)
     if dt is None:
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
-    packed = []
-    for w in ws:
-        q, s = w.q, w.scale
-        if q.dtype != torch.float8_e4m3fn or q.dim() != 2 or not q.is_contiguous():
-            raise ValueError("weight codes must be a contiguous float8_e4m3fn [n, k] tensor")
-        n = q.shape[0]
-        sdt = _SCALE_DTYPE.get(s.dtype)
-        if sdt is None or s.shape != (_blocks(n), _blocks(q.shape[1])) or not s.is_contiguous():
-            raise ValueError("weight scales must be a contiguous float8_e8m0fnu or float32 "
-                             "[ceil(n / 128), ceil(k / 128)] tensor")
-        b = w.bias
-        _check_bias(b, n, dev)
-        if q.device != dev or s.device != dev:
-            raise ValueError("all tensors of one call must be on the same device")
-        packed.append(_FP8_WEIGHTS.pack(q.data_ptr(), s.data_ptr(),
-                                        0 if b is None else b.data_ptr(), n, q.shape[1], sdt))
+    packed = [_weight_args(w, dev) for w in ws]
     if outs is None:
         outs = [torch.empty((m, w.q.shape[0]), dtype=out_dtype, device=dev) for w in ws]
     else:
@@ -309,6 +318,128 @@ def fp8_linear(x: torch.Tensor | Fp8Activation, w: Fp8Weights, out: torch.Tensor
     if out_dtype is None:
         out_dtype = torch.float32 if out is None else out.dtype
     return fp8_linear_grouped(x, (w,), None if out is None else (out,), out_dtype, gelu)[0]
+
+
+_GATED_ACT = {"silu": ACT_SILU, "gelu": ACT_GELU}
+
+
+def _gated_act(act: str) -> int:
+    code = _GATED_ACT.get(act)
+    if code is None:
+        raise ValueError('act must be "silu" or "gelu"')
+    return code
+
+
+def fp8_gated(x: torch.Tensor | Fp8Activation, gate: Fp8Weights, up: Fp8Weights, act: str = "silu",
+              out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, keep: bool = False):
+    """act(G) * U of a gated feed-forward, G = X gate^T + its bias, U = X up^T + its bias, in one kernel.
+
+    x    : as ``fp8_linear`` takes it
+    gate, up : [n, k] each, with scales of one type
+    act  : "silu" or "gelu" (erf form), of the unrounded G
+    Returns float32 (by default) or bfloat16 [m, n]; with ``keep`` also the pair (G, U) as bfloat16
+    [m, n], which ``fp8_gated_backward`` takes.  ``out`` may lie over an unpacked x.
+    """
+    code = _gated_act(act)
+    rows = None
+    if isinstance(x, Fp8Activation):
+        dev = _check_activation(x)
+        m, k = x.q.shape
+    else:
+        dev = _device(x, "x")
+        rows = _rows(x, "x")
+        m, k = x.shape
+        if not _few_rows(m, k):
+            x, rows = fp8_pack_activations(x), None
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    dt = _DTYPE.get(out_dtype)
+    if dt is None:
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    weights = _weight_args(gate, dev) + _weight_args(up, dev)
+    n = gate.q.shape[0]
+    if up.q.shape != gate.q.shape or up.scale.dtype != gate.scale.dtype:
+        raise ValueError("gate and up must share shape and type of scales")
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    else:
+        if out.dtype != out_dtype:
+            raise ValueError("out must be of out_dtype")
+        _rows(out, "out", dev, (m, n))
+        _writable_rows(out, "out")
+        if rows is not None:  # a workgroup may write Y while another still reads X
+            (lo, hi), (a, b) = _span(x), _span(out)
+            if a < hi and lo < b:
+                x, rows = fp8_pack_activations(x), None
+    kept = None
+    if keep:
+        kept = tuple(torch.empty((m, n), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    args = weights + _GATED_TAIL.pack(out.data_ptr(), _row_stride(out), dt, code,
+                                      kept[0].data_ptr() if keep else 0, kept[1].data_ptr() if keep else 0, n)
+    if rows is None:
+        _launch(lib().convrot_fp8_gated, "convrot_fp8_gated", dev, _pack_args(x), args)
+    else:
+        _launch(lib().convrot_fp8_gated_rows, "convrot_fp8_gated_rows", dev, x.data_ptr(), rows, m, k,
+                _row_stride(x), args)
+    return (out, kept) if keep else out
+
+
+def fp8_transpose_weights(ws) -> Fp8Weights:
+    """The transposes of weights [n_i, k] side by side, as one weight [k, sum of n_i rounded up to 128]:
+    the same codes and scales, zeros behind each n_i.  Made once, for gradients at a linear's input."""
+    if not ws or len(ws) > MAX_GROUPED:
+        raise ValueError(f"1 to {MAX_GROUPED} weights")
+    dev = _device(ws[0].q, "weight codes")
+    args = b"".join(_weight_args(w, dev) for w in ws)
+    k = ws[0].q.shape[1]
+    if any(w.q.shape[1] != k or w.scale.dtype != ws[0].scale.dtype for w in ws):
+        raise ValueError("the weights must share k and the type of their scales")
+    columns = sum(_blocks(w.q.shape[0]) for w in ws) * FP8_BLOCK
+    if columns > MAX_K:
+        raise ValueError(f"at most {MAX_K} rows of weights, each weight's rounded up to 128")
+    q = torch.empty((k, columns), dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty((_blocks(k), columns // FP8_BLOCK), dtype=ws[0].scale.dtype, device=dev)
+    _launch(lib().convrot_fp8_transpose_weights, "convrot_fp8_transpose_weights", dev, args, len(ws),
+            q.data_ptr(), scale.data_ptr())
+    return Fp8Weights(q, scale)
+
+
+def fp8_gated_backward(dy: torch.Tensor, kept, back: Fp8Weights, act: str = "silu"):
+    """The way back through ``fp8_gated``: (dX, (dG, dU)), all bfloat16.
+
+    dG = dY U act'(G) and dU = dY act(G) are the gradients at the two projections' outputs (what an
+    adapter beside them needs), and dX = dG gate + dU up the one at X.  The weights are fixed codes
+    and have none.
+
+    dy   : float32 or bfloat16 [m, n]
+    kept : (G, U) of ``fp8_gated`` with ``keep``
+    back : ``fp8_transpose_weights([gate, up])``
+    dG and dU go into the product for dX as FP8 activations do (E4M3, a scale for each 128 features of
+    a row), quantised from their float32 values.
+    """
+    code = _gated_act(act)
+    dev = _device(dy, "dy")
+    dt = _rows(dy, "dy")
+    m, n = dy.shape
+    if len(kept) != 2:
+        raise ValueError("kept must be the pair that fp8_gated returned")
+    for t in kept:
+        if not isinstance(t, torch.Tensor) or _rows(t, "a kept projection", dev, dy.shape) != BF16:
+            raise ValueError("the kept projections must be bfloat16")
+    if kept[0].stride() != kept[1].stride():
+        raise ValueError("the kept projections must share their strides")
+    np = _blocks(n) * FP8_BLOCK
+    _weight_args(back, dev)
+    if n < 1 or back.q.shape[1] != 2 * np:
+        raise ValueError("back must be fp8_transpose_weights([gate, up])")
+    packed = _new_activation(m, 2 * np, dev)
+    dgate, dup = (torch.empty((m, n), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    pk = _writable(_pack_args(packed))
+    _launch(lib().convrot_fp8_gated_backward, "convrot_fp8_gated_backward", dev,
+            _GATED_BACKWARD.pack(dy.data_ptr(), kept[0].data_ptr(), kept[1].data_ptr(), dgate.data_ptr(),
+                                 dup.data_ptr(), ctypes.addressof(pk), m, n, _row_stride(dy),
+                                 _row_stride(kept[0]), n, dt, code))
+    return fp8_linear(packed, back, out_dtype=torch.bfloat16), (dgate, dup)
 
 
 # ---------------------------------------------------------------------------

@@ -26,7 +26,8 @@ CEILING_LIB_PATH = os.path.join(PKG_DIR, "libconvrot_ceiling.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "pack.hip", "wprep.hip", "gemm.hip", "gemm_small.hip", "lora.hip",
-           "api_block.cpp", "fp8_pack.hip", "fp8_gemm.hip", "fp8_gemm_wide.hip", "fp8_gemm_rows.hip", "block_norm.hip", "rope.hip",
+           "api_block.cpp", "fp8_pack.hip", "fp8_gemm.hip", "fp8_gemm_wide.hip", "fp8_gemm_rows.hip", "fp8_gated.hip",
+           "block_norm.hip", "rope.hip",
            "group_norm.hip", "api_attention.cpp", "attention.hip"]
 CEILING_SOURCES = ["ceiling.hip"]
 

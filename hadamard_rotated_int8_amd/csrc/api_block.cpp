@@ -109,6 +109,31 @@ convrot_status check_fp8_linear(const convrot_fp8_weights* w, int32_t count, voi
   return tiles * ((a->m + 31) / 32) > int64_t(INT32_MAX) ? CONVROT_ERR_SHAPE : CONVROT_OK;
 }
 
+// The gated pair g on an activation whose m and k are filled in.
+convrot_status check_gated(const convrot_gated* g, convrot::Fp8GemmArgs* a) {
+  if (!g) return CONVROT_ERR_NULL;
+  const convrot_fp8_weights w[2] = {g->gate, g->up};
+  void* const y[2] = {g->y, g->y};
+  const int64_t ldy[2] = {g->ldy, g->ldy};
+  if (g->gate.n != g->up.n) return CONVROT_ERR_SHAPE;
+  const convrot_status st = check_fp8_linear(w, 2, y, ldy, g->y_dtype, CONVROT_ACT_NONE, a);
+  if (st != CONVROT_OK) return st;
+  if (g->act != CONVROT_ACT_SILU && g->act != CONVROT_ACT_GELU) return CONVROT_ERR_DTYPE;
+  if (!g->kept_gate != !g->kept_up) return CONVROT_ERR_NULL;
+  if (g->kept_gate) {
+    if (g->ldk < g->gate.n || g->ldk > kMaxStride) return CONVROT_ERR_SHAPE;
+    if (!aligned(g->kept_gate, 2) || !aligned(g->kept_up, 2) || g->kept_gate == g->kept_up ||
+        g->kept_gate == g->y || g->kept_up == g->y)
+      return CONVROT_ERR_UNSUPPORTED;
+  }
+  a->gated = true;
+  a->act = g->act == CONVROT_ACT_GELU ? convrot::kActGelu : convrot::kActSilu;
+  a->kept[0] = g->kept_gate;
+  a->kept[1] = g->kept_up;
+  a->ldk = g->ldk;
+  return CONVROT_OK;
+}
+
 convrot_status check_group_norm_sizes(const convrot_group_norm& g) {
   if (g.batch < 0 || g.positions < 0 || g.batch > kMaxRows || g.positions > kMaxRows || g.c < 1 ||
       g.c > CONVROT_MAX_GROUP_NORM_C || g.groups < 1 || g.c % g.groups != 0 ||
@@ -212,6 +237,125 @@ convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m
   if (!x) return CONVROT_ERR_NULL;
   if (!rows_at_16(x, m, ldx, x_dtype)) return CONVROT_ERR_UNSUPPORTED;
   return from_hip(convrot::launch_fp8_gemm_rows(a, static_cast<hipStream_t>(stream)));
+}
+
+convrot_status convrot_fp8_gated(const convrot_fp8_packed* x, const convrot_gated* g, void* stream) {
+  if (!x) return CONVROT_ERR_NULL;
+  convrot::Fp8GemmArgs a{};
+  a.qx = static_cast<const uint8_t*>(x->q);
+  a.sx = static_cast<const uint8_t*>(x->scale);
+  a.lds = x->lds;
+  a.m = x->m;
+  a.k = x->k;
+  convrot_status st = check_gated(g, &a);
+  if (st != CONVROT_OK) return st;
+  st = check_fp8_stride(x->lds, x->m);
+  if (st != CONVROT_OK) return st;
+  if (x->m == 0 || a.count == 0) return CONVROT_OK;
+  st = check_fp8_buffers(x);
+  if (st != CONVROT_OK) return st;
+  return from_hip(convrot::launch_fp8_gemm(a, static_cast<hipStream_t>(stream)));
+}
+
+convrot_status convrot_fp8_gated_rows(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t ldx,
+                                      const convrot_gated* g, void* stream) {
+  if (k < 1 || k > CONVROT_MAX_K || m > CONVROT_FP8_MAX_ROWS ||
+      (m > 0 && blocks(k) * 128 > CONVROT_FP8_MAX_ROWS_BYTES / m))
+    return CONVROT_ERR_SHAPE;
+  convrot::Fp8GemmArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.x_bf16 = x_dtype == CONVROT_BF16;
+  a.m = m;
+  a.k = k;
+  const convrot_status st = check_gated(g, &a);
+  if (st != CONVROT_OK) return st;
+  if (ldx < k || ldx > kMaxStride) return CONVROT_ERR_SHAPE;
+  if (!float_type(x_dtype)) return CONVROT_ERR_DTYPE;
+  if (m == 0 || a.count == 0) return CONVROT_OK;
+  if (!x) return CONVROT_ERR_NULL;
+  if (!rows_at_16(x, m, ldx, x_dtype)) return CONVROT_ERR_UNSUPPORTED;
+  return from_hip(convrot::launch_fp8_gemm_rows(a, static_cast<hipStream_t>(stream)));
+}
+
+convrot_status convrot_fp8_gated_backward(const convrot_gated_backward* b, void* stream) {
+  if (!b || !b->packed) return CONVROT_ERR_NULL;
+  if (b->m < 0 || b->m > kMaxRows || b->n < 1 || 2 * blocks(b->n) * CONVROT_FP8_BLOCK > CONVROT_MAX_K ||
+      b->lddy < b->n || b->ldk < b->n || b->ldd < b->n || b->lddy > kMaxStride || b->ldk > kMaxStride ||
+      b->ldd > kMaxStride)
+    return CONVROT_ERR_SHAPE;
+  if (!float_type(b->dy_dtype) || (b->act != CONVROT_ACT_SILU && b->act != CONVROT_ACT_GELU))
+    return CONVROT_ERR_DTYPE;
+  convrot_status st = check_fp8_stride(b->packed->lds, b->m);
+  if (st != CONVROT_OK) return st;
+  if (b->m > 0) {
+    if (!b->dy || !b->gate || !b->up || !b->dgate || !b->dup) return CONVROT_ERR_NULL;
+    if ((st = check_fp8_buffers(b->packed)) != CONVROT_OK) return st;
+    if (!aligned(b->dy, size_of(b->dy_dtype)) || !aligned(b->gate, 2) || !aligned(b->up, 2) ||
+        !aligned(b->dgate, 2) || !aligned(b->dup, 2) || b->dgate == b->dup)
+      return CONVROT_ERR_UNSUPPORTED;
+    for (const void* out : {b->dgate, b->dup})
+      if (out == b->dy || out == b->gate || out == b->up) return CONVROT_ERR_UNSUPPORTED;
+  }
+  b->packed->m = b->m;
+  b->packed->k = 2 * blocks(b->n) * CONVROT_FP8_BLOCK;
+  if (b->m == 0) return CONVROT_OK;
+  convrot::GatedBackArgs a{};
+  a.dy = b->dy;
+  a.gate = static_cast<const uint16_t*>(b->gate);
+  a.up = static_cast<const uint16_t*>(b->up);
+  a.dgate = static_cast<uint16_t*>(b->dgate);
+  a.dup = static_cast<uint16_t*>(b->dup);
+  a.q = static_cast<uint8_t*>(b->packed->q);
+  a.q_scale = static_cast<uint8_t*>(b->packed->scale);
+  a.m = b->m;
+  a.n = b->n;
+  a.lddy = b->lddy;
+  a.ldk = b->ldk;
+  a.ldd = b->ldd;
+  a.lds = b->packed->lds;
+  a.dy_bf16 = b->dy_dtype == CONVROT_BF16;
+  a.act = b->act == CONVROT_ACT_GELU ? convrot::kActGelu : convrot::kActSilu;
+  return from_hip(convrot::launch_gated_back(a, static_cast<hipStream_t>(stream)));
+}
+
+convrot_status convrot_fp8_transpose_weights(const convrot_fp8_weights* w, int32_t count, void* q_out,
+                                             void* scale_out, void* stream) {
+  if (!w) return CONVROT_ERR_NULL;
+  if (count < 1 || count > CONVROT_MAX_GROUPED) return CONVROT_ERR_SHAPE;
+  const convrot_status st = check_k(w[0].k);
+  if (st != CONVROT_OK) return st;
+  int64_t columns = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (w[i].k != w[0].k || w[i].n < 1 || w[i].n > CONVROT_MAX_K) return CONVROT_ERR_SHAPE;
+    if ((w[i].scale_dtype != CONVROT_F32 && w[i].scale_dtype != CONVROT_E8M0) ||
+        w[i].scale_dtype != w[0].scale_dtype)
+      return CONVROT_ERR_DTYPE;
+    if (!w[i].q || !w[i].scale) return CONVROT_ERR_NULL;
+    if (!aligned16(w[i].q) || (w[i].scale_dtype == CONVROT_F32 && !aligned(w[i].scale, 4)))
+      return CONVROT_ERR_UNSUPPORTED;
+    columns += blocks(w[i].n) * CONVROT_FP8_BLOCK;
+  }
+  if (columns > CONVROT_MAX_K) return CONVROT_ERR_SHAPE;
+  if (!q_out || !scale_out) return CONVROT_ERR_NULL;
+  const bool f32 = w[0].scale_dtype == CONVROT_F32;
+  if (!aligned16(q_out) || (f32 && !aligned(scale_out, 4))) return CONVROT_ERR_UNSUPPORTED;
+  int64_t at = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    convrot::Fp8TransposeArgs a{};
+    a.q = static_cast<const uint8_t*>(w[i].q);
+    a.scale = w[i].scale;
+    a.n = w[i].n;
+    a.k = w[i].k;
+    a.q_out = static_cast<uint8_t*>(q_out) + at;
+    a.scale_out = static_cast<uint8_t*>(scale_out) + at / CONVROT_FP8_BLOCK * (f32 ? 4 : 1);
+    a.ldq = columns;
+    a.f32_scale = f32;
+    const convrot_status st = from_hip(convrot::launch_fp8_transpose(a, static_cast<hipStream_t>(stream)));
+    if (st != CONVROT_OK) return st;
+    at += blocks(w[i].n) * CONVROT_FP8_BLOCK;
+  }
+  return CONVROT_OK;
 }
 
 convrot_status convrot_block_norm(const convrot_block* b, void* stream) {

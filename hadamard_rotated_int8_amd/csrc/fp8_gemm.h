@@ -26,6 +26,9 @@ struct Fp8Params {
   int nseg;
   int tiles_m, tiles_n;
   int y_bf16, gelu;
+  int act;        // of a gated pair (seg[0] the gate, seg[1] the up projection)
+  void* kept[2];  // ... and its projections as bfloat16, or nullptr
+  int64_t ldk;
   int first;  // tile of the launch's first workgroup
   struct Seg {
     const uint8_t* qw;
@@ -60,7 +63,8 @@ CR_DEVICE Fp8Tile fp8_tile(const Fp8Params& p, int t) {
   return {tm * BM, (tn - tn0) * BN, s};
 }
 
-// The kernel's parameters for BM x BN tiles.
+// The kernel's parameters for BM x BN tiles (of a gated pair: BN rows of W, half
+// of them the gate's, for BN / 2 columns of Y).
 template <int BM, int BN>
 inline Fp8Params fp8_params(const Fp8GemmArgs& a) {
   Fp8Params p{};
@@ -74,6 +78,17 @@ inline Fp8Params fp8_params(const Fp8GemmArgs& a) {
   p.y_bf16 = a.y_bf16;
   p.gelu = a.gelu;
   p.tiles_m = int((a.m + BM - 1) / BM);
+  if (a.gated) {
+    for (int i = 0; i < 2; ++i)
+      p.seg[i] = {a.w[i].q, a.w[i].scale, a.w[i].bias, a.w[0].y, a.w[0].ldy, int(a.w[0].n), 0};
+    p.nseg = 1;
+    p.tiles_n = int((a.w[0].n + BN / 2 - 1) / (BN / 2));
+    p.act = a.act;
+    p.kept[0] = a.kept[0];
+    p.kept[1] = a.kept[1];
+    p.ldk = a.ldk;
+    return p;
+  }
   for (int i = 0; i < a.count; ++i) {
     p.seg[i] = {a.w[i].q, a.w[i].scale, a.w[i].bias, a.w[i].y, a.w[i].ldy, int(a.w[i].n), p.tiles_n};
     p.tiles_n += int((a.w[i].n + BN - 1) / BN);
@@ -103,6 +118,33 @@ CR_DEVICE void store4(void* y, int64_t at, const float* v, int left, bool bf16, 
       for (int i = 0; i < 4; ++i)
         if (i < left) p[i] = v[i];
     }
+  }
+}
+
+// Where a gated pair's outputs go.
+struct GatedOut {
+  void *y, *gate, *up;  // (gate, up: nullptr where they are not kept)
+  int64_t ldy, ldk;
+  int n;
+  bool bf16, gelu;
+};
+CR_DEVICE GatedOut gated_out(const Fp8Params& p) {
+  return {p.seg[0].y, p.kept[0], p.kept[1], p.seg[0].ldy, p.ldk, p.seg[0].n, p.y_bf16 != 0, p.act == kActGelu};
+}
+
+// Four consecutive columns of an output row from the biased sums.
+CR_DEVICE void store_gated4(const GatedOut& o, int64_t m, int n, const float* g, const float* u) {
+  const int left = o.n - n;
+  auto vector = [&](const void* y, int64_t ld, unsigned bytes) {
+    return left >= 4 && (ld & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & (bytes - 1)) == 0;
+  };
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (o.gelu ? gelu_erf(g[e]) : silu(g[e])) * u[e];
+  store4(o.y, m * o.ldy + n, v, left, o.bf16, vector(o.y, o.ldy, o.bf16 ? 8 : 16));
+  if (o.gate) {
+    store4(o.gate, m * o.ldk + n, g, left, true, vector(o.gate, o.ldk, 8));
+    store4(o.up, m * o.ldk + n, u, left, true, vector(o.up, o.ldk, 8));
   }
 }
 

@@ -55,13 +55,21 @@ CR_DEVICE f32x16 mfma_bf16(const Bf16Frag& a, const Bf16Frag& b, f32x16 c) {
 // its own copy, so that all have the same number of loads to wait for); the
 // weights' scales of the whole tile are laid out in LDS as 32-bit values first.
 // EXACT: bfloat16 instructions (float32 outputs).
-template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT>
+//
+// GATED: of the BN rows of W in a tile every 32 are 16 of the gate's and the
+// same 16 of the up projection's.  A lane then holds both sums of 8 of its 16
+// columns of a 32 x 32 block, and the tile gives BN / 2 columns of
+// act(gate) * up.
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT, bool GATED>
 __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Params p) {
   constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN, WAVES = WM * WN;
   constexpr int XB = BM * kBK, WB = BN * kBK;
   constexpr int STAGE = XB + WB + WAVES * 256;  // + the rows' scales, a copy for each wave
   constexpr int PIECES = (XB + WB) / 1024;  // 1 KB: 8 rows
-  constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;  // weight scale rows of a tile
+  constexpr int OUTS = GATED ? BN / 2 : BN;  // columns of Y
+  // Weight scale rows of a tile (gated: the gate's, the up projection's).
+  constexpr int NBW = GATED ? 2 : BN > kFp8Block ? BN / kFp8Block : 1;
+  static_assert(!GATED || OUTS <= kFp8Block, "one scale row each");
   constexpr int LOADS = PIECES / WAVES + 1;  // of a wave and stage
   // The fragments come before the next loads, or after them where four waves
   // to a SIMD have others to hide behind: 333 x 4112 -> 4096 float32 (eight
@@ -81,13 +89,17 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
   uint8_t* ring = smem + group * STAGES * STAGE;
   const int wm = wave / WN, wn = wave % WN;
   const int K = p.K, kb = p.kb, kbp = kb + KG - 1;  // (the last turn's blocks)
-  const Fp8Tile tile = fp8_tile<BM, BN>(p, p.first + xcd_slot(blockIdx.x, gridDim.x));
-  const Fp8Params::Seg& sg = p.seg[tile.seg];
+  const Fp8Tile tile = fp8_tile<BM, OUTS>(p, p.first + xcd_slot(blockIdx.x, gridDim.x));
+  const Fp8Params::Seg& sg = p.seg[GATED ? 0 : tile.seg];
   const int m0 = tile.m0, n0 = tile.n0;
   const int rows = p.M - m0 < BM ? p.M - m0 : BM;
-  const int cols = sg.n - n0 < BN ? sg.n - n0 : BN;
+  const int cols = sg.n - n0 < OUTS ? sg.n - n0 : OUTS;
   const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(p.qx + (int64_t)m0 * K, rows * K);
-  const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(sg.qw + (int64_t)n0 * K, cols * K);
+  static_assert(!GATED || (XB / 1024 % 4 == 0 && (WAVES < 4 || WAVES % 4 == 0)), "whose a piece is");
+  const uint8_t* uw = GATED ? p.seg[1].qw : sg.qw;
+  const __amdgpu_buffer_rsrc_t ur = buffer_rsrc(uw + (int64_t)n0 * K, cols * K);
+  const __amdgpu_buffer_rsrc_t wr =
+      buffer_rsrc((GATED && WAVES >= 4 && (wave & 2) ? uw : sg.qw) + (int64_t)n0 * K, cols * K);
 
   // Past the last block everything is out of range: the loads keep their
   // number, for the waits.
@@ -95,16 +107,19 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
     uint8_t* st = ring + slot * STAGE;
     const int step = turn * KG + group;
     const int k0 = step * kBK;
-#pragma unroll
-    for (int i = 0; i < PIECES / WAVES; ++i) {
+    for_each_index(std::make_integer_sequence<int, PIECES / WAVES>{}, [&](auto i_t) {
+      constexpr int i = decltype(i_t)::value;
       const int q = wave + WAVES * i;
       const bool is_x = q < XB / 1024;
       const int row = (is_x ? q : q - XB / 1024) * 8 + lane / 8;
       const int kc = k0 + ((lane & 7) ^ swz(row)) * 16;
-      const unsigned off = kc < K ? unsigned(row * K + kc) : kOutOfRange;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? xr : wr, (lds_void*)(st + q * 1024), 16, off,
-                                               0, 0, 0);
-    }
+      const int from = GATED && !is_x ? (row >> 5) * 16 + (row & 15) : row;  // of the operand
+      const unsigned off = kc < K ? unsigned(from * K + kc) : kOutOfRange;
+      // (Pieces 4 n + 2 and 4 n + 3 are the up projection's: known here, or the same for all of a wave's.)
+      constexpr bool kUp = GATED && WAVES < 4 && ((WAVES * i) & 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? xr : kUp ? ur : wr, (lds_void*)(st + q * 1024), 16, off, 0, 0,
+                                               0);
+    });
     // (the scales' rows are padded to a multiple of 4)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         buffer_rsrc(p.sx + step * p.lds + m0, step < kb ? (rows + 3) & ~3 : 0),
@@ -117,14 +132,19 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
   {  // the tile's weight scales (rows past n, blocks past K: one) and bias
     const int first_row = n0 / kFp8Block, nrows = (sg.n + kFp8Block - 1) / kFp8Block;
     for (int i = threadIdx.x; i < NBW * kbp; i += KG * WAVES * 64) {
-      const int r = first_row + i / kbp, b = i % kbp;
+      const int r = first_row + (GATED ? 0 : i / kbp), b = i % kbp;
+      const void* sw = GATED && i >= kbp ? p.seg[1].sw : sg.sw;
       const int64_t at = (int64_t)r * kb + b;
       unsigned v = F32SCALE ? __float_as_uint(1.f) : 127u;
       if (r < nrows && b < kb)
-        v = F32SCALE ? static_cast<const unsigned*>(sg.sw)[at] : static_cast<const uint8_t*>(sg.sw)[at];
+        v = F32SCALE ? static_cast<const unsigned*>(sw)[at] : static_cast<const uint8_t*>(sw)[at];
       wscale[i] = v;
     }
-    for (int i = threadIdx.x; i < BN; i += KG * WAVES * 64) bias[i] = sg.bias && i < cols ? sg.bias[n0 + i] : 0.f;
+    for (int i = threadIdx.x; i < BN; i += KG * WAVES * 64) {
+      const int c = i % OUTS;
+      const float* b = GATED && i >= OUTS ? p.seg[1].bias : sg.bias;
+      bias[i] = b && c < cols ? b[n0 + c] : 0.f;
+    }
   }
 
   const int fr = lane & 31, fh = lane >> 5;
@@ -145,13 +165,19 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
     const uint8_t* st = ring + slot * STAGE;
     // All of the step's fragments are requested before the first is used.
     int sx[FM];
-    unsigned sw[FN];
+    unsigned sw[FN], su[FN];  // (su: the up projection's float32 scale)
     v8i xf[2][FM], wf[2][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i) sx[i] = st[XB + WB + wave * 256 + wm * FM * 32 + i * 32 + fr];
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      sw[j] = wscale[(wn * FN * 32 + j * 32) / kFp8Block * kbp + step];
+    for (int j = 0; j < FN; ++j) {
+      // Of a gated block the first operand's rows 16 .. 31, lanes like rows, are the up projection's.
+      sw[j] = wscale[(GATED ? (!F32SCALE && (lane & 16) ? 1 : 0) : (wn * FN * 32 + j * 32) / kFp8Block) * kbp + step];
+      if (GATED && F32SCALE) su[j] = wscale[kbp + step];
+    }
+    auto block_scale = [&](int j, int e) {  // float32, of element e of block j
+      return __uint_as_float(GATED && e >= 8 ? su[j] : sw[j]);
+    };
 #pragma unroll
     for (int t2 = 0; t2 < 2; ++t2) {
 #pragma unroll
@@ -193,7 +219,7 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
           for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              acc[i][j][e] = __builtin_fmaf(part[i][j][e], __uint_as_float(sw[j]), acc[i][j][e]);
+              acc[i][j][e] = __builtin_fmaf(part[i][j][e], block_scale(j, e), acc[i][j][e]);
       }
     } else {
 #pragma unroll
@@ -207,7 +233,7 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
             c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[t2][j], xf[t2][i], c, 0, 0, 0, s, 0, sx[i]);
           if constexpr (F32SCALE) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) c[e] = __builtin_fmaf(c[e], __uint_as_float(sw[j]), acc[i][j][e]);
+            for (int e = 0; e < 16; ++e) c[e] = __builtin_fmaf(c[e], block_scale(j, e), acc[i][j][e]);
           }
           acc[i][j] = c;
         }
@@ -245,41 +271,64 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
           }
   }
   // Register e of block (i, j): column 8 (e / 4) + 4 (lane / 32) + e % 4, row lane % 32.
+  const GatedOut out = gated_out(p);
   const int64_t ldy = sg.ldy;
   const bool vec = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(sg.y) & (p.y_bf16 ? 7 : 15)) == 0;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m = m0 + wm * FM * 32 + i * 32 + fr;
+    if constexpr (GATED) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + wn * FN * 32 + j * 32 + 8 * q + 4 * fh;
-        float v[4];
+        for (int q = 0; q < 2; ++q) {
+          const int c = (wn * FN + j) * 16 + 8 * q + 4 * fh, n = n0 + c;
+          float g[4], u[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[i][j][4 * q + e] + bias[n - n0 + e];
-          if (p.gelu) v[e] = gelu_erf(v[e]);
+          for (int e = 0; e < 4; ++e) {
+            g[e] = acc[i][j][4 * q + e] + bias[c + e];
+            u[e] = acc[i][j][8 + 4 * q + e] + bias[OUTS + c + e];
+          }
+          if (m < p.M && n < sg.n) store_gated4(out, m, n, g, u);
         }
-        if (m < p.M && n < sg.n)
-          store4(sg.y, (int64_t)m * ldy + n, v, sg.n - n, p.y_bf16, vec && sg.n - n >= 4);
-      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = n0 + wn * FN * 32 + j * 32 + 8 * q + 4 * fh;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = acc[i][j][4 * q + e] + bias[n - n0 + e];
+            if (p.gelu) v[e] = gelu_erf(v[e]);
+          }
+          if (m < p.M && n < sg.n)
+            store4(sg.y, (int64_t)m * ldy + n, v, sg.n - n, p.y_bf16, vec && sg.n - n >= 4);
+        }
+    }
   }
 }
 
-template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT>
-hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT, bool GATED>
+hipError_t launch_g(const Fp8GemmArgs& a, hipStream_t stream) {
   constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
-  constexpr int NBW = BN > kFp8Block ? BN / kFp8Block : 1;
+  constexpr int NBW = GATED ? 2 : BN > kFp8Block ? BN / kFp8Block : 1;
   Fp8Params p = fp8_params<BM, BN>(a);
   const size_t lds = KG * STAGES * ((BM + BN) * kBK + WM * WN * 256) + BN * 4 + size_t(NBW) * (p.kb + KG - 1) * 4;
   constexpr int kThreads = WM * WN * KG * 64;
   in_launches(int64_t(p.tiles_m) * p.tiles_n, kThreads, [&](int64_t first, unsigned count) {
     p.first = int(first);
-    hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT>), dim3(count), dim3(kThreads),
-                       lds, stream, p);
+    hipLaunchKernelGGL((fp8_gemm_kernel<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, GATED>), dim3(count),
+                       dim3(kThreads), lds, stream, p);
   });
   return hipGetLastError();
+}
+
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT>
+hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
+  return a.gated ? launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, true>(a, stream)
+                 : launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, false>(a, stream);
 }
 
 template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool EXACT>
@@ -297,7 +346,7 @@ hipError_t launch_modes(const Fp8GemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
-  if (fp8_wide_wanted(a)) return launch_fp8_gemm_wide(a, stream);
+  if (fp8_wide_wanted(a)) return a.gated ? launch_fp8_gated_wide(a, stream) : launch_fp8_gemm_wide(a, stream);
   // What bounds few tiles is the latency of a step's loads, barrier and
   // fragments, some 0.3 us however little they bring, and that a CU has only
   // so many loads under way: so tiles as small as the CUs still take one of
@@ -325,8 +374,9 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   // (Eight groups need a stage less, which costs more than they gain where
   // the products are quick, with bfloat16 outputs.)
   auto tiles = [&](int64_t bm, int64_t bn) {
-    int64_t t = 0;
+    int64_t t = 0;  // (a gated pair's columns of W come 16 and 16)
     for (int i = 0; i < a.count; ++i) t += (a.w[i].n + bn - 1) / bn;
+    if (a.gated) t = (a.w[0].n + bn / 2 - 1) / (bn / 2);
     return t * ((a.m + bm - 1) / bm);
   };
   const int64_t cus = device_cu_count();

@@ -49,11 +49,13 @@ CR_DEVICE void load16(float* v, const void* x, bool bf16, int64_t at) {
   }
 }
 
-// NT: 16-row groups of W.
-template <int NT, bool F32SCALE, bool EXACT>
+// NT: 16-row groups of W.  GATED: of two, one of the gate's and one of the up
+// projection's, for 16 columns of act(gate) * up.
+template <int NT, bool F32SCALE, bool EXACT, bool GATED>
 __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Params p, const void* x, int64_t ldx,
                                                                   bool x_bf16) {
-  constexpr int kRows = 16 * NT;
+  static_assert(!GATED || NT == 2, "a pair");
+  constexpr int kRows = GATED ? 16 : 16 * NT;  // columns of Y
   __shared__ float part[kWaves][NT][64][4];
   __shared__ __attribute__((aligned(16))) uint8_t xlds[kFp8RawBytes];  // codes [M][128 kb]
   __shared__ uint8_t slds[kFp8RawBytes / kBK];                         // scales [M][kb]
@@ -63,12 +65,13 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
   const int K = p.K, kb = p.kb;
   const int tile = p.first + int(blockIdx.x);
   int s = 0;
-  for (int i = 1; i < p.nseg; ++i)
+  for (int i = 1; !GATED && i < p.nseg; ++i)
     if (tile >= p.seg[i].tn0) s = i;
   const Fp8Params::Seg& sg = p.seg[s];
   const int n0 = (tile - sg.tn0) * kRows;
   const int cols = sg.n - n0 < kRows ? sg.n - n0 : kRows;
   const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(sg.qw + (int64_t)n0 * K, cols * K);
+  const __amdgpu_buffer_rsrc_t ur = GATED ? buffer_rsrc(p.seg[1].qw + (int64_t)n0 * K, cols * K) : wr;
 
   // Lane l: row l % 16 of 16, features 16 g .. +15 and 64 + 16 g .. +15 of a
   // block, g = l / 16 (both operands alike).
@@ -84,7 +87,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
           const int f = (b0 + kWaves * u) * kBK + 64 * c + 16 * fg;
           w[u][t][c] = __builtin_bit_cast(
               v4i, __builtin_amdgcn_raw_buffer_load_b128(
-                       wr, f < K ? unsigned((16 * t + fr) * K + f) : kOutOfRange, 0, 0));
+                       GATED && t == 1 ? ur : wr,
+                       f < K ? unsigned((GATED ? fr : 16 * t + fr) * K + f) : kOutOfRange, 0, 0));
         }
   };
   load_w(wave);
@@ -135,12 +139,15 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
       const int64_t at = (int64_t)(n0 / kFp8Block) * kb + b;
       float sf = 1.f;
       int se = 127;
-      if constexpr (F32SCALE)
-        sf = static_cast<const float*>(sg.sw)[at];
-      else
-        se = static_cast<const uint8_t*>(sg.sw)[at];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
+        if (j == 0 || GATED) {
+          const void* sw = j == 0 ? sg.sw : p.seg[1].sw;
+          if constexpr (F32SCALE)
+            sf = static_cast<const float*>(sw)[at];
+          else
+            se = static_cast<const uint8_t*>(sw)[at];
+        }
         const v4i* q = w[u][j];
         const v8i wq = {q[0][0], q[0][1], q[0][2], q[0][3], q[1][0], q[1][1], q[1][2], q[1][3]};
         if constexpr (EXACT) {
@@ -168,6 +175,23 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
   for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4*>(part[wave][j][lane]) = acc[j];
   __syncthreads();
   // Element e of lane l in group j: column 16 j + 4 (l / 16) + e, row l % 16.
+  if constexpr (GATED) {
+    const int n = n0 + 4 * fg, row = fr;
+    if (wave == 0 && row < p.M && n < sg.n) {
+      float v[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f32x4 sum = *reinterpret_cast<const f32x4*>(part[0][j][lane]);
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) sum += *reinterpret_cast<const f32x4*>(part[i][j][lane]);
+        const float* bias = p.seg[j].bias;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][e] = sum[e] + (bias && n + e < sg.n ? bias[n + e] : 0.f);
+      }
+      store_gated4(gated_out(p), row, n, v[0], v[1]);
+    }
+    return;
+  }
   if (wave < NT) {
     f32x4 v = *reinterpret_cast<const f32x4*>(part[0][wave][lane]);
 #pragma unroll
@@ -187,13 +211,13 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
   }
 }
 
-template <int NT>
+template <int NT, bool GATED>
 void launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
   Fp8Params p = fp8_params<16, 16 * NT>(a);
   auto go = [&](auto f32, auto exact) {
     in_launches(p.tiles_n, kWaves * 64, [&](int64_t first, unsigned count) {
       p.first = int(first);
-      hipLaunchKernelGGL((fp8_rows_kernel<NT, decltype(f32)::value, decltype(exact)::value>), dim3(count),
+      hipLaunchKernelGGL((fp8_rows_kernel<NT, decltype(f32)::value, decltype(exact)::value, GATED>), dim3(count),
                          dim3(kWaves * 64), 0, stream, p, a.x, a.ldx, a.x_bf16);
     });
   };
@@ -211,10 +235,12 @@ void launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
 hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs& a, hipStream_t stream) {
   int64_t groups = 0;
   for (int i = 0; i < a.count; ++i) groups += (a.w[i].n + 31) / 32;
-  if (groups < device_cu_count())
-    launch_t<1>(a, stream);
+  if (a.gated)
+    launch_t<2, true>(a, stream);
+  else if (groups < device_cu_count())
+    launch_t<1, false>(a, stream);
   else
-    launch_t<2>(a, stream);
+    launch_t<2, false>(a, stream);
   return hipGetLastError();
 }
 

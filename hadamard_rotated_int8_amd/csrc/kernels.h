@@ -106,7 +106,13 @@ struct Fp8GemmArgs {
   int count;
   Fp8Weight w[kMaxGemmGroup];
   bool f32_scale, y_bf16, gelu;
+  // Gated: w[0] is the gate (with y), w[1] the up projection, act one of kAct*.
+  bool gated;
+  int act;
+  void* kept[2];  // both projections as bfloat16 [m, ldk], or nullptr
+  int64_t ldk;
 };
+constexpr int kActGelu = 1, kActSilu = 2;
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream);
 // A few rows of X itself (fp8_gemm_rows.hip).
 constexpr int kFp8RawBytes = 49152;  // codes of an unpacked X (at most 16 rows of whole blocks)
@@ -114,6 +120,30 @@ hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs& a, hipStream_t stream);
 // Outputs with many tiles of 256 x 256 (fp8_gemm_wide.hip).
 bool fp8_wide_wanted(const Fp8GemmArgs& a);
 hipError_t launch_fp8_gemm_wide(const Fp8GemmArgs& a, hipStream_t stream);
+hipError_t launch_fp8_gated_wide(const Fp8GemmArgs& a, hipStream_t stream);  // (fp8_gated.hip)
+// A gated pair's way back and the transposed weights it takes (fp8_gated.hip).
+struct GatedBackArgs {
+  const void* dy;
+  const uint16_t *gate, *up;  // the kept projections
+  uint16_t *dgate, *dup;
+  uint8_t *q, *q_scale;  // both gradients packed: [m, 2 * (n rounded up to 128)]
+  int64_t m, n, lddy, ldk, ldd, lds;
+  bool dy_bf16;
+  int act;
+};
+hipError_t launch_gated_back(const GatedBackArgs& a, hipStream_t stream);
+// q_out [k, ldq] = q^T, zeros up to the next multiple of 128 columns, and its
+// blocks' scales [ceil(k / 128), ldq / 128].
+struct Fp8TransposeArgs {
+  const uint8_t* q;
+  const void* scale;
+  int64_t n, k;
+  uint8_t* q_out;
+  void* scale_out;
+  int64_t ldq;
+  bool f32_scale;
+};
+hipError_t launch_fp8_transpose(const Fp8TransposeArgs& a, hipStream_t stream);
 
 // The norms around a block (block_norm.hip).
 constexpr int64_t kMaxNormK = 32768;

@@ -73,7 +73,8 @@ typedef enum convrot_dtype {
 
 typedef enum convrot_act {
   CONVROT_ACT_NONE = 0,
-  CONVROT_ACT_GELU = 1            /* x * Phi(x), erf form; not on the page, used by DiT MLPs */
+  CONVROT_ACT_GELU = 1,           /* x * Phi(x), erf form; not on the page, used by DiT MLPs */
+  CONVROT_ACT_SILU = 2            /* x / (1 + exp(-x)); of gated projections only */
 } convrot_act;
 
 /*
@@ -366,6 +367,72 @@ convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m
                                        int64_t ldx, const convrot_fp8_weights* w, int32_t count,
                                        void* const* y, const int64_t* ldy, int32_t y_dtype,
                                        int32_t act, void* stream);
+
+/*
+ * A gated pair of projections on FP8 weights, in one kernel:
+ *   Y = act(G) * U,   G = X Wg^T + bg,   U = X Wu^T + bu
+ * with the sums of convrot_fp8_linear_grouped, and act and the product taken
+ * of the unrounded G and U.
+ *   gate, up  : [n, k] each, of one scale_dtype
+ *   y         : device [m, n] of y_dtype (CONVROT_F32 or CONVROT_BF16), row stride ldy >= n
+ *   act       : CONVROT_ACT_SILU or CONVROT_ACT_GELU
+ *   kept_gate, kept_up : device bfloat16 [m, n], row stride ldk >= n, for G and U,
+ *               which convrot_fp8_gated_backward takes; both or neither (NULL)
+ * Outputs must not overlap one another or any input.
+ */
+typedef struct convrot_gated {
+  convrot_fp8_weights gate, up;
+  void* y;
+  int64_t ldy;
+  int32_t y_dtype, act;
+  void *kept_gate, *kept_up;
+  int64_t ldk;
+} convrot_gated;
+
+/* On a packed activation.  Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP. */
+convrot_status convrot_fp8_gated(const convrot_fp8_packed* x, const convrot_gated* g, void* stream);
+
+/* On a few rows of X itself, as convrot_fp8_linear_rows.  Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP. */
+convrot_status convrot_fp8_gated_rows(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t ldx,
+                                      const convrot_gated* g, void* stream);
+
+/*
+ * The gradients at the projections of a gated pair,
+ *   dG = dY * U * act'(G),   dU = dY * act(G)
+ * from the kept bfloat16 G and U, in float32: as bfloat16, and (from the
+ * unrounded values) as one FP8 activation [m, 2 np], np = n rounded up to 128:
+ * dG in features 0 .., dU in features np .., zeros between.  The gradient at X
+ * is a linear of that activation on convrot_fp8_transpose_weights(gate, up).
+ * (Weights are fixed codes: they have no gradient.)
+ *   dy       : device [m, n] of dy_dtype (CONVROT_F32 or CONVROT_BF16), row stride lddy >= n
+ *   gate, up : device bfloat16 [m, n], row stride ldk >= n
+ *   dgate, dup : device bfloat16 [m, n], row stride ldd >= n
+ *   packed   : q, scale and lds are the caller's; the call sets m and k
+ * Pointers need their element's alignment only; 2 np <= CONVROT_MAX_K.
+ * Outputs must not overlap one another or any input.
+ * Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP.
+ */
+typedef struct convrot_gated_backward {
+  const void* dy;
+  const void *gate, *up;
+  void *dgate, *dup;
+  convrot_fp8_packed* packed;
+  int64_t m, n;
+  int64_t lddy, ldk, ldd;
+  int32_t dy_dtype, act;
+} convrot_gated_backward;
+convrot_status convrot_fp8_gated_backward(const convrot_gated_backward* b, void* stream);
+
+/*
+ * The transposes of several weights [n_i, k] side by side, as one weight of k
+ * rows and sum of np_i columns (np_i: n_i rounded up to 128, zeros behind
+ * n_i): codes and scales as they are, since a block is square.  Offline.
+ *   q_out     : device E4M3 [k, sum np_i], 16-byte aligned, sum np_i <= CONVROT_MAX_K
+ *   scale_out : device [ceil(k / 128), sum np_i / 128] of the weights' scale_dtype
+ * Errors: NULL, SHAPE, DTYPE, UNSUPPORTED, HIP.
+ */
+convrot_status convrot_fp8_transpose_weights(const convrot_fp8_weights* w, int32_t count, void* q_out,
+                                             void* scale_out, void* stream);
 
 /*
  * ---------------------------------------------------------------------------
