@@ -12,7 +12,7 @@ import torch
 from . import lib
 from .block import _device, _launch, _no_overlap, _span, _workspace
 
-MAX_HEAD_DIM = 256
+MAX_HEAD_DIM = 192
 
 _ATTENTION = struct.Struct("=4Q12q3q3ifQQqQq")
 
@@ -29,7 +29,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | 
     lengths : int32 [batch]: a batch entry's keys from there on are hidden
     mask    : bool [batch, l] or [l]: the keys that are seen
     out     : where the result goes, in memory of its own; by default a new contiguous tensor
-    d is a multiple of 8 up to 256.  Any strides but 1 along d that are multiples of 8, 16-byte
+    d is a multiple of 8 up to 192.  Any strides but 1 along d that are multiples of 8, 16-byte
     aligned (column ranges of a projection's rows, expanded batches).  Returns bfloat16 in q's
     shape; a query that sees no key gives zeros.  Hidden keys and values may hold anything.
     """

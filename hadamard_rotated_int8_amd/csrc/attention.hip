@@ -20,10 +20,13 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
 constexpr int kKeys = 64;  // keys of a tile
 constexpr int kWaves = 4;
 constexpr float kLog2e = 1.44269504f;
+constexpr float kSlack = 8.f;  // powers of two that a weight may exceed 1 by
 constexpr float kMinusInf = -__builtin_inff();
 
 // The 16-byte chunk c of row r of a tile lies at slot c ^ swizzle(r).  A
@@ -39,21 +42,63 @@ CR_DEVICE int value_swizzle(int row) {
   return kPitch == 128 ? (row & 2) << 1 : (row & 3) << 2;
 }
 
+// 16 bytes for each lane from `base` + place + soff to LDS, lane by lane from
+// `to` on; zeros where place lies outside the first `bytes`.  As inline
+// assembly, since the compiler drains every direct-to-LDS load that it knows
+// of before it lets a transposing read pass, and the loads for later tiles are
+// to stay in flight.  It has no register to write; the waits that its data
+// need are waitvm's, before a barrier.  (Nothing else in these kernels uses m0.)
+CR_DEVICE void load_to_lds(const void* base, unsigned bytes, unsigned place, int soff, unsigned to) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const u32x4 resource = {unsigned(at), unsigned(at >> 32) & 0xFFFFu, bytes, unsigned(kBufferWord3)};
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(to), "v"(place), "s"(resource), "s"(soff)
+               : "memory");
+}
+
 CR_DEVICE float other_half(float v) {  // lane ^ 32
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// Words of a batch entry's keys that take part, from its length and mask, one
+// bit for each, for the main kernel's scalar loads.
+__global__ __launch_bounds__(256) void attention_bits_kernel(const AttentionArgs p, int64_t words) {
+  const int64_t w = (p.first + blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (w >= words * p.batch) return;
+  const int64_t batch = w / words, at = (w - batch * words) * kKeys + (threadIdx.x & 63);
+  const bool seen = at < p.l && p.mask[batch * p.mask_stride + at] != 0;
+  const uint64_t bits = __ballot(seen);
+  if ((threadIdx.x & 63) == 0) p.bits[w] = bits;
+}
+
 // D: the head's features rounded up to 32.  QB: blocks of 32 queries of a wave.
+//
+// One wave to a SIMD: what hides the softmax is the wave's own matrix
+// instructions.  Keys go in blocks of 32; step t multiplies Q with block t + 1
+// and the weights of block t - 1 with its values, QB D / 8 instructions of 32
+// cycles, and turns the scores of block t into weights between them.  The
+// products with K come first, so that the maximum of block t + 1 is known at
+// the end of the step.
+//
+// The weights are powers of two relative to a base that follows the maximum
+// only when that has risen by more than kSlack powers of two, which no other
+// block after the first few does: float32 sums and bfloat16 weights have the
+// same relative precision at 256 as at 1.
 template <int D, int QB>
-__global__ __launch_bounds__(kWaves * 64) void attention_kernel(const AttentionArgs p) {
+__global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void attention_kernel(const AttentionArgs p) {
   constexpr int kPitch = D <= 64 ? 128 : D <= 128 ? 256 : 512;  // bytes of a row in LDS
   constexpr int kChunks = kPitch / 16;
   constexpr int kRowsPiece = 1024 / kPitch;   // rows that one load instruction of a wave brings
   constexpr int kTile = kKeys * kPitch;       // bytes of K, or of V
   constexpr int kPieces = kTile / 1024 / kWaves;
   constexpr int kRows = kWaves * QB * 32;     // queries of a workgroup
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * kTile];
+  constexpr int kRing = kPitch == 128 ? 3 : 2;  // tiles of K and V in LDS
+  constexpr int KF = D / 16, NF = D / 32;     // fragments of 32 keys of K; blocks of 32 features of V
+  constexpr int kHalf = KF * QB;              // matrix instructions of each product of a step
+  constexpr int kAhead = 4;                   // fragments read ahead
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * 2 * kTile];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, fh = lane >> 5;
@@ -76,147 +121,304 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(const AttentionA
   const int first = int(all * split / p.splits), last = int(all * (split + 1) / p.splits);
   const uint16_t* kbase = p.k + batch * p.ks[0] + head * p.ks[2];
   const uint16_t* vbase = p.v + batch * p.vs[0] + head * p.vs[2];
-  const uint8_t* mask = p.mask ? p.mask + batch * p.mask_stride : nullptr;
   const int dbytes = p.d * 2;
+  typedef const __attribute__((address_space(4))) uint64_t* const_words;
+  const const_words words = (const_words)(p.bits + batch * ((p.l + kKeys - 1) / kKeys));
 
-  // The keys of tile t that take part, one bit for each.
-  auto tile_mask = [&](int t) -> uint64_t {
+  // The keys of tile t that take part, one bit for each; none behind the last.
+  auto tile_bits = [&](int t) -> uint64_t {
     const int64_t left = keys - int64_t(t) * kKeys;
-    if (left <= 0) return 0;
-    if (!mask) return left >= kKeys ? ~uint64_t(0) : (uint64_t(1) << left) - 1;
-    return __ballot(lane < left && mask[int64_t(t) * kKeys + lane] != 0);
+    uint64_t bits = t >= last || left <= 0 ? 0 : left >= kKeys ? ~uint64_t(0) : (uint64_t(1) << left) - 1;
+    if (p.mask && t < last) bits &= words[t];
+    return bits;
   };
-  // Rows of K and V of tile t into LDS area `to`; absent keys and features
-  // read as zero (a NaN of a hidden V must not meet a weight of zero).
-  auto issue = [&](int t, int to, uint64_t seen) {
-    const __amdgpu_buffer_rsrc_t kr = buffer_rsrc(kbase + int64_t(t) * kKeys * p.ks[1], 0x7FFFFFFF);
-    const __amdgpu_buffer_rsrc_t vr = buffer_rsrc(vbase + int64_t(t) * kKeys * p.vs[1], 0x7FFFFFFF);
+  // Rows of K (of tile t) and V (of the tile before) into LDS area `to`; hidden
+  // and absent ones read as zero: a score is then what its accumulator starts
+  // from, and a NaN of a hidden value does not meet its weight of zero.  Piece i is 4 i pieces' rows behind
+  // the wave's first; with 512-byte rows that is 8, and K's chunks change places.
+  constexpr int kStep = kWaves * kRowsPiece;
+  constexpr int kPlaces = kPitch == 512 ? 2 : 1;
+  const int prow = wave * kRowsPiece + lane / kChunks;
+  unsigned kplace[kPlaces], vplace;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int q = wave + kWaves * i;
-      const int row = q * kRowsPiece + lane / kChunks, at = lane % kChunks;
-      const bool in = (seen >> row) & 1;
-      const int kc = (at ^ key_swizzle<kPitch>(row)) * 16, vc = (at ^ value_swizzle<kPitch>(row)) * 16;
-      uint8_t* dst = smem + to * 2 * kTile + q * 1024;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(kr, (lds_void*)dst, 16,
-                                               in && kc < dbytes ? unsigned(row * int(p.ks[1]) * 2 + kc) : kOutOfRange,
-                                               0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_void*)(dst + kTile), 16,
-                                               in && vc < dbytes ? unsigned(row * int(p.vs[1]) * 2 + vc) : kOutOfRange,
-                                               0, 0, 0);
-    }
+  for (int i = 0; i < kPlaces; ++i) {
+    const int c = (lane % kChunks ^ key_swizzle<kPitch>(prow + i * kStep)) * 16;
+    kplace[i] = c < dbytes ? unsigned(prow * int(p.ks[1]) * 2 + c) : kOutOfRange;
+  }
+  {
+    const int c = (lane % kChunks ^ value_swizzle<kPitch>(prow)) * 16;
+    vplace = c < dbytes ? unsigned(prow * int(p.vs[1]) * 2 + c) : kOutOfRange;
+  }
+  auto issue = [&](int t, int to) __attribute__((always_inline)) {
+    auto rows = [&](const uint16_t* base, int64_t stride, int u, const unsigned* place, int places, unsigned dst)
+                    __attribute__((always_inline)) {
+      const uint64_t seen = u < first ? 0 : tile_bits(u);
+      const unsigned bytes = seen ? (kKeys - 1) * unsigned(stride) * 2 + dbytes : 0;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        unsigned at = place[i % places];
+        if (seen != ~uint64_t(0)) at = (seen >> (prow + i * kStep)) & 1 ? at : kOutOfRange;
+        load_to_lds(base + int64_t(u) * kKeys * stride, bytes, at, i * kStep * int(stride) * 2,
+                    dst + i * kWaves * 1024);
+      }
+    };
+    const unsigned dst = unsigned(reinterpret_cast<uintptr_t>((lds_byte*)smem)) + to * 2 * kTile + wave * 1024;
+    rows(kbase, p.ks[1], t, kplace, kPlaces, dst);
+    rows(vbase, p.vs[1], t - 1, &vplace, 1, dst + kTile);
   };
 
   // Q: lane l holds query l % 32, features 16 t + 8 (l / 32) .. +7.
-  bf16x8 qf[QB][D / 16];
+  bf16x8 qf[QB][KF];
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
     const int64_t r = row0 + 32 * b + fr;
-    const int64_t token = r / p.ratio, j = r - token * p.ratio;
+    const int64_t token = p.ratio == 1 ? r : int64_t(unsigned(r) / unsigned(p.ratio));
+    const int64_t j = r - token * p.ratio;
     const uint16_t* src = p.q + batch * p.qs[0] + token * p.qs[1] + (head * p.ratio + j) * p.qs[2];
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t) {
+    for (int t = 0; t < KF; ++t) {
       const int f = 16 * t + 8 * fh;
       qf[b][t] = r < rows && f < p.d ? *reinterpret_cast<const bf16x8*>(src + f) : bf16x8{};
     }
   }
 
-  f32x16 o[QB][D / 32] = {};
-  float top[QB], total[QB];
+  // Tile u's area holds K of tile u and V of tile u - 1: what the two steps
+  // before and at block 2 u read.
+  if (first < last) {
+#pragma unroll
+    for (int u = 0; u < kRing; ++u) issue(first + u, u);
+  }
+
+  const float c = p.scale * kLog2e, slack = kSlack / c;
+  f32x16 o[QB][NF] = {}, s[2][QB];
+  u32x4 pf[2][QB][2];
+  bf16x8 kf[kAhead], vf[kAhead];
+  float top[QB], total[QB], base[QB], shrink[QB];
+  bool rose = false;  // the base has moved: the output's sums follow a step later
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
     top[b] = kMinusInf;
-    total[b] = 0.f;
+    total[b] = base[b] = 0.f;
+    shrink[b] = 1.f;
   }
-  const float c = p.scale * kLog2e;
 
-  uint64_t seen = first < last ? tile_mask(first) : 0;
-  if (first < last) issue(first, 0, seen);
-  for (int t = first; t < last; ++t) {
-    const uint8_t* kt = smem + ((t - first) & 1) * 2 * kTile;
-    const uint8_t* vt = kt + kTile;
-    const uint64_t next = t + 1 < last ? tile_mask(t + 1) : 0;
-    waitvm<0>();  // this tile has landed, and every wave has read the one before it
-    barrier();
-    if (t + 1 < last) issue(t + 1, (t + 1 - first) & 1, next);
+  const int kat = fr * kPitch + ((fh ^ key_swizzle<kPitch>(fr)) << 4);
+  const int vrow = 4 * fh + ((lane & 15) >> 2);
+  const int vat = vrow * kPitch + (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<kPitch>(vrow)) << 4) +
+                  (lane & 1) * 8;
+  // Fragments of the area at `at`; `rows`: the first of 32 rows.
+  auto read_k = [&](int at, int row, int k) __attribute__((always_inline)) {
+    kf[k % kAhead] = *(const lds_bf16x8*)((const lds_byte*)smem + ((kat + at) ^ (k << 5)) + row * kPitch);
+  };
+  auto read_v = [&](int at, int row, int j) __attribute__((always_inline)) {  // block j % NF of keys 16 (j / NF) ..
+    i16x4 part[2];
 #pragma unroll
-    for (int g = 0; g < kKeys / 32; ++g) {
-      const unsigned bits = unsigned(seen >> (32 * g));
-      f32x16 s[QB] = {};
+    for (int i = 0; i < 2; ++i)
+      part[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_i16x4*)((lds_byte*)smem + ((vat + at) ^ ((j % NF) << 6)) + kTile + (row + 16 * (j / NF) + 8 * i) * kPitch));
+    vf[j % kAhead] = __builtin_bit_cast(bf16x8, i16x8{part[0][0], part[0][1], part[0][2], part[0][3], part[1][0],
+                                                      part[1][1], part[1][2], part[1][3]});
+  };
+  // Score e of block b to a weight.
+  auto weigh = [&](int x, int n) __attribute__((always_inline)) {
+    const int b = n / 16, e = n % 16;
+    s[x][b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][b][e], c, -base[b]));
+    if (e % 2) {
+      const bf16x2 w = {(__bf16)s[x][b][e - 1], (__bf16)s[x][b][e]};
+      const unsigned word = __builtin_bit_cast(unsigned, w);
+      asm volatile("" ::"v"(word));  // (formed here, not where the compiler would collect them)
+      pf[x][b][e / 8][e % 8 / 2] = word;
+      total[b] = __builtin_amdgcn_fdot2_f32_bf16(w, bf16x2{(__bf16)1.f, (__bf16)1.f}, total[b], false);
+    }
+  };
+  float most[QB];
+  // What the scores of a block start from: zero, minus infinity where the key is hidden.
+  // Register e: key 8 (e / 4) + 4 (lane / 32) + e % 4 of the 32.
+  f32x16 start = {};
+  unsigned starts = ~0u;
+  auto hide = [&](unsigned bits) __attribute__((always_inline)) {
+    if (bits != starts) {
+      starts = bits;
+      const unsigned hidden = ~bits >> (4 * fh);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int row = 32 * g + fr;
-        const bf16x8 kf =
-            *reinterpret_cast<const bf16x8*>(kt + row * kPitch + (((2 * k + fh) ^ key_swizzle<kPitch>(row)) << 4));
+      for (int e = 0; e < 16; ++e)
+        start[e] = __uint_as_float(unsigned(__builtin_amdgcn_sbfe(int(hidden), 8 * (e / 4) + e % 4, 1)) & 0xFF800000u);
+    }
+  };
+  // The maximum of a block, n-th part.
+  auto maximum = [&](int x, int n, int parts) __attribute__((always_inline)) {
+    const int lo = 16 * QB * n / parts, hi = 16 * QB * (n + 1) / parts;
+    for (int i = lo; i < hi; ++i) {
+      const int b = i / 16, e = i % 16;
+      most[b] = e == 0 ? s[x][b][0] : fmaxf(most[b], s[x][b][e]);
+    }
+  };
+  // Behind a block's maximum: its base.
+  auto settle = [&]() __attribute__((always_inline)) {
+    bool more = false;
 #pragma unroll
-        for (int b = 0; b < QB; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[b][k], s[b], 0, 0, 0);
-      }
-      bf16x8 pf[QB][2];
+    for (int b = 0; b < QB; ++b) {
+      most[b] = fmaxf(most[b], other_half(most[b]));
+      more |= most[b] > top[b] + slack;
+    }
+    rose = __ballot(more) != 0;
+    if (rose) {
 #pragma unroll
       for (int b = 0; b < QB; ++b) {
-        // Register e: key 8 (e / 4) + 4 (lane / 32) + e % 4 of the 32.
-        if (bits != ~0u) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (!((bits >> (8 * (e / 4) + 4 * fh + e % 4)) & 1)) s[b][e] = kMinusInf;
-        }
-        float most = s[b][0];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) most = fmaxf(most, s[b][e]);
-        most = fmaxf(most, other_half(most));
-        const float now = fmaxf(top[b], most);
-        const float base = now == kMinusInf ? 0.f : now;
-        const float shrink = __builtin_amdgcn_exp2f((top[b] - base) * c);
+        const float now = fmaxf(top[b], most[b]);
+        const float to = now == kMinusInf ? 0.f : now * c;
+        shrink[b] = __builtin_amdgcn_exp2f(__builtin_fmaf(top[b], c, -to));
         top[b] = now;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const __bf16 w = (__bf16)__builtin_amdgcn_exp2f((s[b][e] - base) * c);
-          pf[b][e / 8][e % 8] = w;
-          sum += float(w);
-        }
-        total[b] = total[b] * shrink + sum;
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n) o[b][n] *= shrink;
+        base[b] = to;
+        total[b] *= shrink[b];
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n) {
-          i16x4 part[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = 32 * g + 16 * h + 8 * i + 4 * fh + ((lane & 15) >> 2);
-            const int chunk = 4 * n + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-            part[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_i16x4*)(vt + row * kPitch + ((chunk ^ value_swizzle<kPitch>(row)) << 4) + (lane & 1) * 8));
-          }
-          const bf16x8 vf = __builtin_bit_cast(
-              bf16x8, i16x8{part[0][0], part[0][1], part[0][2], part[0][3], part[1][0], part[1][1], part[1][2],
-                            part[1][3]});
-#pragma unroll
-          for (int b = 0; b < QB; ++b) o[b][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[b][h], o[b][n], 0, 0, 0);
-        }
     }
-    seen = next;
+  };
+
+  // The step with the scores and weights of set X, on rows ROW .. of the area at `at`: the next
+  // block's K and the last one's values.  `middle` is called in every slot.
+  auto step = [&](auto x_t, auto pv_t, auto row_t, int at, unsigned bits,
+                  auto&& middle) __attribute__((always_inline)) {
+    constexpr int ROW = decltype(row_t)::value;
+    constexpr int X = decltype(x_t)::value, Y = 1 - X;
+    constexpr bool PV = decltype(pv_t)::value;
+    const bool follow = rose;
+    float by[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) by[b] = shrink[b];
+    hide(bits);
+    for_each_index(std::make_integer_sequence<int, 2 * kHalf>{}, [&](auto i_t) __attribute__((always_inline)) {
+      constexpr int i = decltype(i_t)::value;
+      constexpr int b = i % QB, f = i % kHalf / QB;  // the query block and fragment
+      if constexpr (i < kHalf) {
+        s[Y][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], f == 0 ? start : s[Y][b], 0, 0, 0);
+        if (b == QB - 1 && f + kAhead < KF) read_k(at, ROW, f + kAhead);
+        if (PV && b == QB - 1 && f >= KF - kAhead) read_v(at, ROW, f - (KF - kAhead));
+      } else {
+        if constexpr (PV) {
+          o[b][f % NF] =
+              __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[Y][b][f / NF]), o[b][f % NF], 0, 0, 0);
+          if (b == QB - 1 && f + kAhead < KF) read_v(at, ROW, f + kAhead);
+        }
+        if (i >= kHalf + 2) maximum(Y, i - kHalf - 2, kHalf - 2);
+      }
+      constexpr int lo = 16 * QB * i / (2 * kHalf), hi = 16 * QB * (i + 1) / (2 * kHalf);
+      for (int n = lo; n < hi; ++n) weigh(X, n);
+      middle(i_t);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    settle();
+    if (follow && PV) {
+#pragma unroll
+      for (int b = 0; b < QB; ++b)
+#pragma unroll
+        for (int n = 0; n < NF; ++n) o[b][n] *= by[b];
+    }
+  };
+
+  constexpr int kSync = 2 * kHalf - 2 * QB - 1;  // the slot, behind a step's last reads, where its area is given up
+  static_assert(kSync > kHalf, "slots");
+  // (opaque, so that addresses are formed where they are used and not kept for every area)
+  auto area = [&](int u) __attribute__((always_inline)) {
+    int at = (u - first) % kRing * 2 * kTile;
+    asm volatile("" : "+s"(at));
+    return at;
+  };
+  // K's first fragments of the next step, in the last slots of this one.
+  auto ahead = [&](auto i_t, int at, int row) __attribute__((always_inline)) {
+    constexpr int i = decltype(i_t)::value;
+    constexpr int slots = 2 * kHalf - 1 - kSync;
+    if constexpr (i > kSync) {
+#pragma unroll
+      for (int k = kAhead * (i - kSync - 1) / slots; k < kAhead * (i - kSync) / slots; ++k) read_k(at, row, k);
+    }
+  };
+  // The same where the next step's area is another one, which has landed once
+  // only the loads behind it may be in flight; every wave has read this one.
+  auto cross = [&](auto i_t, int u, int to) __attribute__((always_inline)) {
+    constexpr int i = decltype(i_t)::value;
+    if constexpr (i == kSync) {
+      wait_lgkm0();
+      waitvm<(kRing - 2) * 2 * kPieces>();
+      barrier();
+      issue(u + kRing, (u - first) % kRing);
+    }
+    ahead(i_t, to, 0);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I32 = std::integral_constant<int, 32>;
+
+  if (first < last) {
+    int at = area(first);
+    waitvm<(kRing - 1) * 2 * kPieces>();
+    barrier();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) read_k(at, 0, k);
+    uint64_t bits = tile_bits(first);
+    hide(unsigned(bits));
+#pragma unroll
+    for (int f = 0; f < KF; ++f) {
+#pragma unroll
+      for (int b = 0; b < QB; ++b)
+        s[0][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], f == 0 ? start : s[0][b], 0, 0, 0);
+      if (f + kAhead < KF) read_k(at, 0, f + kAhead);
+    }
+    maximum(0, 0, 1);
+    settle();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) read_k(at, 32, k);
+    int to = area(first + 1);
+    step(I0{}, No{}, I32{}, at, unsigned(bits >> 32),
+         [&](auto i_t) __attribute__((always_inline)) { cross(i_t, first, to); });
+    for (int u = first + 1; u < last; ++u) {
+      at = to;
+      to = area(u + 1);
+      bits = tile_bits(u);
+      step(I1{}, Yes{}, I0{}, at, unsigned(bits), [&](auto i_t) __attribute__((always_inline)) { ahead(i_t, at, 32); });
+      step(I0{}, Yes{}, I32{}, at, unsigned(bits >> 32),
+           [&](auto i_t) __attribute__((always_inline)) { cross(i_t, u, to); });
+    }
+    at = to;
+    step(I1{}, Yes{}, I0{}, at, 0u, [&](auto) __attribute__((always_inline)) {});
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) read_v(at, 32, j);
+#pragma unroll
+    for (int f = 0; f < KF; ++f) {
+#pragma unroll
+      for (int b = 0; b < QB; ++b)
+        o[b][f % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[1][b][f / NF]), o[b][f % NF], 0, 0, 0);
+      if (f + kAhead < KF) read_v(at, 32, f + kAhead);
+    }
+    waitvm<0>();  // no load into LDS may be in flight where the outputs go through it
+    wait_lgkm0();
+    barrier();
   }
 
   // Register e of block n: feature 32 n + 8 (e / 4) + 4 (lane / 32) + e % 4 of query lane % 32.
+  auto place = [&](int64_t r, int64_t* token, int* j) __attribute__((always_inline)) {
+    *token = p.ratio == 1 ? r : int64_t(unsigned(r) / unsigned(p.ratio));  // (rows are below 2^31)
+    *j = int(r - *token * p.ratio);
+  };
+  uint8_t* mine = smem + wave * QB * 32 * kPitch;
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
     const float sum = total[b] + other_half(total[b]);
-    const int64_t r = row0 + 32 * b + fr;
-    if (r >= rows) continue;
-    const int64_t token = r / p.ratio, j = r - token * p.ratio;
     if (p.splits > 1) {
+      const int64_t r = row0 + 32 * b + fr;
+      if (r >= rows) continue;
       const int64_t at = ((int64_t(split) * p.batch + batch) * p.kv_heads + head) * rows + r;
       float* dst = p.part + at * p.d;
       if (fh == 0) {
-        p.stats[2 * at] = top[b] * c;
+        p.stats[2 * at] = top[b] == kMinusInf ? kMinusInf : base[b];
         p.stats[2 * at + 1] = sum;
       }
 #pragma unroll
-      for (int n = 0; n < D / 32; ++n)
+      for (int n = 0; n < NF; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int f = 32 * n + 8 * q + 4 * fh;
@@ -224,20 +426,31 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(const AttentionA
             *reinterpret_cast<f32x4*>(dst + f) =
                 f32x4{o[b][n][4 * q], o[b][n][4 * q + 1], o[b][n][4 * q + 2], o[b][n][4 * q + 3]};
         }
-      continue;
-    }
-    uint16_t* dst = p.out + batch * p.os[0] + token * p.os[1] + (head * p.ratio + j) * p.os[2];
-    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    } else {
+      const float f = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int n = 0; n < D / 32; ++n)
+      for (int n = 0; n < NF; ++n)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = 32 * n + 8 * q + 4 * fh;
-        if (at < p.d)
-          *reinterpret_cast<u32x2*>(dst + at) =
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<u32x2*>(mine + (32 * b + fr) * kPitch + (((4 * n + q) ^ key_swizzle<kPitch>(fr)) << 4) +
+                                    8 * fh) =
               u32x2{bf16_pair(o[b][n][4 * q] * f, o[b][n][4 * q + 1] * f),
                     bf16_pair(o[b][n][4 * q + 2] * f, o[b][n][4 * q + 3] * f)};
-      }
+    }
+  }
+  if (p.splits > 1) return;
+  // Whole rows out of the wave's own part of LDS (whose accesses stay in order).
+#pragma unroll
+  for (int i = 0; i < QB * 32 / (64 / kChunks); ++i) {
+    const int row = i * (64 / kChunks) + lane / kChunks, chunk = lane % kChunks;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kPitch + ((chunk ^ key_swizzle<kPitch>(row & 31)) << 4));
+    const int64_t r = row0 + row;
+    if (r < rows && chunk * 16 < dbytes) {
+      int64_t token;
+      int j;
+      place(r, &token, &j);
+      *reinterpret_cast<u32x4*>(p.out + batch * p.os[0] + token * p.os[1] + (head * p.ratio + j) * p.os[2] + chunk * 8) = v;
+    }
   }
 }
 
@@ -269,6 +482,13 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
 template <int D, int QB>
 hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
   AttentionArgs p = a;
+  if (a.mask) {
+    const int64_t words = (a.l + kKeys - 1) / kKeys;
+    in_launches((words * a.batch + 3) / 4, 256, [&](int64_t first, unsigned count) {
+      p.first = first;
+      hipLaunchKernelGGL(attention_bits_kernel, dim3(count), dim3(256), 0, stream, p, words);
+    });
+  }
   in_launches(a.batch * a.kv_heads * a.tiles * a.splits, kWaves * 64, [&](int64_t first, unsigned count) {
     p.first = first;
     hipLaunchKernelGGL((attention_kernel<D, QB>), dim3(count), dim3(kWaves * 64), 0, stream, p);
@@ -285,9 +505,10 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
 }  // namespace
 
 AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d) {
-  constexpr int kTileRows = kWaves * 32;
   AttentionPlan plan{};
-  plan.tiles = (rows + kTileRows - 1) / kTileRows;
+  plan.blocks = 1;
+  const int tile_rows = kWaves * 32 * plan.blocks;
+  plan.tiles = (rows + tile_rows - 1) / tile_rows;
   plan.splits = 1;
   const int64_t blocks = batch * kv_heads * plan.tiles, cus = device_cu_count();
   const int64_t key_tiles = (l + kKeys - 1) / kKeys;
@@ -304,7 +525,7 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream) {
   if (a.d <= 96) return launch_t<96, 1>(a, stream);
   if (a.d <= 128) return launch_t<128, 1>(a, stream);
   if (a.d <= 160) return launch_t<160, 1>(a, stream);
-  return launch_t<256, 1>(a, stream);
+  return launch_t<192, 1>(a, stream);
 }
 
 }  // namespace convrot

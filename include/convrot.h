@@ -634,7 +634,7 @@ convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* strea
  * What a hidden key or its value holds does not matter (a NaN neither).
  * ---------------------------------------------------------------------------
  */
-#define CONVROT_MAX_HEAD_DIM 256
+#define CONVROT_MAX_HEAD_DIM 192
 
 /*
  *   q_stride .. out_stride : of batch, token and head, 0 .. 2^40; the tokens'
@@ -666,7 +666,8 @@ typedef struct convrot_attention {
 /*
  * The bytes of workspace that a call of these sizes needs on the current
  * device: few queries over many keys are worked on by several workgroups,
- * whose parts meet there.  Reads batch, m, l, heads, kv_heads and d only.
+ * whose parts meet there, and a mask is turned into bits.  Reads batch, m, l,
+ * heads, kv_heads, d and whether there is a mask.
  * Errors: NULL, SHAPE, UNSUPPORTED.
  */
 convrot_status convrot_attention_workspace(const convrot_attention* a, int64_t* bytes);

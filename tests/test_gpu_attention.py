@@ -28,7 +28,7 @@ def _check(q, k, v, out, **kw):
     assert not out.isnan().any() and worst <= 0, (worst, off.max().item())
 
 
-@pytest.mark.parametrize("d", [8, 16, 40, 64, 72, 80, 96, 104, 128, 136, 160, 168, 192, 256])
+@pytest.mark.parametrize("d", [8, 16, 40, 64, 72, 80, 96, 104, 128, 136, 160, 168, 192])
 @pytest.mark.parametrize("m, l", [(1, 1), (33, 65), (130, 129)])
 def test_head_dimensions(d, m, l):
     q, k, v = _inputs(2, m, l, 2, 2, d, seed=d)
