@@ -108,6 +108,7 @@ convrot_status convrot_attention_apply(const convrot_attention* a, void* stream)
   p.tiles = int(plan.tiles);
   p.splits = plan.splits;
   p.blocks = plan.blocks;
+  p.waves = plan.waves;
   p.bits = static_cast<uint64_t*>(a->workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + bits_bytes(*a));
   p.stats = p.part + int64_t(plan.splits) * a->batch * a->m * a->heads * a->d;

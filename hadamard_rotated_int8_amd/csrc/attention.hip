@@ -24,7 +24,6 @@ typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
 constexpr int kKeys = 64;  // keys of a tile
-constexpr int kWaves = 4;
 constexpr float kLog2e = 1.44269504f;
 constexpr float kSlack = 8.f;  // powers of two that a weight may exceed 1 by
 constexpr float kMinusInf = -__builtin_inff();
@@ -75,18 +74,18 @@ __global__ __launch_bounds__(256) void attention_bits_kernel(const AttentionArgs
 
 // D: the head's features rounded up to 32.  QB: blocks of 32 queries of a wave.
 //
-// One wave to a SIMD: what hides the softmax is the wave's own matrix
-// instructions.  Keys go in blocks of 32; step t multiplies Q with block t + 1
-// and the weights of block t - 1 with its values, QB D / 8 instructions of 32
-// cycles, and turns the scores of block t into weights between them.  The
-// products with K come first, so that the maximum of block t + 1 is known at
-// the end of the step.
+// Keys go in blocks of 32; step t multiplies Q with block t + 1 and the
+// weights of block t - 1 with its values, QB D / 8 instructions of 32 cycles,
+// one of each in turn, and turns the scores of block t into weights between
+// them.  K's and V's fragments are read 4 ahead, across steps.
 //
 // The weights are powers of two relative to a base that follows the maximum
 // only when that has risen by more than kSlack powers of two, which no other
 // block after the first few does: float32 sums and bfloat16 weights have the
-// same relative precision at 256 as at 1.
-template <int D, int QB>
+// same relative precision at 256 as at 1.  So a step takes the base as it is,
+// finds the maximum beside it, and if that has risen too far does its weights
+// again at the end.
+template <int D, int QB, int kWaves>
 __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void attention_kernel(const AttentionArgs p) {
   constexpr int kPitch = D <= 64 ? 128 : D <= 128 ? 256 : 512;  // bytes of a row in LDS
   constexpr int kChunks = kPitch / 16;
@@ -94,10 +93,10 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   constexpr int kTile = kKeys * kPitch;       // bytes of K, or of V
   constexpr int kPieces = kTile / 1024 / kWaves;
   constexpr int kRows = kWaves * QB * 32;     // queries of a workgroup
-  constexpr int kRing = kPitch == 128 ? 3 : 2;  // tiles of K and V in LDS
+  constexpr int kRing = kPitch == 512 ? 2 : kWaves == 8 ? 4 : kPitch == 128 ? 3 : 2;  // tiles of K and V in LDS
   constexpr int KF = D / 16, NF = D / 32;     // fragments of 32 keys of K; blocks of 32 features of V
   constexpr int kHalf = KF * QB;              // matrix instructions of each product of a step
-  constexpr int kAhead = 4;                   // fragments read ahead
+  constexpr int kAhead = KF % 4 == 0 ? 4 : KF / 2;  // fragments read ahead (the next step takes the same registers)
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * 2 * kTile];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -193,20 +192,18 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   f32x16 o[QB][NF] = {}, s[2][QB];
   u32x4 pf[2][QB][2];
   bf16x8 kf[kAhead], vf[kAhead];
-  float top[QB], total[QB], base[QB], shrink[QB];
-  bool rose = false;  // the base has moved: the output's sums follow a step later
+  float top[QB], total[QB], base[QB], limit[QB];
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
-    top[b] = kMinusInf;
+    top[b] = limit[b] = kMinusInf;
     total[b] = base[b] = 0.f;
-    shrink[b] = 1.f;
   }
 
   const int kat = fr * kPitch + ((fh ^ key_swizzle<kPitch>(fr)) << 4);
   const int vrow = 4 * fh + ((lane & 15) >> 2);
   const int vat = vrow * kPitch + (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<kPitch>(vrow)) << 4) +
                   (lane & 1) * 8;
-  // Fragments of the area at `at`; `rows`: the first of 32 rows.
+  // Fragments of the area at `at`; `row`: the first of 32 rows.
   auto read_k = [&](int at, int row, int k) __attribute__((always_inline)) {
     kf[k % kAhead] = *(const lds_bf16x8*)((const lds_byte*)smem + ((kat + at) ^ (k << 5)) + row * kPitch);
   };
@@ -219,19 +216,21 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
     vf[j % kAhead] = __builtin_bit_cast(bf16x8, i16x8{part[0][0], part[0][1], part[0][2], part[0][3], part[1][0],
                                                       part[1][1], part[1][2], part[1][3]});
   };
-  // Score e of block b to a weight.
+  float most[QB], sum[QB], held = 0.f;
+  // Score n of block t to a weight, two at a time.
   auto weigh = [&](int x, int n) __attribute__((always_inline)) {
     const int b = n / 16, e = n % 16;
-    s[x][b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][b][e], c, -base[b]));
-    if (e % 2) {
-      const bf16x2 w = {(__bf16)s[x][b][e - 1], (__bf16)s[x][b][e]};
-      const unsigned word = __builtin_bit_cast(unsigned, w);
+    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][b][e], c, -base[b]));
+    if (e % 2 == 0) {
+      held = w;
+    } else {
+      const bf16x2 both = {(__bf16)held, (__bf16)w};
+      const unsigned word = __builtin_bit_cast(unsigned, both);
       asm volatile("" ::"v"(word));  // (formed here, not where the compiler would collect them)
       pf[x][b][e / 8][e % 8 / 2] = word;
-      total[b] = __builtin_amdgcn_fdot2_f32_bf16(w, bf16x2{(__bf16)1.f, (__bf16)1.f}, total[b], false);
+      sum[b] = __builtin_amdgcn_fdot2_f32_bf16(both, bf16x2{(__bf16)1.f, (__bf16)1.f}, e == 1 ? 0.f : sum[b], false);
     }
   };
-  float most[QB];
   // What the scores of a block start from: zero, minus infinity where the key is hidden.
   // Register e: key 8 (e / 4) + 4 (lane / 32) + e % 4 of the 32.
   f32x16 start = {};
@@ -245,106 +244,98 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
         start[e] = __uint_as_float(unsigned(__builtin_amdgcn_sbfe(int(hidden), 8 * (e / 4) + e % 4, 1)) & 0xFF800000u);
     }
   };
-  // The maximum of a block, n-th part.
-  auto maximum = [&](int x, int n, int parts) __attribute__((always_inline)) {
-    const int lo = 16 * QB * n / parts, hi = 16 * QB * (n + 1) / parts;
-    for (int i = lo; i < hi; ++i) {
-      const int b = i / 16, e = i % 16;
-      most[b] = e == 0 ? s[x][b][0] : fmaxf(most[b], s[x][b][e]);
-    }
-  };
-  // Behind a block's maximum: its base.
-  auto settle = [&]() __attribute__((always_inline)) {
-    bool more = false;
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      most[b] = fmaxf(most[b], other_half(most[b]));
-      more |= most[b] > top[b] + slack;
-    }
-    rose = __ballot(more) != 0;
-    if (rose) {
-#pragma unroll
-      for (int b = 0; b < QB; ++b) {
-        const float now = fmaxf(top[b], most[b]);
-        const float to = now == kMinusInf ? 0.f : now * c;
-        shrink[b] = __builtin_amdgcn_exp2f(__builtin_fmaf(top[b], c, -to));
-        top[b] = now;
-        base[b] = to;
-        total[b] *= shrink[b];
-      }
-    }
+  // A block's maximum so far, with scores [n]; at the end over both halves of the wave.
+  auto maximum = [&](int x, int n) __attribute__((always_inline)) {
+    const int b = n / 16, e = n % 16;
+    most[b] = e == 0 ? s[x][b][0] : fmaxf(most[b], s[x][b][e]);
+    if (e == 15) most[b] = fmaxf(most[b], other_half(most[b]));
   };
 
-  // The step with the scores and weights of set X, on rows ROW .. of the area at `at`: the next
-  // block's K and the last one's values.  `middle` is called in every slot.
-  auto step = [&](auto x_t, auto pv_t, auto row_t, int at, unsigned bits,
-                  auto&& middle) __attribute__((always_inline)) {
-    constexpr int ROW = decltype(row_t)::value;
-    constexpr int X = decltype(x_t)::value, Y = 1 - X;
-    constexpr bool PV = decltype(pv_t)::value;
-    const bool follow = rose;
-    float by[QB];
-#pragma unroll
-    for (int b = 0; b < QB; ++b) by[b] = shrink[b];
+  // The step with the scores and weights of set X, on rows ROW .. of the area at
+  // `at`: the next block's K (`bits`: which of its keys are seen) and the last
+  // one's values; the next step's rows start at NROW of the area at `nat`.
+  // CROSS: that is another area, which has landed once only the loads behind
+  // it may be in flight, and this one, which every wave has then read, is
+  // given up to load(): at slot kSync, two behind the last reads.
+  constexpr int kSync = 2 * (KF - kAhead) * QB + 2;
+  auto step = [&](auto x_t, auto pv_t, auto row_t, auto cross_t, int at, int nat, unsigned bits,
+                  auto&& load) __attribute__((always_inline)) {
+    constexpr int X = decltype(x_t)::value, Y = 1 - X, ROW = decltype(row_t)::value, NROW = 32 - ROW;
+    constexpr bool PV = decltype(pv_t)::value, CROSS = decltype(cross_t)::value;
     hide(bits);
     for_each_index(std::make_integer_sequence<int, 2 * kHalf>{}, [&](auto i_t) __attribute__((always_inline)) {
       constexpr int i = decltype(i_t)::value;
-      constexpr int b = i % QB, f = i % kHalf / QB;  // the query block and fragment
-      if constexpr (i < kHalf) {
+      constexpr bool K = i % 2 == 0;
+      constexpr int b = i / 2 % QB, f = i / 2 / QB;  // the query block and fragment
+      if constexpr (K)
         s[Y][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], f == 0 ? start : s[Y][b], 0, 0, 0);
-        if (b == QB - 1 && f + kAhead < KF) read_k(at, ROW, f + kAhead);
-        if (PV && b == QB - 1 && f >= KF - kAhead) read_v(at, ROW, f - (KF - kAhead));
-      } else {
-        if constexpr (PV) {
-          o[b][f % NF] =
-              __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[Y][b][f / NF]), o[b][f % NF], 0, 0, 0);
-          if (b == QB - 1 && f + kAhead < KF) read_v(at, ROW, f + kAhead);
-        }
-        if (i >= kHalf + 2) maximum(Y, i - kHalf - 2, kHalf - 2);
+      else if constexpr (PV)
+        o[b][f % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[Y][b][f / NF]), o[b][f % NF], 0, 0, 0);
+      // The fragment 4 ahead, of this step's rows or the next one's.
+      if constexpr (b == QB - 1 && f + kAhead < KF) {
+        if constexpr (K)
+          read_k(at, ROW, f + kAhead);
+        else if constexpr (PV)
+          read_v(at, ROW, f + kAhead);
       }
+      if constexpr (CROSS && i == kSync) {
+        wait_lgkm0();
+        waitvm<(kRing - 2) * 2 * kPieces>();
+        barrier();
+        load();
+      }
+      auto next = [&](auto j_t) __attribute__((always_inline)) {  // what slot j frees the registers for
+        constexpr int j = decltype(j_t)::value, jf = j / 2 / QB + kAhead - KF;
+        if constexpr (j / 2 % QB == QB - 1 && jf >= 0) {
+          if constexpr (j % 2 == 0)
+            read_k(nat, NROW, jf);
+          else
+            read_v(nat, NROW, jf);
+        }
+      };
+      if constexpr (!CROSS || i > kSync) next(i_t);
+      if constexpr (CROSS && i == kSync)
+        for_each_index(std::make_integer_sequence<int, kSync + 1>{}, next);
       constexpr int lo = 16 * QB * i / (2 * kHalf), hi = 16 * QB * (i + 1) / (2 * kHalf);
+#pragma unroll
       for (int n = lo; n < hi; ++n) weigh(X, n);
-      middle(i_t);
+      // (the maximum within three quarters of the step)
+      constexpr int span = 3 * kHalf / 2;
+      constexpr int mlo = i < span ? 16 * QB * i / span : 16 * QB, mhi = i < span ? 16 * QB * (i + 1) / span : 16 * QB;
+#pragma unroll
+      for (int n = mlo; n < mhi; ++n) maximum(X, n);
       __builtin_amdgcn_sched_barrier(0);
     });
-    settle();
-    if (follow && PV) {
+    bool more = false;
 #pragma unroll
-      for (int b = 0; b < QB; ++b)
+    for (int b = 0; b < QB; ++b) more |= most[b] > limit[b];
+    if (__ballot(more) != 0) {
 #pragma unroll
-        for (int n = 0; n < NF; ++n) o[b][n] *= by[b];
+      for (int b = 0; b < QB; ++b) {
+        const float now = fmaxf(top[b], most[b]);
+        base[b] = now == kMinusInf ? 0.f : now * c;
+        const float shrink = __builtin_amdgcn_exp2f(__builtin_fmaf(top[b], c, -base[b]));
+        top[b] = now;
+        limit[b] = now + slack;
+        total[b] *= shrink;
+        if (PV) {
+#pragma unroll
+          for (int n = 0; n < NF; ++n) o[b][n] *= shrink;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 16 * QB; ++n) weigh(X, n);
     }
+#pragma unroll
+    for (int b = 0; b < QB; ++b) total[b] += sum[b];
   };
 
-  constexpr int kSync = 2 * kHalf - 2 * QB - 1;  // the slot, behind a step's last reads, where its area is given up
-  static_assert(kSync > kHalf, "slots");
   // (opaque, so that addresses are formed where they are used and not kept for every area)
   auto area = [&](int u) __attribute__((always_inline)) {
     int at = (u - first) % kRing * 2 * kTile;
     asm volatile("" : "+s"(at));
     return at;
-  };
-  // K's first fragments of the next step, in the last slots of this one.
-  auto ahead = [&](auto i_t, int at, int row) __attribute__((always_inline)) {
-    constexpr int i = decltype(i_t)::value;
-    constexpr int slots = 2 * kHalf - 1 - kSync;
-    if constexpr (i > kSync) {
-#pragma unroll
-      for (int k = kAhead * (i - kSync - 1) / slots; k < kAhead * (i - kSync) / slots; ++k) read_k(at, row, k);
-    }
-  };
-  // The same where the next step's area is another one, which has landed once
-  // only the loads behind it may be in flight; every wave has read this one.
-  auto cross = [&](auto i_t, int u, int to) __attribute__((always_inline)) {
-    constexpr int i = decltype(i_t)::value;
-    if constexpr (i == kSync) {
-      wait_lgkm0();
-      waitvm<(kRing - 2) * 2 * kPieces>();
-      barrier();
-      issue(u + kRing, (u - first) % kRing);
-    }
-    ahead(i_t, to, 0);
   };
   using Yes = std::true_type;
   using No = std::false_type;
@@ -353,7 +344,7 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   using I32 = std::integral_constant<int, 32>;
 
   if (first < last) {
-    int at = area(first);
+    int at = area(first), to = area(first + 1);
     waitvm<(kRing - 1) * 2 * kPieces>();
     barrier();
 #pragma unroll
@@ -365,34 +356,29 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
 #pragma unroll
       for (int b = 0; b < QB; ++b)
         s[0][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], f == 0 ? start : s[0][b], 0, 0, 0);
-      if (f + kAhead < KF) read_k(at, 0, f + kAhead);
+      if (f + kAhead < KF)
+        read_k(at, 0, f + kAhead);
+      else
+        read_k(at, 32, f + kAhead - KF);
     }
-    maximum(0, 0, 1);
-    settle();
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) read_k(at, 32, k);
-    int to = area(first + 1);
-    step(I0{}, No{}, I32{}, at, unsigned(bits >> 32),
-         [&](auto i_t) __attribute__((always_inline)) { cross(i_t, first, to); });
+    step(I0{}, No{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
+         [&]() __attribute__((always_inline)) { issue(first + kRing, 0); });
     for (int u = first + 1; u < last; ++u) {
       at = to;
       to = area(u + 1);
       bits = tile_bits(u);
-      step(I1{}, Yes{}, I0{}, at, unsigned(bits), [&](auto i_t) __attribute__((always_inline)) { ahead(i_t, at, 32); });
-      step(I0{}, Yes{}, I32{}, at, unsigned(bits >> 32),
-           [&](auto i_t) __attribute__((always_inline)) { cross(i_t, u, to); });
+      step(I1{}, Yes{}, I0{}, No{}, at, at, unsigned(bits), []() {});
+      step(I0{}, Yes{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
+           [&]() __attribute__((always_inline)) { issue(u + kRing, (u - first) % kRing); });
     }
-    at = to;
-    step(I1{}, Yes{}, I0{}, at, 0u, [&](auto) __attribute__((always_inline)) {});
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) read_v(at, 32, j);
+    step(I1{}, Yes{}, I0{}, No{}, to, to, 0u, []() {});
 #pragma unroll
     for (int f = 0; f < KF; ++f) {
 #pragma unroll
       for (int b = 0; b < QB; ++b)
         o[b][f % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[1][b][f / NF]), o[b][f % NF], 0, 0, 0);
-      if (f + kAhead < KF) read_v(at, 32, f + kAhead);
+      if (f + kAhead < KF) read_v(to, 32, f + kAhead);
     }
     waitvm<0>();  // no load into LDS may be in flight where the outputs go through it
     wait_lgkm0();
@@ -479,7 +465,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
       u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
-template <int D, int QB>
+template <int D, int QB, int kWaves>
 hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
   AttentionArgs p = a;
   if (a.mask) {
@@ -491,7 +477,7 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
   }
   in_launches(a.batch * a.kv_heads * a.tiles * a.splits, kWaves * 64, [&](int64_t first, unsigned count) {
     p.first = first;
-    hipLaunchKernelGGL((attention_kernel<D, QB>), dim3(count), dim3(kWaves * 64), 0, stream, p);
+    hipLaunchKernelGGL((attention_kernel<D, QB, kWaves>), dim3(count), dim3(kWaves * 64), 0, stream, p);
   });
   if (a.splits > 1) {
     const int64_t values = a.batch * a.kv_heads * a.m * a.ratio * (a.d / 4);
@@ -507,7 +493,8 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
 AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d) {
   AttentionPlan plan{};
   plan.blocks = 1;
-  const int tile_rows = kWaves * 32 * plan.blocks;
+  plan.waves = 4;
+  const int tile_rows = plan.waves * 32 * plan.blocks;
   plan.tiles = (rows + tile_rows - 1) / tile_rows;
   plan.splits = 1;
   const int64_t blocks = batch * kv_heads * plan.tiles, cus = device_cu_count();
@@ -521,11 +508,11 @@ AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int6
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream) {
-  if (a.d <= 64) return launch_t<64, 1>(a, stream);
-  if (a.d <= 96) return launch_t<96, 1>(a, stream);
-  if (a.d <= 128) return launch_t<128, 1>(a, stream);
-  if (a.d <= 160) return launch_t<160, 1>(a, stream);
-  return launch_t<192, 1>(a, stream);
+  if (a.d <= 64) return launch_t<64, 1, 4>(a, stream);
+  if (a.d <= 96) return launch_t<96, 1, 4>(a, stream);
+  if (a.d <= 128) return launch_t<128, 1, 4>(a, stream);
+  if (a.d <= 160) return launch_t<160, 1, 4>(a, stream);
+  return launch_t<192, 1, 4>(a, stream);
 }
 
 }  // namespace convrot

@@ -238,13 +238,14 @@ struct AttentionArgs {
   float* part;   // [splits][batch][kv_heads][m ratio][d] where the keys are split
   float* stats;  // ... and the maximum (in powers of two) and sum of each row
   uint64_t* bits;  // [batch][ceil(l / 64)], with a mask: its bits
-  int tiles, splits, blocks;
+  int tiles, splits, blocks, waves;
   int64_t first;  // workgroup of the launch's first one
 };
 struct AttentionPlan {
   int64_t tiles;  // of a key head's queries
   int splits;     // of the keys
   int blocks;     // of 32 queries of a wave
+  int waves;      // of a workgroup
 };
 AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
