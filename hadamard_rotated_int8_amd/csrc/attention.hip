@@ -56,6 +56,25 @@ CR_DEVICE void load_to_lds(const void* base, unsigned bytes, unsigned place, int
                : "memory");
 }
 
+// One product onto (FIRST: from `start` into) its accumulators, for waves that
+// have a SIMD to themselves: the output's sums and Q are to stay in the
+// accumulation half of the registers and scores in the other, which the
+// compiler, free to choose, mixes.  It does not see that these are matrix
+// instructions: an operand that a vector instruction may have written right
+// before takes 2 wait states, results are touched 18 later (mfma_settle, or two
+// more products).
+template <bool FIRST>
+CR_DEVICE void scores_mfma(f32x16& s, bf16x8 k, bf16x8 q, const f32x16& start) {
+  if constexpr (FIRST)
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %3" : "=&v"(s) : "v"(k), "a"(q), "v"(start));
+  else
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(k), "a"(q));
+}
+CR_DEVICE void output_mfma(f32x16& o, bf16x8 v, bf16x8 p) {
+  asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(v), "v"(p));
+}
+CR_DEVICE void mfma_settle(f32x16& o) { asm volatile("" : "+a"(o)); }
+
 CR_DEVICE float other_half(float v) {  // lane ^ 32
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
@@ -93,7 +112,8 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   constexpr int kTile = kKeys * kPitch;       // bytes of K, or of V
   constexpr int kPieces = kTile / 1024 / kWaves;
   constexpr int kRows = kWaves * QB * 32;     // queries of a workgroup
-  constexpr int kRing = kPitch == 512 ? 2 : kWaves == 8 ? 4 : kPitch == 128 ? 3 : 2;  // tiles of K and V in LDS
+  constexpr bool kAlone = QB == 2;            // a wave has its SIMD to itself
+  constexpr int kRing = kPitch == 512 ? 2 : kPitch == 128 || kAlone ? 3 : 2;  // tiles of K and V in LDS
   constexpr int KF = D / 16, NF = D / 32;     // fragments of 32 keys of K; blocks of 32 features of V
   constexpr int kHalf = KF * QB;              // matrix instructions of each product of a step
   constexpr int kAhead = KF % 4 == 0 ? 4 : KF / 2;  // fragments read ahead (the next step takes the same registers)
@@ -181,6 +201,12 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
     }
   }
 
+  if constexpr (kAlone) {  // (into the accumulation half, where the products take them)
+#pragma unroll
+    for (int b = 0; b < QB; ++b)
+#pragma unroll
+      for (int t = 0; t < KF; ++t) asm volatile("" : "+a"(qf[b][t]));
+  }
   // Tile u's area holds K of tile u and V of tile u - 1: what the two steps
   // before and at block 2 u read.
   if (first < last) {
@@ -229,6 +255,7 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
       asm volatile("" ::"v"(word));  // (formed here, not where the compiler would collect them)
       pf[x][b][e / 8][e % 8 / 2] = word;
       sum[b] = __builtin_amdgcn_fdot2_f32_bf16(both, bf16x2{(__bf16)1.f, (__bf16)1.f}, e == 1 ? 0.f : sum[b], false);
+      asm volatile("" ::"v"(sum[b]));
     }
   };
   // What the scores of a block start from: zero, minus infinity where the key is hidden.
@@ -251,6 +278,31 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
     if (e == 15) most[b] = fmaxf(most[b], other_half(most[b]));
   };
 
+  auto score = [&](f32x16& to, auto first_t, int b, int f) __attribute__((always_inline)) {
+    if constexpr (kAlone)
+      scores_mfma<decltype(first_t)::value>(to, kf[f % kAhead], qf[b][f], start);
+    else
+      to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], decltype(first_t)::value ? start : to, 0, 0,
+                                                   0);
+  };
+  auto output = [&](int x, int b, int f) __attribute__((always_inline)) {
+    const bf16x8 w = __builtin_bit_cast(bf16x8, pf[x][b][f / NF]);
+    if constexpr (kAlone)
+      output_mfma(o[b][f % NF], vf[f % kAhead], w);
+    else
+      o[b][f % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[f % kAhead], w, o[b][f % NF], 0, 0, 0);
+  };
+  auto settled = [&]() __attribute__((always_inline)) {  // before the output's sums are read
+    if constexpr (kAlone) {
+      asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < QB; ++b)
+#pragma unroll
+        for (int n = 0; n < NF; ++n) mfma_settle(o[b][n]);
+    }
+  };
+
   // The step with the scores and weights of set X, on rows ROW .. of the area at
   // `at`: the next block's K (`bits`: which of its keys are seen) and the last
   // one's values; the next step's rows start at NROW of the area at `nat`.
@@ -258,25 +310,25 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   // it may be in flight, and this one, which every wave has then read, is
   // given up to load(): at slot kSync, two behind the last reads.
   constexpr int kSync = 2 * (KF - kAhead) * QB + 2;
-  auto step = [&](auto x_t, auto pv_t, auto row_t, auto cross_t, int at, int nat, unsigned bits,
+  // QK, PV: which of the products there are (the first and the last step lack one).
+  auto step = [&](auto x_t, auto qk_t, auto pv_t, auto row_t, auto cross_t, int at, int nat, unsigned bits,
                   auto&& load) __attribute__((always_inline)) {
     constexpr int X = decltype(x_t)::value, Y = 1 - X, ROW = decltype(row_t)::value, NROW = 32 - ROW;
-    constexpr bool PV = decltype(pv_t)::value, CROSS = decltype(cross_t)::value;
-    hide(bits);
+    constexpr bool QK = decltype(qk_t)::value, PV = decltype(pv_t)::value, CROSS = decltype(cross_t)::value;
+    if (QK) hide(bits);
     for_each_index(std::make_integer_sequence<int, 2 * kHalf>{}, [&](auto i_t) __attribute__((always_inline)) {
       constexpr int i = decltype(i_t)::value;
       constexpr bool K = i % 2 == 0;
       constexpr int b = i / 2 % QB, f = i / 2 / QB;  // the query block and fragment
-      if constexpr (K)
-        s[Y][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], f == 0 ? start : s[Y][b], 0, 0, 0);
-      else if constexpr (PV)
-        o[b][f % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[Y][b][f / NF]), o[b][f % NF], 0, 0, 0);
+      if constexpr (K && QK)
+        score(s[Y][b], std::integral_constant<bool, f == 0>{}, b, f);
+      else if constexpr (!K && PV)
+        output(Y, b, f);
       // The fragment 4 ahead, of this step's rows or the next one's.
       if constexpr (b == QB - 1 && f + kAhead < KF) {
-        if constexpr (K)
+        if constexpr (K && QK)
           read_k(at, ROW, f + kAhead);
-        else if constexpr (PV)
+        else if constexpr (!K && PV)
           read_v(at, ROW, f + kAhead);
       }
       if constexpr (CROSS && i == kSync) {
@@ -288,9 +340,9 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
       auto next = [&](auto j_t) __attribute__((always_inline)) {  // what slot j frees the registers for
         constexpr int j = decltype(j_t)::value, jf = j / 2 / QB + kAhead - KF;
         if constexpr (j / 2 % QB == QB - 1 && jf >= 0) {
-          if constexpr (j % 2 == 0)
+          if constexpr (j % 2 == 0 && QK)
             read_k(nat, NROW, jf);
-          else
+          else if constexpr (j % 2 == 1)
             read_v(nat, NROW, jf);
         }
       };
@@ -311,6 +363,7 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
 #pragma unroll
     for (int b = 0; b < QB; ++b) more |= most[b] > limit[b];
     if (__ballot(more) != 0) {
+      settled();
 #pragma unroll
       for (int b = 0; b < QB; ++b) {
         const float now = fmaxf(top[b], most[b]);
@@ -351,35 +404,37 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
     for (int k = 0; k < kAhead; ++k) read_k(at, 0, k);
     uint64_t bits = tile_bits(first);
     hide(unsigned(bits));
+    for_each_index(std::make_integer_sequence<int, KF>{}, [&](auto f_t) __attribute__((always_inline)) {
+      constexpr int f = decltype(f_t)::value;
 #pragma unroll
-    for (int f = 0; f < KF; ++f) {
-#pragma unroll
-      for (int b = 0; b < QB; ++b)
-        s[0][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], f == 0 ? start : s[0][b], 0, 0, 0);
-      if (f + kAhead < KF)
+      for (int b = 0; b < QB; ++b) score(s[0][b], std::integral_constant<bool, f == 0>{}, b, f);
+      if constexpr (f + kAhead < KF)
         read_k(at, 0, f + kAhead);
       else
         read_k(at, 32, f + kAhead - KF);
+    });
+    if constexpr (kAlone) {
+#pragma unroll
+      for (int b = 0; b < QB; ++b) asm volatile("s_nop 15\n\ts_nop 3" : "+v"(s[0][b]));
     }
-    step(I0{}, No{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
+    step(I0{}, Yes{}, No{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
          [&]() __attribute__((always_inline)) { issue(first + kRing, 0); });
     for (int u = first + 1; u < last; ++u) {
       at = to;
       to = area(u + 1);
       bits = tile_bits(u);
-      step(I1{}, Yes{}, I0{}, No{}, at, at, unsigned(bits), []() {});
-      step(I0{}, Yes{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
+      step(I1{}, Yes{}, Yes{}, I0{}, No{}, at, at, unsigned(bits), []() {});
+      step(I0{}, Yes{}, Yes{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
            [&]() __attribute__((always_inline)) { issue(u + kRing, (u - first) % kRing); });
     }
-    step(I1{}, Yes{}, I0{}, No{}, to, to, 0u, []() {});
+    step(I1{}, No{}, Yes{}, I0{}, No{}, to, to, 0u, []() {});
 #pragma unroll
     for (int f = 0; f < KF; ++f) {
 #pragma unroll
-      for (int b = 0; b < QB; ++b)
-        o[b][f % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[1][b][f / NF]), o[b][f % NF], 0, 0, 0);
+      for (int b = 0; b < QB; ++b) output(1, b, f);
       if (f + kAhead < KF) read_v(to, 32, f + kAhead);
     }
+    settled();
     waitvm<0>();  // no load into LDS may be in flight where the outputs go through it
     wait_lgkm0();
     barrier();
@@ -492,7 +547,7 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
 
 AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d) {
   AttentionPlan plan{};
-  plan.blocks = 1;
+  plan.blocks = d <= 128 && rows > 128 ? 2 : 1;
   plan.waves = 4;
   const int tile_rows = plan.waves * 32 * plan.blocks;
   plan.tiles = (rows + tile_rows - 1) / tile_rows;
@@ -508,9 +563,10 @@ AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int6
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream) {
-  if (a.d <= 64) return launch_t<64, 1, 4>(a, stream);
-  if (a.d <= 96) return launch_t<96, 1, 4>(a, stream);
-  if (a.d <= 128) return launch_t<128, 1, 4>(a, stream);
+  const bool two = a.blocks == 2;
+  if (a.d <= 64) return two ? launch_t<64, 2, 4>(a, stream) : launch_t<64, 1, 4>(a, stream);
+  if (a.d <= 96) return two ? launch_t<96, 2, 4>(a, stream) : launch_t<96, 1, 4>(a, stream);
+  if (a.d <= 128) return two ? launch_t<128, 2, 4>(a, stream) : launch_t<128, 1, 4>(a, stream);
   if (a.d <= 160) return launch_t<160, 1, 4>(a, stream);
   return launch_t<192, 1, 4>(a, stream);
 }
