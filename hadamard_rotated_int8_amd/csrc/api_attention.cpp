@@ -41,9 +41,10 @@ convrot::AttentionPlan plan_of(const convrot_attention& a) {
 }
 
 // A tensor's strides and alignment; `key`: its rows are loaded by tiles.
-convrot_status check_tensor(const void* p, const int64_t* stride, bool key) {
+convrot_status check_tensor(const void* p, const int64_t* stride, int64_t tokens, int32_t d, bool key) {
   for (int i = 0; i < 3; ++i)
     if (stride[i] < 0 || stride[i] > (key && i == 1 ? kMaxKeyStride : kMaxStride)) return CONVROT_ERR_SHAPE;
+  if (key && tokens > 1 && stride[1] != 0 && stride[1] < d) return CONVROT_ERR_SHAPE;
   for (int i = 0; i < 3; ++i)
     if (stride[i] % 8 != 0) return CONVROT_ERR_UNSUPPORTED;
   if (!p) return CONVROT_ERR_NULL;
@@ -69,11 +70,11 @@ convrot_status convrot_attention_apply(const convrot_attention* a, void* stream)
   if (!(a->scale > 0.f) || a->scale > 3.4e38f) return CONVROT_ERR_UNSUPPORTED;  // a NaN too
   if (a->mask && (a->mask_stride < 0 || a->mask_stride > kMaxStride)) return CONVROT_ERR_SHAPE;
   if (a->batch == 0 || a->m == 0) return CONVROT_OK;
-  if ((st = check_tensor(a->q, a->q_stride, false)) != CONVROT_OK) return st;
-  if ((st = check_tensor(a->out, a->out_stride, false)) != CONVROT_OK) return st;
+  if ((st = check_tensor(a->q, a->q_stride, a->m, a->d, false)) != CONVROT_OK) return st;
+  if ((st = check_tensor(a->out, a->out_stride, a->m, a->d, false)) != CONVROT_OK) return st;
   if (a->l > 0) {
-    if ((st = check_tensor(a->k, a->k_stride, true)) != CONVROT_OK) return st;
-    if ((st = check_tensor(a->v, a->v_stride, true)) != CONVROT_OK) return st;
+    if ((st = check_tensor(a->k, a->k_stride, a->l, a->d, true)) != CONVROT_OK) return st;
+    if ((st = check_tensor(a->v, a->v_stride, a->l, a->d, true)) != CONVROT_OK) return st;
   }
   if (!aligned(a->lengths, 4)) return CONVROT_ERR_UNSUPPORTED;
   if (a->out == a->q || a->out == a->k || a->out == a->v) return CONVROT_ERR_UNSUPPORTED;

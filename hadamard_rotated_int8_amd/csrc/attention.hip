@@ -56,24 +56,40 @@ CR_DEVICE void load_to_lds(const void* base, unsigned bytes, unsigned place, int
                : "memory");
 }
 
-// One product onto (FIRST: from `start` into) its accumulators, for waves that
-// have a SIMD to themselves: the output's sums and Q are to stay in the
-// accumulation half of the registers and scores in the other, which the
-// compiler, free to choose, mixes.  It does not see that these are matrix
-// instructions: an operand that a vector instruction may have written right
-// before takes 2 wait states, results are touched 18 later (mfma_settle, or two
-// more products).
-template <bool FIRST>
+// One product onto (FIRST: from `start` into) its accumulators.  As inline
+// assembly, so that sums stay in their registers: the compiler, free to choose
+// others, gives the output's sums two sets round the loop and spills.  It does
+// not see that these are matrix instructions: an operand that a vector
+// instruction may have written right before takes 2 wait states, results are
+// touched 18 later (mfma_settle, or two more products).
+// tests/test_attention_hazards.py checks the built code for both.  ACC: Q and
+// the output's sums are in the accumulation half of the registers, where a wave
+// has all of them.
+template <bool FIRST, bool ACC>
 CR_DEVICE void scores_mfma(f32x16& s, bf16x8 k, bf16x8 q, const f32x16& start) {
-  if constexpr (FIRST)
+  if constexpr (FIRST && ACC)
     asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %3" : "=&v"(s) : "v"(k), "a"(q), "v"(start));
-  else
+  else if constexpr (FIRST)
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %3" : "=&v"(s) : "v"(k), "v"(q), "v"(start));
+  else if constexpr (ACC)
     asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(k), "a"(q));
+  else
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(k), "v"(q));
 }
+template <bool ACC>
 CR_DEVICE void output_mfma(f32x16& o, bf16x8 v, bf16x8 p) {
-  asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(v), "v"(p));
+  if constexpr (ACC)
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(v), "v"(p));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(o) : "v"(v), "v"(p));
 }
-CR_DEVICE void mfma_settle(f32x16& o) { asm volatile("" : "+a"(o)); }
+template <bool ACC>
+CR_DEVICE void mfma_settle(f32x16& o) {
+  if constexpr (ACC)
+    asm volatile("" : "+a"(o));
+  else
+    asm volatile("" : "+v"(o));
+}
 
 CR_DEVICE float other_half(float v) {  // lane ^ 32
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -104,7 +120,7 @@ __global__ __launch_bounds__(256) void attention_bits_kernel(const AttentionArgs
 // same relative precision at 256 as at 1.  So a step takes the base as it is,
 // finds the maximum beside it, and if that has risen too far does its weights
 // again at the end.
-template <int D, int QB, int kWaves>
+template <int D, int QB, int kWaves, bool MASK>
 __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void attention_kernel(const AttentionArgs p) {
   constexpr int kPitch = D <= 64 ? 128 : D <= 128 ? 256 : 512;  // bytes of a row in LDS
   constexpr int kChunks = kPitch / 16;
@@ -112,7 +128,7 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   constexpr int kTile = kKeys * kPitch;       // bytes of K, or of V
   constexpr int kPieces = kTile / 1024 / kWaves;
   constexpr int kRows = kWaves * QB * 32;     // queries of a workgroup
-  constexpr bool kAlone = QB == 2;            // a wave has its SIMD to itself
+  constexpr bool kAlone = QB == 2 || D > 128;  // a wave has its SIMD, and all of its registers, to itself
   constexpr int kRing = kPitch == 512 ? 2 : kPitch == 128 || kAlone ? 3 : 2;  // tiles of K and V in LDS
   constexpr int KF = D / 16, NF = D / 32;     // fragments of 32 keys of K; blocks of 32 features of V
   constexpr int kHalf = KF * QB;              // matrix instructions of each product of a step
@@ -148,12 +164,14 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   auto tile_bits = [&](int t) -> uint64_t {
     const int64_t left = keys - int64_t(t) * kKeys;
     uint64_t bits = t >= last || left <= 0 ? 0 : left >= kKeys ? ~uint64_t(0) : (uint64_t(1) << left) - 1;
-    if (p.mask && t < last) bits &= words[t];
+    if (MASK && t < last) bits &= words[t];
     return bits;
   };
   // Rows of K (of tile t) and V (of the tile before) into LDS area `to`; hidden
   // and absent ones read as zero: a score is then what its accumulator starts
-  // from, and a NaN of a hidden value does not meet its weight of zero.  Piece i is 4 i pieces' rows behind
+  // from, and a NaN of a hidden value does not meet its weight of zero.  (Rows
+  // behind the last key lie outside the resource: a token's stride is 0 or
+  // holds the row.)  Piece i is 4 i pieces' rows behind
   // the wave's first; with 512-byte rows that is 8, and K's chunks change places.
   constexpr int kStep = kWaves * kRowsPiece;
   constexpr int kPlaces = kPitch == 512 ? 2 : 1;
@@ -168,22 +186,34 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
     const int c = (lane % kChunks ^ value_swizzle<kPitch>(prow)) * 16;
     vplace = c < dbytes ? unsigned(prow * int(p.vs[1]) * 2 + c) : kOutOfRange;
   }
-  auto issue = [&](int t, int to) __attribute__((always_inline)) {
-    auto rows = [&](const uint16_t* base, int64_t stride, int u, const unsigned* place, int places, unsigned dst)
-                    __attribute__((always_inline)) {
-      const uint64_t seen = u < first ? 0 : tile_bits(u);
-      const unsigned bytes = seen ? (kKeys - 1) * unsigned(stride) * 2 + dbytes : 0;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        unsigned at = place[i % places];
-        if (seen != ~uint64_t(0)) at = (seen >> (prow + i * kStep)) & 1 ? at : kOutOfRange;
-        load_to_lds(base + int64_t(u) * kKeys * stride, bytes, at, i * kStep * int(stride) * 2,
-                    dst + i * kWaves * 1024);
-      }
-    };
-    const unsigned dst = unsigned(reinterpret_cast<uintptr_t>((lds_byte*)smem)) + to * 2 * kTile + wave * 1024;
-    rows(kbase, p.ks[1], t, kplace, kPlaces, dst);
-    rows(vbase, p.vs[1], t - 1, &vplace, 1, dst + kTile);
+  struct {
+    const uint16_t *k, *v;
+    unsigned kbytes, vbytes;
+    uint64_t kseen, vseen;  // (with a mask)
+    unsigned to;
+  } load;
+  auto bytes_of = [&](int t, int64_t stride) -> unsigned {  // of tile t's rows, up to the last key
+    const int64_t left = t < first || t >= last ? 0 : keys - int64_t(t) * kKeys;
+    return left <= 0 ? 0 : (left < kKeys ? unsigned(left) - 1 : kKeys - 1) * unsigned(stride) * 2 + dbytes;
+  };
+  auto begin_load = [&](int t, int to) __attribute__((always_inline)) {
+    load.k = kbase + int64_t(t) * kKeys * p.ks[1];
+    load.v = vbase + int64_t(t - 1) * kKeys * p.vs[1];
+    load.kbytes = bytes_of(t, p.ks[1]);
+    load.vbytes = bytes_of(t - 1, p.vs[1]);
+    if (MASK) {
+      load.kseen = tile_bits(t);
+      load.vseen = t == first ? 0 : tile_bits(t - 1);
+    }
+    load.to = unsigned(reinterpret_cast<uintptr_t>((lds_byte*)smem)) + to * 2 * kTile + wave * 1024;
+  };
+  auto piece = [&](int j) __attribute__((always_inline)) {  // K's, then V's
+    const bool v = j >= kPieces;
+    const int i = v ? j - kPieces : j;
+    unsigned at = v ? vplace : kplace[i % kPlaces];
+    if constexpr (MASK) at = ((v ? load.vseen : load.kseen) >> (prow + i * kStep)) & 1 ? at : kOutOfRange;
+    load_to_lds(v ? load.v : load.k, v ? load.vbytes : load.kbytes, at, i * kStep * int(v ? p.vs[1] : p.ks[1]) * 2,
+                load.to + (v ? kTile : 0) + i * kWaves * 1024);
   };
 
   // Q: lane l holds query l % 32, features 16 t + 8 (l / 32) .. +7.
@@ -211,7 +241,11 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   // before and at block 2 u read.
   if (first < last) {
 #pragma unroll
-    for (int u = 0; u < kRing; ++u) issue(first + u, u);
+    for (int u = 0; u < kRing; ++u) {
+      begin_load(first + u, u);
+#pragma unroll
+      for (int j = 0; j < 2 * kPieces; ++j) piece(j);
+    }
   }
 
   const float c = p.scale * kLog2e, slack = kSlack / c;
@@ -247,15 +281,14 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   auto weigh = [&](int x, int n) __attribute__((always_inline)) {
     const int b = n / 16, e = n % 16;
     const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][b][e], c, -base[b]));
+    sum[b] = e == 0 ? w : sum[b] + w;
     if (e % 2 == 0) {
       held = w;
     } else {
       const bf16x2 both = {(__bf16)held, (__bf16)w};
       const unsigned word = __builtin_bit_cast(unsigned, both);
-      asm volatile("" ::"v"(word));  // (formed here, not where the compiler would collect them)
+      asm volatile("" ::"v"(word), "v"(sum[b]));  // (formed here, not where the compiler would collect them)
       pf[x][b][e / 8][e % 8 / 2] = word;
-      sum[b] = __builtin_amdgcn_fdot2_f32_bf16(both, bf16x2{(__bf16)1.f, (__bf16)1.f}, e == 1 ? 0.f : sum[b], false);
-      asm volatile("" ::"v"(sum[b]));
     }
   };
   // What the scores of a block start from: zero, minus infinity where the key is hidden.
@@ -279,28 +312,18 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   };
 
   auto score = [&](f32x16& to, auto first_t, int b, int f) __attribute__((always_inline)) {
-    if constexpr (kAlone)
-      scores_mfma<decltype(first_t)::value>(to, kf[f % kAhead], qf[b][f], start);
-    else
-      to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kAhead], qf[b][f], decltype(first_t)::value ? start : to, 0, 0,
-                                                   0);
+    scores_mfma<decltype(first_t)::value, kAlone>(to, kf[f % kAhead], qf[b][f], start);
   };
   auto output = [&](int x, int b, int f) __attribute__((always_inline)) {
-    const bf16x8 w = __builtin_bit_cast(bf16x8, pf[x][b][f / NF]);
-    if constexpr (kAlone)
-      output_mfma(o[b][f % NF], vf[f % kAhead], w);
-    else
-      o[b][f % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[f % kAhead], w, o[b][f % NF], 0, 0, 0);
+    output_mfma<kAlone>(o[b][f % NF], vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[x][b][f / NF]));
   };
   auto settled = [&]() __attribute__((always_inline)) {  // before the output's sums are read
-    if constexpr (kAlone) {
-      asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int b = 0; b < QB; ++b)
+    for (int b = 0; b < QB; ++b)
 #pragma unroll
-        for (int n = 0; n < NF; ++n) mfma_settle(o[b][n]);
-    }
+      for (int n = 0; n < NF; ++n) mfma_settle<kAlone>(o[b][n]);
   };
 
   // The step with the scores and weights of set X, on rows ROW .. of the area at
@@ -308,11 +331,17 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   // one's values; the next step's rows start at NROW of the area at `nat`.
   // CROSS: that is another area, which has landed once only the loads behind
   // it may be in flight, and this one, which every wave has then read, is
-  // given up to load(): at slot kSync, two behind the last reads.
+  // given up to the loads that begin() names: at slot kSync, two behind the
+  // last reads.  The loads go one by one into the slots from there to the
+  // middle of the next step: the
+  // memory path takes 16 cycles of a CU for each, and a wave whose loads stand
+  // in line issues nothing else (4096 x 8192, 64 heads of 128: 4180 cycles for
+  // 64 keys with the loads all at once).
   constexpr int kSync = 2 * (KF - kAhead) * QB + 2;
+  constexpr int kEvery = 4 * kPieces <= 2 * kHalf ? 2 : 1;  // slots to a load
   // QK, PV: which of the products there are (the first and the last step lack one).
   auto step = [&](auto x_t, auto qk_t, auto pv_t, auto row_t, auto cross_t, int at, int nat, unsigned bits,
-                  auto&& load) __attribute__((always_inline)) {
+                  auto&& begin) __attribute__((always_inline)) {
     constexpr int X = decltype(x_t)::value, Y = 1 - X, ROW = decltype(row_t)::value, NROW = 32 - ROW;
     constexpr bool QK = decltype(qk_t)::value, PV = decltype(pv_t)::value, CROSS = decltype(cross_t)::value;
     if (QK) hide(bits);
@@ -324,6 +353,7 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
         score(s[Y][b], std::integral_constant<bool, f == 0>{}, b, f);
       else if constexpr (!K && PV)
         output(Y, b, f);
+      if (i < 2) __builtin_amdgcn_sched_barrier(0);  // (block t's last scores take that long)
       // The fragment 4 ahead, of this step's rows or the next one's.
       if constexpr (b == QB - 1 && f + kAhead < KF) {
         if constexpr (K && QK)
@@ -335,7 +365,11 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
         wait_lgkm0();
         waitvm<(kRing - 2) * 2 * kPieces>();
         barrier();
-        load();
+        begin();
+      }
+      if constexpr (QK) {
+        constexpr int n = CROSS ? i - kSync - 1 : i + 2 * kHalf - kSync - 1;  // slots since then
+        if constexpr (n >= 0 && n % kEvery == 0 && n / kEvery < 2 * kPieces) piece(n / kEvery);
       }
       auto next = [&](auto j_t) __attribute__((always_inline)) {  // what slot j frees the registers for
         constexpr int j = decltype(j_t)::value, jf = j / 2 / QB + kAhead - KF;
@@ -413,20 +447,20 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
       else
         read_k(at, 32, f + kAhead - KF);
     });
-    if constexpr (kAlone) {
 #pragma unroll
-      for (int b = 0; b < QB; ++b) asm volatile("s_nop 15\n\ts_nop 3" : "+v"(s[0][b]));
-    }
+    for (int b = 0; b < QB; ++b) asm volatile("s_nop 15\n\ts_nop 3" : "+v"(s[0][b]));
     step(I0{}, Yes{}, No{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
-         [&]() __attribute__((always_inline)) { issue(first + kRing, 0); });
-    for (int u = first + 1; u < last; ++u) {
+         [&]() __attribute__((always_inline)) { begin_load(first + kRing, 0); });
+    // (not a loop that tests first: round one the compiler keeps two sets of the output's sums)
+    int u = first + 1;
+    if (u < last) do {
       at = to;
       to = area(u + 1);
       bits = tile_bits(u);
       step(I1{}, Yes{}, Yes{}, I0{}, No{}, at, at, unsigned(bits), []() {});
       step(I0{}, Yes{}, Yes{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
-           [&]() __attribute__((always_inline)) { issue(u + kRing, (u - first) % kRing); });
-    }
+           [&]() __attribute__((always_inline)) { begin_load(u + kRing, (u - first) % kRing); });
+    } while (++u < last);
     step(I1{}, No{}, Yes{}, I0{}, No{}, to, to, 0u, []() {});
 #pragma unroll
     for (int f = 0; f < KF; ++f) {
@@ -532,7 +566,10 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
   }
   in_launches(a.batch * a.kv_heads * a.tiles * a.splits, kWaves * 64, [&](int64_t first, unsigned count) {
     p.first = first;
-    hipLaunchKernelGGL((attention_kernel<D, QB, kWaves>), dim3(count), dim3(kWaves * 64), 0, stream, p);
+    if (a.mask)
+      hipLaunchKernelGGL((attention_kernel<D, QB, kWaves, true>), dim3(count), dim3(kWaves * 64), 0, stream, p);
+    else
+      hipLaunchKernelGGL((attention_kernel<D, QB, kWaves, false>), dim3(count), dim3(kWaves * 64), 0, stream, p);
   });
   if (a.splits > 1) {
     const int64_t values = a.batch * a.kv_heads * a.m * a.ratio * (a.d / 4);
@@ -547,7 +584,7 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
 
 AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d) {
   AttentionPlan plan{};
-  plan.blocks = d <= 128 && rows > 128 ? 2 : 1;
+  plan.blocks = 1;
   plan.waves = 4;
   const int tile_rows = plan.waves * 32 * plan.blocks;
   plan.tiles = (rows + tile_rows - 1) / tile_rows;

@@ -638,7 +638,7 @@ convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* strea
 
 /*
  *   q_stride .. out_stride : of batch, token and head, 0 .. 2^40; the tokens'
- *                 of k and v at most 2^23.  out's elements must not overlap one
+ *                 of k and v at most 2^23, and 0 or at least d.  out's elements must not overlap one
  *                 another nor an input.
  *   d           : a multiple of 8 in 8 .. CONVROT_MAX_HEAD_DIM
  *   scale       : > 0 and finite

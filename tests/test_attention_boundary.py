@@ -28,7 +28,7 @@ def test_an_empty_call_is_no_error():
     dict(batch=-1), dict(m=-1), dict(l=-1), dict(l=2 ** 31), dict(m=2 ** 31), dict(heads=0), dict(kv_heads=0),
     dict(heads=10, kv_heads=4), dict(heads=4097, kv_heads=1), dict(d=0), dict(d=200), dict(d=-8),
     dict(m=2 ** 30, heads=10, kv_heads=2), dict(m=2 ** 30, batch=2 ** 10),
-    dict(m=1, qt=-8), dict(m=1, oh=2 ** 41), dict(m=1, kt=2 ** 24), dict(m=1, vt=2 ** 24),
+    dict(m=1, qt=-8), dict(m=1, kt=56), dict(m=1, vt=8), dict(m=1, oh=2 ** 41), dict(m=1, kt=2 ** 24), dict(m=1, vt=2 ** 24),
     dict(mask=64, mask_stride=-1)])
 def test_shapes_are_refused(kw):
     assert _apply(**kw) == cr.ERR_SHAPE

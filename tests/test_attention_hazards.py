@@ -1,4 +1,4 @@
-"""The attention kernels whose matrix instructions are inline assembly keep the distances that these
+"""The attention kernels' matrix instructions, which are inline assembly, keep the distances that they
 need, in both register files and round the loops (CPU).
 
 As test_matrix_registers.py, for v_mfma_f32_32x32x16_bf16: no vector instruction writes an operand less
@@ -19,7 +19,7 @@ import test_matrix_registers as registers
 from test_matrix_hazards import OBJDUMP
 
 MFMA = "v_mfma_f32_32x32x16_bf16"
-NAME = re.compile(r"attention_kernelILi\d+ELi2E")  # two blocks of queries to a wave: those that have the assembly
+NAME = re.compile(r"attention_kernelILi")
 OPERAND_STATES, RESULT_STATES, MFMA_STATES = 2, 18, 8
 
 
@@ -97,7 +97,7 @@ def test_built_code_keeps_its_distances(tmp_path):
                 assert branch == bool(target), ln
                 kernels[name].append((address, ins.strip(), start + int(target[1] or "0", 16) if branch else None))
     kernels = {name: registers._kernel(lines) for name, lines in kernels.items() if NAME.search(name)}
-    assert len(kernels) == 3  # for heads of up to 64, 96 and 128
+    assert len(kernels) >= 10  # for each size of heads, with and without a mask
     for name, ins in kernels.items():
         count, found = _hazards(ins)
         assert count >= 16, (name, count)
