@@ -590,21 +590,28 @@ def block_update(x: torch.Tensor, branch: torch.Tensor, gate: torch.Tensor | Non
     return out_h, (packed if pack else y)
 
 
-def _workspace(fn, name, args, struct_, dev):
+_needs = {}
+
+
+def _workspace(fn, name, args, struct_, dev, sizes):
     """args (whose last two are the workspace and its size) packed with a workspace of the size that
-    the library asks for, and that workspace, which must live until the call is submitted."""
-    need = ctypes.c_int64()
-    if torch._C._cuda_getDevice() == dev.index:
-        st = fn(struct_.pack(*args), ctypes.byref(need))
-    else:
+    the library asks for, and that workspace, which must live until the call is submitted.  The size
+    follows from `sizes` and the device alone, so the library is asked once for each."""
+    key = (name, dev.index, *sizes)
+    need = _needs.get(key)
+    if need is None:
+        n = ctypes.c_int64()
         with torch.cuda.device(dev):
-            st = fn(struct_.pack(*args), ctypes.byref(need))
-    if st != OK:
-        raise ConvrotError(st, name)
+            st = fn(struct_.pack(*args), ctypes.byref(n))
+        if st != OK:
+            raise ConvrotError(st, name)
+        if len(_needs) >= 4096:
+            _needs.clear()
+        need = _needs[key] = n.value
     space = None
-    if need.value:
-        space = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        args[-2:] = space.data_ptr(), need.value
+    if need:
+        space = torch.empty(need, dtype=torch.uint8, device=dev)
+        args[-2:] = space.data_ptr(), need
     return struct_.pack(*args), space
 
 
@@ -664,7 +671,7 @@ def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
             _DTYPE[x.dtype], _DTYPE[out.dtype], eps, 1 if silu else 0,
             *_vector_args(weight, c, "weight", dev), *_vector_args(bias, c, "bias", dev), 0, 0]
     packed, space = _workspace(lib().convrot_group_norm_workspace, "convrot_group_norm_workspace", args,
-                               _GROUP_NORM, dev)
+                               _GROUP_NORM, dev, (batch, positions, c, groups))
     _launch(lib().convrot_group_norm_apply, "convrot_group_norm_apply", dev, packed)
     return out
 

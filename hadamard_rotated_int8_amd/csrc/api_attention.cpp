@@ -15,7 +15,7 @@ using convrot::kMaxRows;
 namespace {
 
 constexpr int64_t kMaxStride = int64_t(1) << 40;
-// 64 rows of keys or values lie in 31 bits.
+// 128 rows of keys or values lie in 31 bits.
 constexpr int64_t kMaxKeyStride = int64_t(1) << 23;
 
 convrot_status check_sizes(const convrot_attention& a) {
@@ -31,13 +31,13 @@ convrot_status check_sizes(const convrot_attention& a) {
 }
 
 // The mask's bits, and the parts of split keys: sums, then a maximum and a sum.
-int64_t bits_bytes(const convrot_attention& a) { return a.mask ? (((a.l + 63) / 64 * a.batch + 1) & ~int64_t(1)) * 8 : 0; }
+int64_t bits_bytes(const convrot_attention& a) { return a.mask ? (a.l + 127) / 128 * a.batch * 16 : 0; }
 int64_t workspace_bytes(const convrot_attention& a, const convrot::AttentionPlan& plan) {
   return bits_bytes(a) + (plan.splits > 1 ? plan.splits * a.batch * a.m * a.heads * (a.d + 2) * 4 : 0);
 }
 
 convrot::AttentionPlan plan_of(const convrot_attention& a) {
-  return convrot::plan_attention(a.batch, a.kv_heads, a.m * (a.heads / a.kv_heads), a.l, a.d);
+  return convrot::plan_attention(a.batch, a.kv_heads, a.m * (a.heads / a.kv_heads), a.l);
 }
 
 // A tensor's strides and alignment; `key`: its rows are loaded by tiles.
@@ -108,8 +108,7 @@ convrot_status convrot_attention_apply(const convrot_attention* a, void* stream)
   p.mask_stride = a->mask_stride;
   p.tiles = int(plan.tiles);
   p.splits = plan.splits;
-  p.blocks = plan.blocks;
-  p.waves = plan.waves;
+  p.few = plan.few;
   p.bits = static_cast<uint64_t*>(a->workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + bits_bytes(*a));
   p.stats = p.part + int64_t(plan.splits) * a->batch * a->m * a->heads * a->d;

@@ -23,10 +23,15 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
-constexpr int kKeys = 64;  // keys of a tile
 constexpr float kLog2e = 1.44269504f;
 constexpr float kSlack = 8.f;  // powers of two that a weight may exceed 1 by
 constexpr float kMinusInf = -__builtin_inff();
+
+// Bytes of a key's or value's row in LDS.
+constexpr int row_pitch(int d) { return d <= 64 ? 128 : d <= 128 ? 256 : 512; }
+
+// 64-bit words of a batch entry's mask, in pairs: tiles of 128 keys read whole ones.
+CR_DEVICE int64_t bit_words(int64_t l) { return (l + 127) / 128 * 2; }
 
 // The 16-byte chunk c of row r of a tile lies at slot c ^ swizzle(r).  A
 // fragment of K is one chunk of 32 rows, read 16 lanes at a time (rows that
@@ -72,7 +77,7 @@ CR_DEVICE void scores_mfma(f32x16& s, bf16x8 k, bf16x8 q, const f32x16& start) {
   else if constexpr (FIRST)
     asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %3" : "=&v"(s) : "v"(k), "v"(q), "v"(start));
   else if constexpr (ACC)
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(k), "a"(q));
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(k), "a"(q));
   else
     asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(k), "v"(q));
 }
@@ -101,18 +106,23 @@ CR_DEVICE float other_half(float v) {  // lane ^ 32
 __global__ __launch_bounds__(256) void attention_bits_kernel(const AttentionArgs p, int64_t words) {
   const int64_t w = (p.first + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (w >= words * p.batch) return;
-  const int64_t batch = w / words, at = (w - batch * words) * kKeys + (threadIdx.x & 63);
+  const int64_t batch = w / words, at = (w - batch * words) * 64 + (threadIdx.x & 63);
   const bool seen = at < p.l && p.mask[batch * p.mask_stride + at] != 0;
   const uint64_t bits = __ballot(seen);
   if ((threadIdx.x & 63) == 0) p.bits[w] = bits;
 }
 
-// D: the head's features rounded up to 32.  QB: blocks of 32 queries of a wave.
+// Waves of a workgroup; two tiles of 32 keys for each fill LDS.
+constexpr int attention_waves(int d, bool few) { return few && d > 128 ? 2 : 4; }
+
+// D: the head's features rounded up to 32.  MASK: keys are hidden one by one,
+// not only from a length on.
 //
-// Keys go in blocks of 32; step t multiplies Q with block t + 1 and the
-// weights of block t - 1 with its values, QB D / 8 instructions of 32 cycles,
-// one of each in turn, and turns the scores of block t into weights between
-// them.  K's and V's fragments are read 4 ahead, across steps.
+// A wave has 32 queries.  Keys go in blocks of 32; step t multiplies Q with
+// block t + 1 and the weights of block t - 1 with its values, D / 8
+// instructions of 32 cycles, one of each in turn, and turns the scores of block
+// t into weights between them.  K's and V's fragments are read 4 ahead, across
+// steps.
 //
 // The weights are powers of two relative to a base that follows the maximum
 // only when that has risen by more than kSlack powers of two, which no other
@@ -120,19 +130,28 @@ __global__ __launch_bounds__(256) void attention_bits_kernel(const AttentionArgs
 // same relative precision at 256 as at 1.  So a step takes the base as it is,
 // finds the maximum beside it, and if that has risen too far does its weights
 // again at the end.
-template <int D, int QB, int kWaves, bool MASK>
-__global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void attention_kernel(const AttentionArgs p) {
-  constexpr int kPitch = D <= 64 ? 128 : D <= 128 ? 256 : 512;  // bytes of a row in LDS
+//
+// Tiles of kKeys keys lie in a ring of areas in LDS; a wave goes through a tile
+// in two steps.  FEW: of a workgroup's waves each takes its own block of every
+// tile, in one step, for the same 32 queries, and their sums meet in LDS.
+template <int D, bool FEW, bool MASK>
+__global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 : 1) void attention_kernel(
+    const AttentionArgs p) {
+  constexpr int kWaves = attention_waves(D, FEW);
+  constexpr int kPitch = row_pitch(D);        // bytes of a row in LDS
   constexpr int kChunks = kPitch / 16;
   constexpr int kRowsPiece = 1024 / kPitch;   // rows that one load instruction of a wave brings
+  constexpr int kKeys = FEW ? 32 * kWaves : 64;
   constexpr int kTile = kKeys * kPitch;       // bytes of K, or of V
   constexpr int kPieces = kTile / 1024 / kWaves;
-  constexpr int kRows = kWaves * QB * 32;     // queries of a workgroup
-  constexpr bool kAlone = QB == 2 || D > 128;  // a wave has its SIMD, and all of its registers, to itself
-  constexpr int kRing = kPitch == 512 ? 2 : kPitch == 128 || kAlone ? 3 : 2;  // tiles of K and V in LDS
+  constexpr int kRows = FEW ? 32 : kWaves * 32;  // queries of a workgroup
+  constexpr bool kAcc = D > 128 || FEW;       // (see scores_mfma)
+  constexpr int kRing = 2 * kTile * 3 <= 48 * 1024 ? 3 : 2;
   constexpr int KF = D / 16, NF = D / 32;     // fragments of 32 keys of K; blocks of 32 features of V
-  constexpr int kHalf = KF * QB;              // matrix instructions of each product of a step
+  constexpr int kSlots = 2 * KF;              // matrix instructions of a step
   constexpr int kAhead = KF % 4 == 0 ? 4 : KF / 2;  // fragments read ahead (the next step takes the same registers)
+  constexpr int kLag = FEW ? 2 : 1;           // tiles that an area's V is behind its K
+  static_assert(kRing * 2 * kTile <= 160 * 1024 && (!FEW || kWaves * 32 * (D + 4) * 4 <= kRing * 2 * kTile), "LDS");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * 2 * kTile];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -145,7 +164,8 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   slot /= p.tiles;
   const int head = slot % p.kv_heads, batch = slot / p.kv_heads;
   const int64_t rows = p.m * p.ratio;  // a key head's queries, (token, query head)
-  const int64_t row0 = int64_t(tile) * kRows + wave * QB * 32;
+  const int64_t row0 = int64_t(tile) * kRows + (FEW ? 0 : wave * 32);
+  const int own = FEW ? wave * 32 : 0;  // first row of a tile that the wave reads
 
   int64_t keys = p.l;
   if (p.lengths) {
@@ -157,24 +177,26 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   const uint16_t* kbase = p.k + batch * p.ks[0] + head * p.ks[2];
   const uint16_t* vbase = p.v + batch * p.vs[0] + head * p.vs[2];
   const int dbytes = p.d * 2;
-  typedef const __attribute__((address_space(4))) uint64_t* const_words;
-  const const_words words = (const_words)(p.bits + batch * ((p.l + kKeys - 1) / kKeys));
+  typedef const __attribute__((address_space(4))) uint32_t* const_words;
+  const const_words words = (const_words)(p.bits + batch * bit_words(p.l));
 
-  // The keys of tile t that take part, one bit for each; none behind the last.
-  auto tile_bits = [&](int t) -> uint64_t {
-    const int64_t left = keys - int64_t(t) * kKeys;
-    uint64_t bits = t >= last || left <= 0 ? 0 : left >= kKeys ? ~uint64_t(0) : (uint64_t(1) << left) - 1;
-    if (MASK && t < last) bits &= words[t];
+  // The keys of block `row` / 32 of tile t that take part, one bit for each;
+  // none behind the last.
+  auto block_bits = [&](int t, int row) -> unsigned {
+    const int64_t left = keys - int64_t(t) * kKeys - row;
+    unsigned bits = t >= last || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1;
+    if (MASK && bits != 0) bits &= words[(int64_t(t) * kKeys + row) / 32];
     return bits;
   };
-  // Rows of K (of tile t) and V (of the tile before) into LDS area `to`; hidden
-  // and absent ones read as zero: a score is then what its accumulator starts
-  // from, and a NaN of a hidden value does not meet its weight of zero.  (Rows
-  // behind the last key lie outside the resource: a token's stride is 0 or
-  // holds the row.)  Piece i is 4 i pieces' rows behind
-  // the wave's first; with 512-byte rows that is 8, and K's chunks change places.
+  // Rows of K (of tile t) and V (of the tile kLag before) into LDS area `to`, in
+  // pieces of 1 KB; hidden and absent ones read as zero: a score is then what
+  // its accumulator starts from, and a NaN of a hidden value does not meet its
+  // weight of zero.  (Rows behind the last key lie outside the resource: a
+  // token's stride is 0 or holds the row.)  A wave's piece i is kStep i rows
+  // behind its first; where those are no multiples of 16, K's chunks change places.
   constexpr int kStep = kWaves * kRowsPiece;
-  constexpr int kPlaces = kPitch == 512 ? 2 : 1;
+  constexpr int kPlaces = kStep >= 16 ? 1 : 16 / kStep;
+  static_assert(kStep % 4 == 0 && (kStep % 64 == 0 || 64 % kStep == 0), "places");
   const int prow = wave * kRowsPiece + lane / kChunks;
   unsigned kplace[kPlaces], vplace;
 #pragma unroll
@@ -189,8 +211,8 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   struct {
     const uint16_t *k, *v;
     unsigned kbytes, vbytes;
-    uint64_t kseen, vseen;  // (with a mask)
     unsigned to;
+    uint64_t kseen[kKeys / 64], vseen[kKeys / 64];  // (with a mask)
   } load;
   auto bytes_of = [&](int t, int64_t stride) -> unsigned {  // of tile t's rows, up to the last key
     const int64_t left = t < first || t >= last ? 0 : keys - int64_t(t) * kKeys;
@@ -198,71 +220,70 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   };
   auto begin_load = [&](int t, int to) __attribute__((always_inline)) {
     load.k = kbase + int64_t(t) * kKeys * p.ks[1];
-    load.v = vbase + int64_t(t - 1) * kKeys * p.vs[1];
+    load.v = vbase + int64_t(t - kLag) * kKeys * p.vs[1];
     load.kbytes = bytes_of(t, p.ks[1]);
-    load.vbytes = bytes_of(t - 1, p.vs[1]);
-    if (MASK) {
-      load.kseen = tile_bits(t);
-      load.vseen = t == first ? 0 : tile_bits(t - 1);
-    }
+    load.vbytes = bytes_of(t - kLag, p.vs[1]);
     load.to = unsigned(reinterpret_cast<uintptr_t>((lds_byte*)smem)) + to * 2 * kTile + wave * 1024;
+    if constexpr (MASK) {
+#pragma unroll
+      for (int w = 0; w < kKeys / 64; ++w) {
+        load.kseen[w] = block_bits(t, 64 * w) | uint64_t(block_bits(t, 64 * w + 32)) << 32;
+        load.vseen[w] = t - kLag < first ? 0
+                                         : block_bits(t - kLag, 64 * w) | uint64_t(block_bits(t - kLag, 64 * w + 32)) << 32;
+      }
+    }
   };
   auto piece = [&](int j) __attribute__((always_inline)) {  // K's, then V's
     const bool v = j >= kPieces;
     const int i = v ? j - kPieces : j;
     unsigned at = v ? vplace : kplace[i % kPlaces];
-    if constexpr (MASK) at = ((v ? load.vseen : load.kseen) >> (prow + i * kStep)) & 1 ? at : kOutOfRange;
+    if constexpr (MASK) {
+      const uint64_t seen = (v ? load.vseen : load.kseen)[i * kStep / 64];
+      at = (seen >> ((prow + i * kStep) % 64)) & 1 ? at : kOutOfRange;
+    }
     load_to_lds(v ? load.v : load.k, v ? load.vbytes : load.kbytes, at, i * kStep * int(v ? p.vs[1] : p.ks[1]) * 2,
                 load.to + (v ? kTile : 0) + i * kWaves * 1024);
   };
 
   // Q: lane l holds query l % 32, features 16 t + 8 (l / 32) .. +7.
-  bf16x8 qf[QB][KF];
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const int64_t r = row0 + 32 * b + fr;
-    const int64_t token = p.ratio == 1 ? r : int64_t(unsigned(r) / unsigned(p.ratio));
+  bf16x8 qf[KF];
+  {
+    const int64_t r = row0 + fr;
+    const int64_t token = p.ratio == 1 ? r : int64_t(unsigned(r) / unsigned(p.ratio));  // (rows are below 2^31)
     const int64_t j = r - token * p.ratio;
     const uint16_t* src = p.q + batch * p.qs[0] + token * p.qs[1] + (head * p.ratio + j) * p.qs[2];
 #pragma unroll
     for (int t = 0; t < KF; ++t) {
       const int f = 16 * t + 8 * fh;
-      qf[b][t] = r < rows && f < p.d ? *reinterpret_cast<const bf16x8*>(src + f) : bf16x8{};
+      qf[t] = r < rows && f < p.d ? *reinterpret_cast<const bf16x8*>(src + f) : bf16x8{};
     }
   }
-
-  if constexpr (kAlone) {  // (into the accumulation half, where the products take them)
+  if constexpr (kAcc) {  // (into the accumulation half, where the products take them)
 #pragma unroll
-    for (int b = 0; b < QB; ++b)
-#pragma unroll
-      for (int t = 0; t < KF; ++t) asm volatile("" : "+a"(qf[b][t]));
+    for (int t = 0; t < KF; ++t) asm volatile("" : "+a"(qf[t]));
   }
-  // Tile u's area holds K of tile u and V of tile u - 1: what the two steps
-  // before and at block 2 u read.
+  // Tile u's area holds K of tile u and V of tile u - kLag: what the steps that
+  // make the scores of tile u read.
+  constexpr int kLoads = 2 * kPieces;
   if (first < last) {
 #pragma unroll
     for (int u = 0; u < kRing; ++u) {
       begin_load(first + u, u);
 #pragma unroll
-      for (int j = 0; j < 2 * kPieces; ++j) piece(j);
+      for (int j = 0; j < kLoads; ++j) piece(j);
     }
   }
 
   const float c = p.scale * kLog2e, slack = kSlack / c;
-  f32x16 o[QB][NF] = {}, s[2][QB];
-  u32x4 pf[2][QB][2];
+  f32x16 o[NF] = {}, s[2];
+  u32x4 pf[2][2] = {};
   bf16x8 kf[kAhead], vf[kAhead];
-  float top[QB], total[QB], base[QB], limit[QB];
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    top[b] = limit[b] = kMinusInf;
-    total[b] = base[b] = 0.f;
-  }
+  float top = kMinusInf, limit = kMinusInf, total = 0.f, base = 0.f;
 
-  const int kat = fr * kPitch + ((fh ^ key_swizzle<kPitch>(fr)) << 4);
+  const int kat = (own + fr) * kPitch + ((fh ^ key_swizzle<kPitch>(fr)) << 4);
   const int vrow = 4 * fh + ((lane & 15) >> 2);
-  const int vat = vrow * kPitch + (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<kPitch>(vrow)) << 4) +
-                  (lane & 1) * 8;
+  const int vat = (own + vrow) * kPitch +
+                  (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<kPitch>(vrow)) << 4) + (lane & 1) * 8;
   // Fragments of the area at `at`; `row`: the first of 32 rows.
   auto read_k = [&](int at, int row, int k) __attribute__((always_inline)) {
     kf[k % kAhead] = *(const lds_bf16x8*)((const lds_byte*)smem + ((kat + at) ^ (k << 5)) + row * kPitch);
@@ -276,19 +297,18 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
     vf[j % kAhead] = __builtin_bit_cast(bf16x8, i16x8{part[0][0], part[0][1], part[0][2], part[0][3], part[1][0],
                                                       part[1][1], part[1][2], part[1][3]});
   };
-  float most[QB], sum[QB], held = 0.f;
-  // Score n of block t to a weight, two at a time.
-  auto weigh = [&](int x, int n) __attribute__((always_inline)) {
-    const int b = n / 16, e = n % 16;
-    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][b][e], c, -base[b]));
-    sum[b] = e == 0 ? w : sum[b] + w;
+  // Score e of block t to a weight, two at a time.
+  float most = 0.f, sum = 0.f, held = 0.f;
+  auto weigh = [&](int x, int e) __attribute__((always_inline)) {
+    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][e], c, -base));
+    sum = e == 0 ? w : sum + w;
     if (e % 2 == 0) {
       held = w;
     } else {
       const bf16x2 both = {(__bf16)held, (__bf16)w};
       const unsigned word = __builtin_bit_cast(unsigned, both);
-      asm volatile("" ::"v"(word), "v"(sum[b]));  // (formed here, not where the compiler would collect them)
-      pf[x][b][e / 8][e % 8 / 2] = word;
+      asm volatile("" ::"v"(word), "v"(sum));  // (formed here, not where the compiler would collect them)
+      pf[x][e / 8][e % 8 / 2] = word;
     }
   };
   // What the scores of a block start from: zero, minus infinity where the key is hidden.
@@ -304,26 +324,25 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
         start[e] = __uint_as_float(unsigned(__builtin_amdgcn_sbfe(int(hidden), 8 * (e / 4) + e % 4, 1)) & 0xFF800000u);
     }
   };
-  // A block's maximum so far, with scores [n]; at the end over both halves of the wave.
-  auto maximum = [&](int x, int n) __attribute__((always_inline)) {
-    const int b = n / 16, e = n % 16;
-    most[b] = e == 0 ? s[x][b][0] : fmaxf(most[b], s[x][b][e]);
-    if (e == 15) most[b] = fmaxf(most[b], other_half(most[b]));
+  // A block's maximum so far, with score e; at the end over both halves of the wave.
+  auto maximum = [&](int x, int e) __attribute__((always_inline)) {
+    most = e == 0 ? s[x][0] : fmaxf(most, s[x][e]);
+    if (e == 15) most = fmaxf(most, other_half(most));
   };
-
-  auto score = [&](f32x16& to, auto first_t, int b, int f) __attribute__((always_inline)) {
-    scores_mfma<decltype(first_t)::value, kAlone>(to, kf[f % kAhead], qf[b][f], start);
+  auto score = [&](f32x16& to, auto first_t, int f) __attribute__((always_inline)) {
+    scores_mfma<decltype(first_t)::value, kAcc>(to, kf[f % kAhead], qf[f], start);
+    // The first product reads `start` after it has been issued, for 11 wait
+    // states that the compiler does not know of: the registers stay taken.
+    if (f == KF - 1) asm volatile("" ::"v"(start));
   };
-  auto output = [&](int x, int b, int f) __attribute__((always_inline)) {
-    output_mfma<kAlone>(o[b][f % NF], vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[x][b][f / NF]));
+  auto output = [&](int x, int f) __attribute__((always_inline)) {
+    output_mfma<kAcc>(o[f % NF], vf[f % kAhead], __builtin_bit_cast(bf16x8, pf[x][f / NF]));
   };
   auto settled = [&]() __attribute__((always_inline)) {  // before the output's sums are read
     asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int b = 0; b < QB; ++b)
-#pragma unroll
-      for (int n = 0; n < NF; ++n) mfma_settle<kAlone>(o[b][n]);
+    for (int n = 0; n < NF; ++n) mfma_settle<kAcc>(o[n]);
   };
 
   // The step with the scores and weights of set X, on rows ROW .. of the area at
@@ -332,30 +351,30 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   // CROSS: that is another area, which has landed once only the loads behind
   // it may be in flight, and this one, which every wave has then read, is
   // given up to the loads that begin() names: at slot kSync, two behind the
-  // last reads.  The loads go one by one into the slots from there to the
-  // middle of the next step: the
-  // memory path takes 16 cycles of a CU for each, and a wave whose loads stand
-  // in line issues nothing else (4096 x 8192, 64 heads of 128: 4180 cycles for
-  // 64 keys with the loads all at once).
-  constexpr int kSync = 2 * (KF - kAhead) * QB + 2;
-  constexpr int kEvery = 4 * kPieces <= 2 * kHalf ? 2 : 1;  // slots to a load
+  // last reads.  The loads go one by one into the kSpan slots from there on,
+  // the next step's among them: the memory path takes 16 cycles of a CU for
+  // each, and a wave whose loads stand in line issues nothing else (4096 x
+  // 8192, 64 heads of 128: 1110 us with the loads all at once, 1020 so).
+  constexpr int kSync = 2 * (KF - kAhead) + 2;
+  constexpr int kRest = kSlots - kSync - 1;            // a step's slots behind kSync
+  constexpr int kMost = FEW ? kSlots - 1 : kSlots + kRest;  // (up to the next kSync, or its step)
+  constexpr int kSpan = 2 * kLoads < kMost ? 2 * kLoads : kMost;
   // QK, PV: which of the products there are (the first and the last step lack one).
   auto step = [&](auto x_t, auto qk_t, auto pv_t, auto row_t, auto cross_t, int at, int nat, unsigned bits,
                   auto&& begin) __attribute__((always_inline)) {
-    constexpr int X = decltype(x_t)::value, Y = 1 - X, ROW = decltype(row_t)::value, NROW = 32 - ROW;
+    constexpr int X = decltype(x_t)::value, Y = 1 - X, ROW = decltype(row_t)::value, NROW = FEW ? 0 : 32 - ROW;
     constexpr bool QK = decltype(qk_t)::value, PV = decltype(pv_t)::value, CROSS = decltype(cross_t)::value;
     if (QK) hide(bits);
-    for_each_index(std::make_integer_sequence<int, 2 * kHalf>{}, [&](auto i_t) __attribute__((always_inline)) {
-      constexpr int i = decltype(i_t)::value;
+    for_each_index(std::make_integer_sequence<int, kSlots>{}, [&](auto i_t) __attribute__((always_inline)) {
+      constexpr int i = decltype(i_t)::value, f = i / 2;
       constexpr bool K = i % 2 == 0;
-      constexpr int b = i / 2 % QB, f = i / 2 / QB;  // the query block and fragment
       if constexpr (K && QK)
-        score(s[Y][b], std::integral_constant<bool, f == 0>{}, b, f);
+        score(s[Y], std::integral_constant<bool, f == 0>{}, f);
       else if constexpr (!K && PV)
-        output(Y, b, f);
+        output(Y, f);
       if (i < 2) __builtin_amdgcn_sched_barrier(0);  // (block t's last scores take that long)
-      // The fragment 4 ahead, of this step's rows or the next one's.
-      if constexpr (b == QB - 1 && f + kAhead < KF) {
+      // The fragment kAhead ahead, of this step's rows or the next one's.
+      if constexpr (f + kAhead < KF) {
         if constexpr (K && QK)
           read_k(at, ROW, f + kAhead);
         else if constexpr (!K && PV)
@@ -363,17 +382,21 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
       }
       if constexpr (CROSS && i == kSync) {
         wait_lgkm0();
-        waitvm<(kRing - 2) * 2 * kPieces>();
+        waitvm<(kRing - 2) * kLoads>();
         barrier();
         begin();
       }
-      if constexpr (QK) {
-        constexpr int n = CROSS ? i - kSync - 1 : i + 2 * kHalf - kSync - 1;  // slots since then
-        if constexpr (n >= 0 && n % kEvery == 0 && n / kEvery < 2 * kPieces) piece(n / kEvery);
+      if constexpr (QK || (FEW && i <= kSync)) {
+        constexpr int n = CROSS && i > kSync ? i - kSync - 1 : CROSS && !FEW ? kSpan : i + kRest;  // slots since kSync
+        if constexpr (n < kSpan)
+          for_each_index(std::make_integer_sequence<int, kLoads>{}, [&](auto j_t) __attribute__((always_inline)) {
+            constexpr int j = decltype(j_t)::value;
+            if constexpr (j * kSpan / kLoads == n) piece(j);
+          });
       }
       auto next = [&](auto j_t) __attribute__((always_inline)) {  // what slot j frees the registers for
-        constexpr int j = decltype(j_t)::value, jf = j / 2 / QB + kAhead - KF;
-        if constexpr (j / 2 % QB == QB - 1 && jf >= 0) {
+        constexpr int j = decltype(j_t)::value, jf = j / 2 + kAhead - KF;
+        if constexpr (jf >= 0) {
           if constexpr (j % 2 == 0 && QK)
             read_k(nat, NROW, jf);
           else if constexpr (j % 2 == 1)
@@ -383,39 +406,31 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
       if constexpr (!CROSS || i > kSync) next(i_t);
       if constexpr (CROSS && i == kSync)
         for_each_index(std::make_integer_sequence<int, kSync + 1>{}, next);
-      constexpr int lo = 16 * QB * i / (2 * kHalf), hi = 16 * QB * (i + 1) / (2 * kHalf);
+      constexpr int lo = 16 * i / kSlots, hi = 16 * (i + 1) / kSlots;
 #pragma unroll
-      for (int n = lo; n < hi; ++n) weigh(X, n);
-      // (the maximum within three quarters of the step)
-      constexpr int span = 3 * kHalf / 2;
-      constexpr int mlo = i < span ? 16 * QB * i / span : 16 * QB, mhi = i < span ? 16 * QB * (i + 1) / span : 16 * QB;
+      for (int e = lo; e < hi; ++e) weigh(X, e);
+      constexpr int span = 3 * kSlots / 4;  // (the maximum within three quarters of the step)
+      constexpr int mlo = i < span ? 16 * i / span : 16, mhi = i < span ? 16 * (i + 1) / span : 16;
 #pragma unroll
-      for (int n = mlo; n < mhi; ++n) maximum(X, n);
+      for (int e = mlo; e < mhi; ++e) maximum(X, e);
       __builtin_amdgcn_sched_barrier(0);
     });
-    bool more = false;
-#pragma unroll
-    for (int b = 0; b < QB; ++b) more |= most[b] > limit[b];
-    if (__ballot(more) != 0) {
+    if (__ballot(most > limit) != 0) {
       settled();
+      const float now = fmaxf(top, most);
+      base = now == kMinusInf ? 0.f : now * c;
+      const float shrink = __builtin_amdgcn_exp2f(__builtin_fmaf(top, c, -base));
+      top = now;
+      limit = now + slack;
+      total *= shrink;
+      if (PV) {
 #pragma unroll
-      for (int b = 0; b < QB; ++b) {
-        const float now = fmaxf(top[b], most[b]);
-        base[b] = now == kMinusInf ? 0.f : now * c;
-        const float shrink = __builtin_amdgcn_exp2f(__builtin_fmaf(top[b], c, -base[b]));
-        top[b] = now;
-        limit[b] = now + slack;
-        total[b] *= shrink;
-        if (PV) {
-#pragma unroll
-          for (int n = 0; n < NF; ++n) o[b][n] *= shrink;
-        }
+        for (int n = 0; n < NF; ++n) o[n] *= shrink;
       }
 #pragma unroll
-      for (int n = 0; n < 16 * QB; ++n) weigh(X, n);
+      for (int e = 0; e < 16; ++e) weigh(X, e);
     }
-#pragma unroll
-    for (int b = 0; b < QB; ++b) total[b] += sum[b];
+    total += sum;
   };
 
   // (opaque, so that addresses are formed where they are used and not kept for every area)
@@ -429,102 +444,176 @@ __global__ __launch_bounds__(kWaves * 64, QB == 1 && D <= 128 ? 2 : 1) void atte
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   using I32 = std::integral_constant<int, 32>;
+  // The last block's values, on rows ROW .. of the area at `at`.
+  auto finish = [&](int x, int at, int row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < KF; ++f) {
+      output(x, f);
+      if (f + kAhead < KF) read_v(at, row, f + kAhead);
+    }
+    settled();
+  };
 
   if (first < last) {
     int at = area(first), to = area(first + 1);
-    waitvm<(kRing - 1) * 2 * kPieces>();
+    waitvm<(kRing - 1) * kLoads>();
     barrier();
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) read_k(at, 0, k);
-    uint64_t bits = tile_bits(first);
-    hide(unsigned(bits));
+    hide(block_bits(first, own));
     for_each_index(std::make_integer_sequence<int, KF>{}, [&](auto f_t) __attribute__((always_inline)) {
       constexpr int f = decltype(f_t)::value;
-#pragma unroll
-      for (int b = 0; b < QB; ++b) score(s[0][b], std::integral_constant<bool, f == 0>{}, b, f);
+      score(s[0], std::integral_constant<bool, f == 0>{}, f);
       if constexpr (f + kAhead < KF)
         read_k(at, 0, f + kAhead);
-      else
+      else if constexpr (!FEW)
         read_k(at, 32, f + kAhead - KF);
     });
+    asm volatile("s_nop 15\n\ts_nop 3" : "+v"(s[0]));
+    // (Neither loop tests first: round one the compiler keeps two sets of the output's sums.)
+    if constexpr (FEW) {
+      wait_lgkm0();
+      waitvm<(kRing - 2) * kLoads>();
+      barrier();
+      begin_load(first + kRing, 0);
 #pragma unroll
-    for (int b = 0; b < QB; ++b) asm volatile("s_nop 15\n\ts_nop 3" : "+v"(s[0][b]));
-    step(I0{}, Yes{}, No{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
-         [&]() __attribute__((always_inline)) { begin_load(first + kRing, 0); });
-    // (not a loop that tests first: round one the compiler keeps two sets of the output's sums)
-    int u = first + 1;
-    if (u < last) do {
-      at = to;
-      to = area(u + 1);
-      bits = tile_bits(u);
-      step(I1{}, Yes{}, Yes{}, I0{}, No{}, at, at, unsigned(bits), []() {});
-      step(I0{}, Yes{}, Yes{}, I32{}, Yes{}, at, to, unsigned(bits >> 32),
-           [&]() __attribute__((always_inline)) { begin_load(u + kRing, (u - first) % kRing); });
-    } while (++u < last);
-    step(I1{}, No{}, Yes{}, I0{}, No{}, to, to, 0u, []() {});
+      for (int j = 0; j < kLoads; ++j)
+        if (j * kSpan / kLoads < kRest) piece(j);  // (the others in the first step)
 #pragma unroll
-    for (int f = 0; f < KF; ++f) {
-#pragma unroll
-      for (int b = 0; b < QB; ++b) output(1, b, f);
-      if (f + kAhead < KF) read_v(to, 32, f + kAhead);
+      for (int k = 0; k < kAhead; ++k) {
+        read_k(to, 0, k);
+        read_v(to, 0, k);
+      }
+      // Step t makes the scores of tile t + 1, so it reads that one's area.
+      int u = first + 1;
+      auto go = [&](auto x_t) __attribute__((always_inline)) {
+        at = to;
+        to = area(u + 1);
+        step(x_t, Yes{}, Yes{}, I0{}, Yes{}, at, to, block_bits(u, own),
+             [&]() __attribute__((always_inline)) { begin_load(u + kRing, (u - first) % kRing); });
+        ++u;
+      };
+      if (u + 1 < last) do {
+        go(I0{});
+        go(I1{});
+      } while (u + 1 < last);
+      auto end = [&](auto x_t) __attribute__((always_inline)) {
+        at = to;
+        to = area(u + 1);
+        step(x_t, No{}, Yes{}, I0{}, Yes{}, at, to, 0u, []() {});
+        finish(decltype(x_t)::value, to, 0);
+      };
+      if (u < last) {
+        go(I0{});
+        end(I1{});
+      } else {
+        end(I0{});
+      }
+    } else {
+      step(I0{}, Yes{}, No{}, I32{}, Yes{}, at, to, block_bits(first, 32),
+           [&]() __attribute__((always_inline)) { begin_load(first + kRing, 0); });
+      int u = first + 1;
+      if (u < last) do {
+        at = to;
+        to = area(u + 1);
+        step(I1{}, Yes{}, Yes{}, I0{}, No{}, at, at, block_bits(u, 0), []() {});
+        step(I0{}, Yes{}, Yes{}, I32{}, Yes{}, at, to, block_bits(u, 32),
+             [&]() __attribute__((always_inline)) { begin_load(u + kRing, (u - first) % kRing); });
+      } while (++u < last);
+      step(I1{}, No{}, Yes{}, I0{}, No{}, to, to, 0u, []() {});
+      finish(1, to, 32);
     }
-    settled();
     waitvm<0>();  // no load into LDS may be in flight where the outputs go through it
     wait_lgkm0();
     barrier();
   }
 
   // Register e of block n: feature 32 n + 8 (e / 4) + 4 (lane / 32) + e % 4 of query lane % 32.
-  auto place = [&](int64_t r, int64_t* token, int* j) __attribute__((always_inline)) {
-    *token = p.ratio == 1 ? r : int64_t(unsigned(r) / unsigned(p.ratio));  // (rows are below 2^31)
-    *j = int(r - *token * p.ratio);
+  auto out_row = [&](int64_t r) __attribute__((always_inline)) {
+    const int64_t token = p.ratio == 1 ? r : int64_t(unsigned(r) / unsigned(p.ratio));
+    return p.out + batch * p.os[0] + token * p.os[1] + (head * p.ratio + r - token * p.ratio) * p.os[2];
   };
-  uint8_t* mine = smem + wave * QB * 32 * kPitch;
+  const int64_t part0 = ((int64_t(split) * p.batch + batch) * p.kv_heads + head) * rows;  // row of the parts
+  const float all_sum = total + other_half(total);
+  if constexpr (FEW) {
+    // The waves' sums, in their order, by all threads.
+    constexpr int kRow = D + 4;  // (a row's distance in floats: 16 bytes off the banks of the one before)
+    float* sums = reinterpret_cast<float*>(smem) + wave * 32 * kRow;
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const float sum = total[b] + other_half(total[b]);
-    if (p.splits > 1) {
-      const int64_t r = row0 + 32 * b + fr;
-      if (r >= rows) continue;
-      const int64_t at = ((int64_t(split) * p.batch + batch) * p.kv_heads + head) * rows + r;
-      float* dst = p.part + at * p.d;
-      if (fh == 0) {
-        p.stats[2 * at] = top[b] == kMinusInf ? kMinusInf : base[b];
-        p.stats[2 * at + 1] = sum;
-      }
+    for (int n = 0; n < NF; ++n)
 #pragma unroll
-      for (int n = 0; n < NF; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int f = 32 * n + 8 * q + 4 * fh;
-          if (f < p.d)
-            *reinterpret_cast<f32x4*>(dst + f) =
-                f32x4{o[b][n][4 * q], o[b][n][4 * q + 1], o[b][n][4 * q + 2], o[b][n][4 * q + 3]};
-        }
-    } else {
-      const float f = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-      for (int n = 0; n < NF; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<u32x2*>(mine + (32 * b + fr) * kPitch + (((4 * n + q) ^ key_swizzle<kPitch>(fr)) << 4) +
-                                    8 * fh) =
-              u32x2{bf16_pair(o[b][n][4 * q] * f, o[b][n][4 * q + 1] * f),
-                    bf16_pair(o[b][n][4 * q + 2] * f, o[b][n][4 * q + 3] * f)};
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(sums + fr * kRow + 32 * n + 8 * q + 4 * fh) =
+            f32x4{o[n][4 * q], o[n][4 * q + 1], o[n][4 * q + 2], o[n][4 * q + 3]};
+    if (fh == 0) {
+      sums[fr * kRow + D] = top == kMinusInf ? kMinusInf : base;
+      sums[fr * kRow + D + 1] = all_sum;
     }
-  }
-  if (p.splits > 1) return;
-  // Whole rows out of the wave's own part of LDS (whose accesses stay in order).
+    __syncthreads();
+    const int chunks = p.d / 8;
+    for (int i = threadIdx.x; i < 32 * chunks; i += kWaves * 64) {
+      const int row = i / chunks, f = (i - row * chunks) * 8;
+      if (row0 + row >= rows) break;
+      const float* at = reinterpret_cast<const float*>(smem) + row * kRow;
+      float most = kMinusInf;
 #pragma unroll
-  for (int i = 0; i < QB * 32 / (64 / kChunks); ++i) {
-    const int row = i * (64 / kChunks) + lane / kChunks, chunk = lane % kChunks;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kPitch + ((chunk ^ key_swizzle<kPitch>(row & 31)) << 4));
-    const int64_t r = row0 + row;
-    if (r < rows && chunk * 16 < dbytes) {
-      int64_t token;
-      int j;
-      place(r, &token, &j);
-      *reinterpret_cast<u32x4*>(p.out + batch * p.os[0] + token * p.os[1] + (head * p.ratio + j) * p.os[2] + chunk * 8) = v;
+      for (int w = 0; w < kWaves; ++w) most = fmaxf(most, at[w * 32 * kRow + D]);
+      f32x4 lo = {}, hi = {};
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float* src = at + w * 32 * kRow;
+        const float weight = __builtin_amdgcn_exp2f(src[D] - (most == kMinusInf ? 0.f : most));
+        sum += weight * src[D + 1];
+        lo += weight * *reinterpret_cast<const f32x4*>(src + f);
+        hi += weight * *reinterpret_cast<const f32x4*>(src + f + 4);
+      }
+      if (p.splits > 1) {
+        float* dst = p.part + (part0 + row0 + row) * p.d + f;
+        *reinterpret_cast<f32x4*>(dst) = lo;
+        *reinterpret_cast<f32x4*>(dst + 4) = hi;
+        if (f == 0) {
+          p.stats[2 * (part0 + row0 + row)] = most;
+          p.stats[2 * (part0 + row0 + row) + 1] = sum;
+        }
+      } else {
+        const float g = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<u32x4*>(out_row(row0 + row) + f) =
+            u32x4{bf16_pair(lo[0] * g, lo[1] * g), bf16_pair(lo[2] * g, lo[3] * g), bf16_pair(hi[0] * g, hi[1] * g),
+                  bf16_pair(hi[2] * g, hi[3] * g)};
+      }
+    }
+  } else if (p.splits > 1) {
+    const int64_t r = row0 + fr;
+    if (r >= rows) return;
+    float* dst = p.part + (part0 + r) * p.d;
+    if (fh == 0) {
+      p.stats[2 * (part0 + r)] = top == kMinusInf ? kMinusInf : base;
+      p.stats[2 * (part0 + r) + 1] = all_sum;
+    }
+#pragma unroll
+    for (int n = 0; n < NF; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int f = 32 * n + 8 * q + 4 * fh;
+        if (f < p.d)
+          *reinterpret_cast<f32x4*>(dst + f) = f32x4{o[n][4 * q], o[n][4 * q + 1], o[n][4 * q + 2], o[n][4 * q + 3]};
+      }
+  } else {
+    // Whole rows out of the wave's own part of LDS (whose accesses stay in order).
+    uint8_t* mine = smem + wave * 32 * kPitch;
+    const float g = all_sum == 0.f ? 0.f : 1.f / all_sum;
+#pragma unroll
+    for (int n = 0; n < NF; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<u32x2*>(mine + fr * kPitch + (((4 * n + q) ^ key_swizzle<kPitch>(fr)) << 4) + 8 * fh) =
+            u32x2{bf16_pair(o[n][4 * q] * g, o[n][4 * q + 1] * g), bf16_pair(o[n][4 * q + 2] * g, o[n][4 * q + 3] * g)};
+#pragma unroll
+    for (int i = 0; i < 32 / (64 / kChunks); ++i) {
+      const int row = i * (64 / kChunks) + lane / kChunks, chunk = lane % kChunks;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kPitch + ((chunk ^ key_swizzle<kPitch>(row)) << 4));
+      if (row0 + row < rows && chunk * 16 < dbytes) *reinterpret_cast<u32x4*>(out_row(row0 + row) + chunk * 8) = v;
     }
   }
 }
@@ -554,22 +643,23 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
       u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
-template <int D, int QB, int kWaves>
+template <int D, bool FEW>
 hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
+  constexpr int kThreads = attention_waves(D, FEW) * 64;
   AttentionArgs p = a;
   if (a.mask) {
-    const int64_t words = (a.l + kKeys - 1) / kKeys;
+    const int64_t words = (a.l + 127) / 128 * 2;
     in_launches((words * a.batch + 3) / 4, 256, [&](int64_t first, unsigned count) {
       p.first = first;
       hipLaunchKernelGGL(attention_bits_kernel, dim3(count), dim3(256), 0, stream, p, words);
     });
   }
-  in_launches(a.batch * a.kv_heads * a.tiles * a.splits, kWaves * 64, [&](int64_t first, unsigned count) {
+  in_launches(a.batch * a.kv_heads * a.tiles * a.splits, kThreads, [&](int64_t first, unsigned count) {
     p.first = first;
     if (a.mask)
-      hipLaunchKernelGGL((attention_kernel<D, QB, kWaves, true>), dim3(count), dim3(kWaves * 64), 0, stream, p);
+      hipLaunchKernelGGL((attention_kernel<D, FEW, true>), dim3(count), dim3(kThreads), 0, stream, p);
     else
-      hipLaunchKernelGGL((attention_kernel<D, QB, kWaves, false>), dim3(count), dim3(kWaves * 64), 0, stream, p);
+      hipLaunchKernelGGL((attention_kernel<D, FEW, false>), dim3(count), dim3(kThreads), 0, stream, p);
   });
   if (a.splits > 1) {
     const int64_t values = a.batch * a.kv_heads * a.m * a.ratio * (a.d / 4);
@@ -580,32 +670,40 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int D>
+hipError_t launch_d(const AttentionArgs& a, hipStream_t stream) {
+  return a.few ? launch_t<D, true>(a, stream) : launch_t<D, false>(a, stream);
+}
+
 }  // namespace
 
-AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d) {
+AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l) {
   AttentionPlan plan{};
-  plan.blocks = 1;
-  plan.waves = 4;
-  const int tile_rows = plan.waves * 32 * plan.blocks;
+  const int64_t cus = device_cu_count(), heads = batch * kv_heads;
+  auto blocks = [&](int64_t n) { return heads * ((rows + n - 1) / n); };
+  // The waves of a workgroup take the same queries where no more workgroups
+  // than CUs come of it: 1 x 32760, 40 query heads on 8 of 128, 42.7 us against
+  // 44.5; 64 x 32760, 8 heads, 41.4 against 46.3; 300 x 2000, 8 heads, 19.1
+  // against 22.4.  With up to twice as many, 2000 x 333, 8 heads: 19.9 against 13.8.
+  plan.few = blocks(32) <= cus;
+  const int64_t tile_rows = plan.few ? 32 : 128;
   plan.tiles = (rows + tile_rows - 1) / tile_rows;
   plan.splits = 1;
-  const int64_t blocks = batch * kv_heads * plan.tiles, cus = device_cu_count();
-  const int64_t key_tiles = (l + kKeys - 1) / kKeys;
-  if (blocks > 0 && blocks < cus) {
-    int64_t want = cus / blocks;
-    if (want > key_tiles / 2) want = key_tiles / 2;
+  const int64_t key_tiles = (l + 127) / 128;
+  if (heads * plan.tiles > 0 && heads * plan.tiles < cus) {
+    int64_t want = cus / (heads * plan.tiles);
+    if (want > key_tiles / 4) want = key_tiles / 4;
     if (want > 1) plan.splits = int(want);
   }
   return plan;
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream) {
-  const bool two = a.blocks == 2;
-  if (a.d <= 64) return two ? launch_t<64, 2, 4>(a, stream) : launch_t<64, 1, 4>(a, stream);
-  if (a.d <= 96) return two ? launch_t<96, 2, 4>(a, stream) : launch_t<96, 1, 4>(a, stream);
-  if (a.d <= 128) return two ? launch_t<128, 2, 4>(a, stream) : launch_t<128, 1, 4>(a, stream);
-  if (a.d <= 160) return launch_t<160, 1, 4>(a, stream);
-  return launch_t<192, 1, 4>(a, stream);
+  if (a.d <= 64) return launch_d<64>(a, stream);
+  if (a.d <= 96) return launch_d<96>(a, stream);
+  if (a.d <= 128) return launch_d<128>(a, stream);
+  if (a.d <= 160) return launch_d<160>(a, stream);
+  return launch_d<192>(a, stream);
 }
 
 }  // namespace convrot

@@ -237,17 +237,17 @@ struct AttentionArgs {
   int64_t mask_stride;
   float* part;   // [splits][batch][kv_heads][m ratio][d] where the keys are split
   float* stats;  // ... and the maximum (in powers of two) and sum of each row
-  uint64_t* bits;  // [batch][ceil(l / 64)], with a mask: its bits
-  int tiles, splits, blocks, waves;
+  uint64_t* bits;  // [batch][2 ceil(l / 128)], with a mask: its bits
+  int tiles, splits;
+  bool few;
   int64_t first;  // workgroup of the launch's first one
 };
 struct AttentionPlan {
   int64_t tiles;  // of a key head's queries
   int splits;     // of the keys
-  int blocks;     // of 32 queries of a wave
-  int waves;      // of a workgroup
+  bool few;       // the waves of a workgroup share 32 queries (else each has 32)
 };
-AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d);
+AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
 
 }  // namespace convrot

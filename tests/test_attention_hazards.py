@@ -2,8 +2,9 @@
 need, in both register files and round the loops (CPU).
 
 As test_matrix_registers.py, for v_mfma_f32_32x32x16_bf16: no vector instruction writes an operand less
-than 2 wait states before it, and nothing touches its result for 18 wait states, but another of these
-instructions onto the same sums may follow at any distance.  Each occupies the matrix core for 8.
+than 2 wait states before it, nothing touches its result for 18 wait states, but another of these
+instructions onto the same sums may follow at any distance, and nothing writes what it adds to for 11: it
+reads that after it has been issued.  Each occupies the matrix core for 8.
 
 Skipped when the library has not been built or there is no disassembler.
 """
@@ -20,7 +21,7 @@ from test_matrix_hazards import OBJDUMP
 
 MFMA = "v_mfma_f32_32x32x16_bf16"
 NAME = re.compile(r"attention_kernelILi")
-OPERAND_STATES, RESULT_STATES, MFMA_STATES = 2, 18, 8
+OPERAND_STATES, RESULT_STATES, ADDEND_STATES, MFMA_STATES = 2, 18, 11, 8
 
 
 def _hazards(ins):
@@ -50,6 +51,16 @@ def _hazards(ins):
             if p.uses & m.result and not onto:
                 found.append(f"{m.text} <- {p.text}")
             open_ += [(q, states + (MFMA_STATES if p.mfma else p.states())) for q in p.after]
+        addend = registers._registers(registers._fields(m.text)[1][3]) - m.result
+        open_, seen = [(p, 0) for p in m.after], {}
+        while open_:
+            p, states = open_.pop()
+            if states >= ADDEND_STATES or seen.get(p, ADDEND_STATES) <= states:
+                continue
+            seen[p] = states
+            if p.writes & addend:
+                found.append(f"{m.text} overwritten by {p.text}")
+            open_ += [(q, states + (MFMA_STATES if p.mfma else p.states())) for q in p.after]
     return count, found
 
 
@@ -67,6 +78,9 @@ def test_planted_hazards_are_seen():
     assert not seen(score, other, "s_nop 9", "v_fma_f32 v60, v3, v61, v62")
     assert not seen(score, score) and seen(score, MFMA + " a[16:31], v[0:3], v[40:43], a[16:31]")
     assert seen(other, "v_accvgpr_read_b32 v60, a20")
+    first = MFMA + " v[0:15], v[32:35], a[0:3], v[16:31]"
+    assert seen(first, "v_add_u32_e32 v30, s74, v115") and seen(first, other, "v_add_u32_e32 v30, s74, v115")
+    assert not seen(first, "s_nop 10", "v_add_u32_e32 v30, s74, v115")
 
 
 def test_built_code_keeps_its_distances(tmp_path):
@@ -97,7 +111,7 @@ def test_built_code_keeps_its_distances(tmp_path):
                 assert branch == bool(target), ln
                 kernels[name].append((address, ins.strip(), start + int(target[1] or "0", 16) if branch else None))
     kernels = {name: registers._kernel(lines) for name, lines in kernels.items() if NAME.search(name)}
-    assert len(kernels) >= 10  # for each size of heads, with and without a mask
+    assert len(kernels) == 20  # for 5 sizes of heads, with and without a mask, few and many queries
     for name, ins in kernels.items():
         count, found = _hazards(ins)
         assert count >= 16, (name, count)
