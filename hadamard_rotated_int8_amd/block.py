@@ -404,6 +404,27 @@ def fp8_transpose_weights(ws) -> Fp8Weights:
     return Fp8Weights(q, scale)
 
 
+def _whole_rounds(m: int, w: Fp8Weights, dev) -> int:
+    """How many of W's rows to take first where the linear is better made as two, else 0.
+
+    The kernel for many tiles gives each CU one tile of 256 rows by 256 (float32 scales: 128) columns
+    at a time, and a last round of few tiles takes as long as any.  The rounds that fill all CUs go
+    first; what is left goes in the tiles of 128 x 128 of the other kernel, if those are no more than
+    two to a CU (float32 scales: one).  4096 x 27648 -> 5120: 632 us in two rounds; 338 for the first
+    4096 columns and 123 for the others.  16384 x 8192 -> 2560, as many as two to a CU: 286 and 260.
+    float32 scales: 4096 x 27648 -> 5120 699 and 636, 600 x 10240 -> 20480, beyond one: 169 and 171.
+    """
+    wide = 128 if w.scale.dtype == torch.float32 else 256
+    n, rows = w.q.shape[0], -(-m // 256)
+    cus = torch.cuda.get_device_properties(dev).multi_processor_count
+    tiles = rows * -(-n // wide)
+    if tiles <= cus or tiles % cus == 0:
+        return 0
+    at = tiles // cus * cus // rows * wide
+    rest = -(-m // 128) * -(-(n - at) // 128)
+    return at if rest <= cus * wide // 128 else 0
+
+
 def fp8_gated_backward(dy: torch.Tensor, kept, back: Fp8Weights, act: str = "silu"):
     """The way back through ``fp8_gated``: (dX, (dG, dU)), all bfloat16.
 
@@ -439,7 +460,11 @@ def fp8_gated_backward(dy: torch.Tensor, kept, back: Fp8Weights, act: str = "sil
             _GATED_BACKWARD.pack(dy.data_ptr(), kept[0].data_ptr(), kept[1].data_ptr(), dgate.data_ptr(),
                                  dup.data_ptr(), ctypes.addressof(pk), m, n, _row_stride(dy),
                                  _row_stride(kept[0]), n, dt, code))
-    return fp8_linear(packed, back, out_dtype=torch.bfloat16), (dgate, dup)
+    dx = torch.empty((m, back.q.shape[0]), dtype=torch.bfloat16, device=dev)
+    at = _whole_rounds(m, back, dev)
+    for lo, hi in ((0, at), (at, back.q.shape[0])) if at else ((0, back.q.shape[0]),):
+        fp8_linear(packed, Fp8Weights(back.q[lo:hi], back.scale[lo // FP8_BLOCK:_blocks(hi)]), dx[:, lo:hi])
+    return dx, (dgate, dup)
 
 
 # ---------------------------------------------------------------------------

@@ -267,7 +267,8 @@ def test_projection_gradients(m, n, dtype, act):
 
 
 @SCALES
-@pytest.mark.parametrize("m, k, n", [(1, 16, 1), (5, 400, 130), (70, 1040, 1000), (33, 144, 2049), (1030, 1024, 1500)])
+@pytest.mark.parametrize("m, k, n", [(1, 16, 1), (5, 400, 130), (70, 1040, 1000), (33, 144, 2049), (1030, 1024, 1500),
+                                     (4100, 4336, 200)])
 def test_gradient_at_x(m, k, n, scale):
     gate, up = _weights(n, k, scale, 1), _weights(n, k, scale, 2)
     back = cr.fp8_transpose_weights([gate, up])
@@ -276,6 +277,8 @@ def test_gradient_at_x(m, k, n, scale):
     wd = _dequantised(back)
     assert torch.equal(wd[:, :n], _dequantised(gate).t()) and torch.equal(wd[:, np:np + n], _dequantised(up).t())
     assert (wd[:, n:np] == 0).all() and (wd[:, np + n:] == 0).all()
+    if m > 4096 and torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert impl._whole_rounds(m, back, torch.device("cuda", 0)) == 3840  # two products
     dy, kept = _kept(m, n, m + n)
     packed, outs = _packed_gradients(dy, kept, "silu")
     dx, grads = cr.fp8_gated_backward(dy, kept, back)
