@@ -84,6 +84,6 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | 
             0 if lengths is None else lengths.data_ptr(), 0 if mask is None else mask.data_ptr(),
             mask_stride, 0, 0]
     packed, space = _workspace(lib().convrot_attention_workspace, "convrot_attention_workspace", args,
-                               _ATTENTION, dev, (batch, m, l, heads, kv_heads, d, mask is not None))
+                               _ATTENTION, dev, (batch, m, l, heads, kv_heads, d))
     _launch(lib().convrot_attention_apply, "convrot_attention_apply", dev, packed)
     return out

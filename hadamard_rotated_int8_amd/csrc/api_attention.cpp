@@ -30,10 +30,9 @@ convrot_status check_sizes(const convrot_attention& a) {
   return a.d % 8 == 0 ? CONVROT_OK : CONVROT_ERR_UNSUPPORTED;
 }
 
-// The mask's bits, and the parts of split keys: sums, then a maximum and a sum.
-int64_t bits_bytes(const convrot_attention& a) { return a.mask ? (a.l + 127) / 128 * a.batch * 16 : 0; }
+// The parts of split keys: sums, then a maximum and a sum.
 int64_t workspace_bytes(const convrot_attention& a, const convrot::AttentionPlan& plan) {
-  return bits_bytes(a) + (plan.splits > 1 ? plan.splits * a.batch * a.m * a.heads * (a.d + 2) * 4 : 0);
+  return plan.splits > 1 ? plan.splits * a.batch * a.m * a.heads * (a.d + 2) * 4 : 0;
 }
 
 convrot::AttentionPlan plan_of(const convrot_attention& a) {
@@ -109,8 +108,7 @@ convrot_status convrot_attention_apply(const convrot_attention* a, void* stream)
   p.tiles = int(plan.tiles);
   p.splits = plan.splits;
   p.few = plan.few;
-  p.bits = static_cast<uint64_t*>(a->workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + bits_bytes(*a));
+  p.part = static_cast<float*>(a->workspace);
   p.stats = p.part + int64_t(plan.splits) * a->batch * a->m * a->heads * a->d;
   return from_hip(convrot::launch_attention(p, static_cast<hipStream_t>(stream)));
 }

@@ -30,9 +30,6 @@ constexpr float kMinusInf = -__builtin_inff();
 // Bytes of a key's or value's row in LDS.
 constexpr int row_pitch(int d) { return d <= 64 ? 128 : d <= 128 ? 256 : 512; }
 
-// 64-bit words of a batch entry's mask, in pairs: tiles of 128 keys read whole ones.
-CR_DEVICE int64_t bit_words(int64_t l) { return (l + 127) / 128 * 2; }
-
 // The 16-byte chunk c of row r of a tile lies at slot c ^ swizzle(r).  A
 // fragment of K is one chunk of 32 rows, read 16 lanes at a time (rows that
 // differ in their last 4 bits), one of V 4 chunks of 4 rows: both then touch
@@ -101,15 +98,10 @@ CR_DEVICE float other_half(float v) {  // lane ^ 32
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
-// Words of a batch entry's keys that take part, from its length and mask, one
-// bit for each, for the main kernel's scalar loads.
-__global__ __launch_bounds__(256) void attention_bits_kernel(const AttentionArgs p, int64_t words) {
-  const int64_t w = (p.first + blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (w >= words * p.batch) return;
-  const int64_t batch = w / words, at = (w - batch * words) * 64 + (threadIdx.x & 63);
-  const bool seen = at < p.l && p.mask[batch * p.mask_stride + at] != 0;
-  const uint64_t bits = __ballot(seen);
-  if ((threadIdx.x & 63) == 0) p.bits[w] = bits;
+// Bit i: byte i of the four is not 0.
+CR_DEVICE unsigned byte_bits(unsigned w) {
+  const unsigned t = (((w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w) >> 7 & 0x01010101u;
+  return t * 0x01020408u >> 24;
 }
 
 // Waves of a workgroup; two tiles of 32 keys for each fill LDS.
@@ -167,25 +159,58 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
   const int64_t row0 = int64_t(tile) * kRows + (FEW ? 0 : wave * 32);
   const int own = FEW ? wave * 32 : 0;  // first row of a tile that the wave reads
 
-  int64_t keys = p.l;
+  int keys = int(p.l);
   if (p.lengths) {
     const int n = p.lengths[batch];
     keys = n < 0 ? 0 : n < keys ? n : keys;
   }
-  const int64_t all = (keys + kKeys - 1) / kKeys;  // tiles of keys
+  const int64_t all = (int64_t(keys) + kKeys - 1) / kKeys;  // tiles of keys
   const int first = int(all * split / p.splits), last = int(all * (split + 1) / p.splits);
   const uint16_t* kbase = p.k + batch * p.ks[0] + head * p.ks[2];
   const uint16_t* vbase = p.v + batch * p.vs[0] + head * p.vs[2];
   const int dbytes = p.d * 2;
-  typedef const __attribute__((address_space(4))) uint32_t* const_words;
-  const const_words words = (const_words)(p.bits + batch * bit_words(p.l));
+
+  // MASK: a bit for each key of 64 blocks of 32 from block `window` on, a word in
+  // each lane; read anew where a tile's step needs words behind them.  (2 x 4096
+  // x 77, 10 heads of 64: 16.4 us with a mask, 12.6 without; 4096 x 4096, 16 of
+  // 128: 173 and 155, 181 where no two blocks hide the same keys.  As scalar
+  // loads from words that another kernel made: 18.7 and 203, and 3.8 for that.)
+  unsigned seen = 0;
+  int window = first * (kKeys / 32);
+  auto mask_words = [&](int block) __attribute__((always_inline)) {
+    const uint8_t* row = p.mask + batch * p.mask_stride;
+    const unsigned at = unsigned(block + lane) * 32;
+    unsigned bits = 0;
+    if (p.l >= 32) {  // (32 keys up to the last one and what is in front of `at` shifted out)
+      const unsigned end = unsigned(p.l) - 32, from = at < end ? at : end;
+      unsigned w[8];
+      __builtin_memcpy(w, row + from, 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bits |= byte_bits(w[i]) << (4 * i);
+      bits = at - from < 32 ? bits >> (at - from) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) bits |= row[i < p.l ? i : 0] ? 1u << i : 0u;
+    }
+    return bits;
+  };
+  auto move_window = [&](int t) __attribute__((always_inline)) {  // for tile t and those that its step loads
+    if (MASK && (t + kRing + 1) * (kKeys / 32) - window > 64) {
+      window = t * (kKeys / 32);
+      seen = mask_words(window);
+    }
+  };
+  if (MASK && first < last) seen = mask_words(window);
+  auto block_word = [&](int t, int row) __attribute__((always_inline)) {
+    return unsigned(__builtin_amdgcn_readlane(seen, t * (kKeys / 32) + row / 32 - window));
+  };
 
   // The keys of block `row` / 32 of tile t that take part, one bit for each;
   // none behind the last.
   auto block_bits = [&](int t, int row) -> unsigned {
-    const int64_t left = keys - int64_t(t) * kKeys - row;
-    unsigned bits = t >= last || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1;
-    if (MASK && bits != 0) bits &= words[(int64_t(t) * kKeys + row) / 32];
+    const int left = t >= last ? 0 : keys - t * kKeys - row;
+    unsigned bits = unsigned((uint64_t(1) << (left < 0 ? 0 : left < 32 ? left : 32)) - 1);
+    if (MASK) bits &= block_word(t, row);
     return bits;
   };
   // Rows of K (of tile t) and V (of the tile kLag before) into LDS area `to`, in
@@ -215,7 +240,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     uint64_t kseen[kKeys / 64], vseen[kKeys / 64];  // (with a mask)
   } load;
   auto bytes_of = [&](int t, int64_t stride) -> unsigned {  // of tile t's rows, up to the last key
-    const int64_t left = t < first || t >= last ? 0 : keys - int64_t(t) * kKeys;
+    const int left = t < first || t >= last ? 0 : keys - t * kKeys;
     return left <= 0 ? 0 : (left < kKeys ? unsigned(left) - 1 : kKeys - 1) * unsigned(stride) * 2 + dbytes;
   };
   auto begin_load = [&](int t, int to) __attribute__((always_inline)) {
@@ -224,12 +249,11 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     load.kbytes = bytes_of(t, p.ks[1]);
     load.vbytes = bytes_of(t - kLag, p.vs[1]);
     load.to = unsigned(reinterpret_cast<uintptr_t>((lds_byte*)smem)) + to * 2 * kTile + wave * 1024;
-    if constexpr (MASK) {
+    if constexpr (MASK) {  // (whatever it says of tiles that are not there)
 #pragma unroll
       for (int w = 0; w < kKeys / 64; ++w) {
-        load.kseen[w] = block_bits(t, 64 * w) | uint64_t(block_bits(t, 64 * w + 32)) << 32;
-        load.vseen[w] = t - kLag < first ? 0
-                                         : block_bits(t - kLag, 64 * w) | uint64_t(block_bits(t - kLag, 64 * w + 32)) << 32;
+        load.kseen[w] = block_word(t, 64 * w) | uint64_t(block_word(t, 64 * w + 32)) << 32;
+        load.vseen[w] = block_word(t - kLag, 64 * w) | uint64_t(block_word(t - kLag, 64 * w + 32)) << 32;
       }
     }
   };
@@ -238,8 +262,10 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     const int i = v ? j - kPieces : j;
     unsigned at = v ? vplace : kplace[i % kPlaces];
     if constexpr (MASK) {
-      const uint64_t seen = (v ? load.vseen : load.kseen)[i * kStep / 64];
-      at = (seen >> ((prow + i * kStep) % 64)) & 1 ? at : kOutOfRange;
+      // (the wave's rows of the piece are neighbours: its first one's bit, then the lane's)
+      const uint64_t rows = (v ? load.vseen : load.kseen)[i * kStep / 64];
+      const unsigned hidden = unsigned(~rows >> ((wave * kRowsPiece + i * kStep) % 64));
+      at |= hidden << (31 - lane / kChunks) & kOutOfRange;
     }
     load_to_lds(v ? load.v : load.k, v ? load.vbytes : load.kbytes, at, i * kStep * int(v ? p.vs[1] : p.ks[1]) * 2,
                 load.to + (v ? kTile : 0) + i * kWaves * 1024);
@@ -318,10 +344,15 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
   auto hide = [&](unsigned bits) __attribute__((always_inline)) {
     if (bits != starts) {
       starts = bits;
-      const unsigned hidden = ~bits >> (4 * fh);
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        start[e] = __uint_as_float(unsigned(__builtin_amdgcn_sbfe(int(hidden), 8 * (e / 4) + e % 4, 1)) & 0xFF800000u);
+      for (int e = 0; e < 16; ++e) {
+        const int at = 8 * (e / 4) + e % 4;  // (for either half of the wave a bit, as its lanes' select)
+        const uint64_t both = unsigned(__builtin_amdgcn_sbfe(int(bits), at, 1)) |
+                              uint64_t(unsigned(__builtin_amdgcn_sbfe(int(bits), at + 4, 1))) << 32;
+        float v;
+        asm("v_cndmask_b32_e64 %0, %1, 0, %2" : "=v"(v) : "v"(kMinusInf), "s"(both));
+        start[e] = v;
+      }
     }
   };
   // A block's maximum so far, with score e; at the end over both halves of the wave.
@@ -489,6 +520,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
       auto go = [&](auto x_t) __attribute__((always_inline)) {
         at = to;
         to = area(u + 1);
+        move_window(u);
         step(x_t, Yes{}, Yes{}, I0{}, Yes{}, at, to, block_bits(u, own),
              [&]() __attribute__((always_inline)) { begin_load(u + kRing, (u - first) % kRing); });
         ++u;
@@ -516,6 +548,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
       if (u < last) do {
         at = to;
         to = area(u + 1);
+        move_window(u);
         step(I1{}, Yes{}, Yes{}, I0{}, No{}, at, at, block_bits(u, 0), []() {});
         step(I0{}, Yes{}, Yes{}, I32{}, Yes{}, at, to, block_bits(u, 32),
              [&]() __attribute__((always_inline)) { begin_load(u + kRing, (u - first) % kRing); });
@@ -602,16 +635,19 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
   } else {
     // Whole rows out of the wave's own part of LDS (whose accesses stay in order).
     uint8_t* mine = smem + wave * 32 * kPitch;
+    int me = lane;
+    asm volatile("" : "+v"(me));  // (places are formed again: kept, they would be registers too many)
+    const int query = me & 31;
     const float g = all_sum == 0.f ? 0.f : 1.f / all_sum;
 #pragma unroll
     for (int n = 0; n < NF; ++n)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<u32x2*>(mine + fr * kPitch + (((4 * n + q) ^ key_swizzle<kPitch>(fr)) << 4) + 8 * fh) =
+        *reinterpret_cast<u32x2*>(mine + query * kPitch + (((4 * n + q) ^ key_swizzle<kPitch>(query)) << 4) + 8 * fh) =
             u32x2{bf16_pair(o[n][4 * q] * g, o[n][4 * q + 1] * g), bf16_pair(o[n][4 * q + 2] * g, o[n][4 * q + 3] * g)};
 #pragma unroll
     for (int i = 0; i < 32 / (64 / kChunks); ++i) {
-      const int row = i * (64 / kChunks) + lane / kChunks, chunk = lane % kChunks;
+      const int row = i * (64 / kChunks) + me / kChunks, chunk = me % kChunks;
       const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kPitch + ((chunk ^ key_swizzle<kPitch>(row)) << 4));
       if (row0 + row < rows && chunk * 16 < dbytes) *reinterpret_cast<u32x4*>(out_row(row0 + row) + chunk * 8) = v;
     }
@@ -647,13 +683,6 @@ template <int D, bool FEW>
 hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
   constexpr int kThreads = attention_waves(D, FEW) * 64;
   AttentionArgs p = a;
-  if (a.mask) {
-    const int64_t words = (a.l + 127) / 128 * 2;
-    in_launches((words * a.batch + 3) / 4, 256, [&](int64_t first, unsigned count) {
-      p.first = first;
-      hipLaunchKernelGGL(attention_bits_kernel, dim3(count), dim3(256), 0, stream, p, words);
-    });
-  }
   in_launches(a.batch * a.kv_heads * a.tiles * a.splits, kThreads, [&](int64_t first, unsigned count) {
     p.first = first;
     if (a.mask)

@@ -237,7 +237,6 @@ struct AttentionArgs {
   int64_t mask_stride;
   float* part;   // [splits][batch][kv_heads][m ratio][d] where the keys are split
   float* stats;  // ... and the maximum (in powers of two) and sum of each row
-  uint64_t* bits;  // [batch][2 ceil(l / 128)], with a mask: its bits
   int tiles, splits;
   bool few;
   int64_t first;  // workgroup of the launch's first one

@@ -626,7 +626,7 @@ convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* strea
  * over the keys that are seen; a query that sees none gives zeros.  Query head
  * h reads key head h / (heads / kv_heads).  Scores, maxima, sums and the
  * output's sums are float32; the weights p are rounded to bfloat16 (2^-8 of
- * each, before their sum is taken) and so is the output.
+ * each, beside their sum, which is of the unrounded ones) and so is the output.
  *
  * Tensors are bfloat16 [batch, m or l, heads, d] with any element strides of
  * the first three axes (stride 1 along d), 16-byte aligned with strides that
@@ -666,8 +666,7 @@ typedef struct convrot_attention {
 /*
  * The bytes of workspace that a call of these sizes needs on the current
  * device: few queries over many keys are worked on by several workgroups,
- * whose parts meet there, and a mask is turned into bits.  Reads batch, m, l,
- * heads, kv_heads, d and whether there is a mask.
+ * whose parts meet there.  Reads batch, m, l, heads, kv_heads and d.
  * Errors: NULL, SHAPE, UNSUPPORTED.
  */
 convrot_status convrot_attention_workspace(const convrot_attention* a, int64_t* bytes);
