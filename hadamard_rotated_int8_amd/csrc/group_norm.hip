@@ -4,10 +4,14 @@
 //
 // Bound by memory.  A group of up to 65536 values (32768 where its channels are
 // no multiple of 8) stays in one workgroup's registers between its statistics
-// and its result: one launch, x read once.
-// Larger ones take three: statistics of runs of positions, their union, and
-// the result, which goes through x from its end, where the first pass left it
-// in the last-level cache.
+// and its result: one launch, x read once.  2 x 64 positions of 1280 channels in
+// 32 groups: 4.7 us, a launch and two trips to memory.
+// Larger ones take three launches: statistics of runs of positions, their
+// union, and the result, which goes through x from its end, where the first
+// pass left it in the last-level cache.  1048576 positions of 128 channels take
+// 166 us: 61 to read them once (4.4 TB/s), 101 to read them and write y (5.3
+// TB/s), 4.7 between.  Workgroups that unite the runs for themselves in the
+// third launch spend more than the second one takes (190 us).
 //
 // Sums are float32 in a fixed order.  In the first form the variance is taken
 // of the differences from the mean, whose own mean takes off the mean's
@@ -79,6 +83,7 @@ template <bool BF16, int V>
 __global__ __launch_bounds__(1024) void group_norm_held_kernel(const GroupNormArgs a) {
   constexpr int N = held_values(V) / V;
   __shared__ float2 part[2][16];
+  extern __shared__ float affine[];  // the group's weights, its biases
   const int64_t at = a.first + blockIdx.x;
   const int64_t batch = at / a.groups;
   const int group = int(at - batch * a.groups);
@@ -88,6 +93,11 @@ __global__ __launch_bounds__(1024) void group_norm_held_kernel(const GroupNormAr
 
   float v[N][V];
   float sum = 0.f;
+  // (on its way beside x)
+  for (int c = threadIdx.x; c < each; c += blockDim.x) {
+    affine[c] = vector_value(a.weight, group * each + c, 1.f);
+    affine[each + c] = vector_value(a.bias, group * each + c, 0.f);
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int e = threadIdx.x + i * blockDim.x, row = e / columns;
@@ -134,8 +144,7 @@ __global__ __launch_bounds__(1024) void group_norm_held_kernel(const GroupNormAr
     if (e < vectors) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float w = vector_value(a.weight, group * each + c + j, 1.f), b = vector_value(a.bias, group * each + c + j, 0.f);
-        const float n = __builtin_fmaf((v[i][j] - off) * r, w, b);
+        const float n = __builtin_fmaf((v[i][j] - off) * r, affine[c + j], affine[each + c + j]);
         v[i][j] = a.silu ? silu(n) : n;
       }
       store_values<V>(v[i], a.y, a.y_bf16, ybase + row * a.ys[1] + c);
@@ -149,49 +158,94 @@ struct Place {
   int c, left, row, step;  // first channel, how many there are, first row, rows at a time
   bool in;
 };
+// Rows at a time, and those that a thread has under way: a block of kRows steps.
+constexpr int kRows = 4;
+constexpr __host__ __device__ int row_step(int c) { return kThreads / ((c + 7) / 8); }
+// Run r of an image has the blocks r, r + runs, ...: how many rows that is.
+struct RunRows {
+  int64_t block, blocks, base, extra, last, missing;
+  CR_DEVICE explicit RunRows(const GroupNormArgs& a) {
+    block = kRows * row_step(a.c);
+    blocks = (a.positions + block - 1) / block;
+    base = blocks / a.runs;
+    extra = blocks - base * a.runs;  // runs with a block more
+    last = extra > 0 ? extra - 1 : a.runs - 1;  // whose last block is the image's last one
+    missing = blocks * block - a.positions;
+  }
+  CR_DEVICE int64_t of(int64_t run) const { return (base + (run < extra)) * block - (run == last ? missing : 0); }
+};
 CR_DEVICE Place place(int c) {
-  const int columns = (c + 7) / 8, step = kThreads / columns;
+  const int columns = (c + 7) / 8, step = row_step(c);
   const int row = int(threadIdx.x) / columns, at = (int(threadIdx.x) - row * columns) * 8;
   return {at, c - at < 8 ? c - at : 8, row, step, row < step};
 }
+template <bool BF16>
+struct Raw {  // eight values as they lie in memory
+  uint32_t w[BF16 ? 4 : 8];
+};
 template <bool BF16, bool WHOLE>
-CR_DEVICE void load_row(float* v, const void* p, int64_t at, int left) {
+CR_DEVICE Raw<BF16> load_row(const void* p, int64_t at, int left) {
+  constexpr int kSize = BF16 ? 2 : 4;
+  Raw<BF16> r = {};
+  const uint8_t* from = static_cast<const uint8_t*>(p) + at * kSize;
   if (WHOLE || left == 8) {
-    load_values<BF16, 8>(v, p, at);
+    __builtin_memcpy(r.w, from, 8 * kSize);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? load_one(p, BF16, at + i) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      if (i >= left) continue;
+      if constexpr (BF16)
+        r.w[i / 2] |= unsigned(static_cast<const uint16_t*>(p)[at + i]) << (16 * (i & 1));
+      else
+        r.w[i] = static_cast<const uint32_t*>(p)[at + i];
+    }
   }
+  return r;
+}
+template <bool BF16>
+CR_DEVICE float value_of(const Raw<BF16>& r, int i) {
+  if constexpr (BF16)
+    return i & 1 ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+  else
+    return __uint_as_float(r.w[i]);
 }
 
 // Mean (relative to the group's first value) and squared differences from it
-// of each group over one run of positions.
+// of each group over one run.  (Neighbouring blocks go to different runs, and
+// all workgroups are on one stretch of x: 262144 positions of 256 channels 86
+// us, 90 with each run in one piece.)
 template <bool BF16, bool WHOLE>
-__global__ __launch_bounds__(kThreads) void group_norm_stats_kernel(const GroupNormArgs a) {
-  constexpr int U = BF16 ? 8 : 4;  // rows at once
+__global__ __launch_bounds__(kThreads, 4) void group_norm_stats_kernel(const GroupNormArgs a) {
   __shared__ float means[kThreads * 8], squares[kThreads * 8];
-  const int64_t run = a.first + blockIdx.x;
-  const int64_t batch = run / a.runs;
-  const int64_t p0 = a.positions * (run - batch * a.runs) / a.runs;
-  const int64_t p1 = a.positions * (run - batch * a.runs + 1) / a.runs;
+  const int64_t at = a.first + blockIdx.x;
+  const int64_t batch = at / a.runs, run = at - batch * a.runs;
   const int each = a.c / a.groups;
   const Place me = place(a.c);
+  const int64_t block = kRows * me.step, stride = block * a.runs;
   float mean[8] = {}, sq[8] = {};
   if (me.in) {
     const int64_t base = batch * a.xs[0];
     float pivot[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) pivot[i] = load_one(a.x, BF16, base + (me.c + (i < me.left ? i : 0)) / each * each);
-    float n = 0.f;
-    for (int64_t r = p0 + me.row; r < p1; r += U * me.step) {
-      float v[U][8];
-      int rows = 0;
+    // The next rows are on their way while these are summed.
+    Raw<BF16> held[kRows];
+    auto load = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t at = r + u * me.step;
-        if (at < p1) ++rows;
-        load_row<BF16, WHOLE>(v[u], a.x, base + (at < p1 ? at : r) * a.xs[1] + me.c, me.left);
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t row = r + u * me.step;
+        held[u] = load_row<BF16, WHOLE>(a.x, base + (row < a.positions ? row : a.positions - 1) * a.xs[1] + me.c, me.left);
       }
+    };
+    float n = 0.f;
+    auto add = [&](auto whole, int rows, int64_t next) __attribute__((always_inline)) {
+      constexpr bool kAll = decltype(whole)::value;  // (rows is kRows)
+      float v[kRows][8];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = value_of<BF16>(held[u], i);
+      load(next);
       const float nb = float(rows), inv = 1.f / nb;
       const float share = nb / (n + nb), both = n * share;
       n += nb;
@@ -199,21 +253,25 @@ __global__ __launch_bounds__(kThreads) void group_norm_stats_kernel(const GroupN
       for (int i = 0; i < 8; ++i) {
         float s = 0.f, q = 0.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < kRows; ++u) {
           v[u][i] -= pivot[i];
-          s += u < rows ? v[u][i] : 0.f;
+          s += kAll || u < rows ? v[u][i] : 0.f;
         }
         s *= inv;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float d = u < rows ? v[u][i] - s : 0.f;
+        for (int u = 0; u < kRows; ++u) {
+          const float d = kAll || u < rows ? v[u][i] - s : 0.f;
           q = __builtin_fmaf(d, d, q);
         }
         const float d = s - mean[i];
         mean[i] = __builtin_fmaf(d, share, mean[i]);
         sq[i] += __builtin_fmaf(d * d, both, q);
       }
-    }
+    };
+    int64_t r = run * block + me.row;
+    load(r);
+    for (; r + (kRows - 1) * me.step < a.positions; r += stride) add(std::true_type{}, kRows, r + stride);
+    if (r < a.positions) add(std::false_type{}, int((a.positions - r + me.step - 1) / me.step), r);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -223,58 +281,71 @@ __global__ __launch_bounds__(kThreads) void group_norm_stats_kernel(const GroupN
   __syncthreads();
   // A group's channels of all rows, a wave to a group.
   const int columns = (a.c + 7) / 8, lane = threadIdx.x & 63;
+  const int64_t rows = RunRows(a).of(run);
+  const float some = float(rows / me.step);  // ... of a step's row, and one more of the first ones
+  const int more = int(rows % me.step);
+  const float all = float(rows) * float(each);
   for (int g = threadIdx.x >> 6; g < a.groups; g += kThreads / 64) {
     const int entries = each * me.step;
     float s = 0.f;
     for (int e = lane; e < entries; e += 64) {
       const int row = e / each, c = g * each + e - row * each;
-      const int64_t rows = p1 - p0 > row ? (p1 - p0 - row + me.step - 1) / me.step : 0;
-      s += float(rows) * means[(row * columns + c / 8) * 8 + c % 8];
+      s += (row < more ? some + 1.f : some) * means[(row * columns + c / 8) * 8 + c % 8];
     }
-    const float m = wave_total(s) / (float(p1 - p0) * float(each));
+    const float m = wave_total(s) / all;
     s = 0.f;
     for (int e = lane; e < entries; e += 64) {
-      const int row = e / each, c = g * each + e - row * each, at = (row * columns + c / 8) * 8 + c % 8;
-      const int64_t rows = p1 - p0 > row ? (p1 - p0 - row + me.step - 1) / me.step : 0;
-      const float d = means[at] - m;
-      s += squares[at] + float(rows) * d * d;
+      const int row = e / each, c = g * each + e - row * each, i = (row * columns + c / 8) * 8 + c % 8;
+      const float d = means[i] - m;
+      s += squares[i] + (row < more ? some + 1.f : some) * d * d;
     }
     s = wave_total(s);
-    if (lane == 0) reinterpret_cast<float2*>(a.part)[run * a.groups + g] = make_float2(m, s);
+    if (lane == 0) {
+      reinterpret_cast<float2*>(a.part)[(batch * a.groups + g) * a.runs + run] = make_float2(m, s);
+      // (kept, since y may be x)
+      if (run == 0) a.stats[(batch * a.groups + g) * 4] = load_one(a.x, BF16, batch * a.xs[0] + g * each);
+    }
   }
 }
 
-// The runs of a group, united; a wave to a group of an image.
-template <bool BF16>
-__global__ __launch_bounds__(64) void group_norm_unite_kernel(const GroupNormArgs a) {
-  const int64_t at = a.first + blockIdx.x, batch = at / a.groups;
-  const int group = int(at - batch * a.groups), each = a.c / a.groups;
-  const float2* part = reinterpret_cast<const float2*>(a.part) + batch * a.runs * a.groups + group;
-  auto rows = [&](int64_t i) { return double(a.positions * (i + 1) / a.runs - a.positions * i / a.runs); };
+// The runs of a group, united; a workgroup to a group of an image.
+constexpr int kUniters = 256;
+__global__ __launch_bounds__(kUniters) void group_norm_unite_kernel(const GroupNormArgs a) {
+  __shared__ double sums[2][kUniters / 64];
+  const int64_t at = a.first + blockIdx.x;
+  const int each = a.c / a.groups;
+  const float2* part = reinterpret_cast<const float2*>(a.part) + at * a.runs;
+  const RunRows rows(a);
+  auto total = [&](double s, int slot) {
+    s = wave_total(s);
+    if ((threadIdx.x & 63) == 0) sums[slot][threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0;
+#pragma unroll
+    for (int w = 0; w < kUniters / 64; ++w) s += sums[slot][w];
+    return s;
+  };
   double s = 0;
-  for (int i = threadIdx.x; i < a.runs; i += 64) s += rows(i) * double(part[int64_t(i) * a.groups].x);
-  const double mean = wave_total(s) / double(a.positions);
+  for (int i = threadIdx.x; i < a.runs; i += kUniters) s += double(rows.of(i)) * double(part[i].x);
+  const double mean = total(s, 0) / double(a.positions);
   s = 0;
-  for (int i = threadIdx.x; i < a.runs; i += 64) {
-    const float2 p = part[int64_t(i) * a.groups];
+  for (int i = threadIdx.x; i < a.runs; i += kUniters) {
+    const float2 p = part[i];
     const double d = double(p.x) - mean;
-    s += double(p.y) + rows(i) * each * d * d;
+    s += double(p.y) + double(rows.of(i)) * each * d * d;
   }
-  const double var = wave_total(s) / (double(a.positions) * each);
+  const double var = total(s, 1) / (double(a.positions) * each);
   if (threadIdx.x == 0) {
-    const float r = float(1.0 / sqrt(var + double(a.eps)));
-    reinterpret_cast<f32x4*>(a.stats)[at] = f32x4{load_one(a.x, BF16, batch * a.xs[0] + group * each), float(mean), r, 0.f};
+    a.stats[4 * at + 1] = float(mean);
+    a.stats[4 * at + 2] = float(1.0 / sqrt(var + double(a.eps)));
   }
 }
 
 template <bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void group_norm_apply_kernel(const GroupNormArgs a) {
-  constexpr int U = 4;
   // (from the end of x)
-  const int64_t run = a.batch * a.runs - 1 - (a.first + blockIdx.x);
-  const int64_t batch = run / a.runs;
-  const int64_t p0 = a.positions * (run - batch * a.runs) / a.runs;
-  const int64_t p1 = a.positions * (run - batch * a.runs + 1) / a.runs;
+  const int64_t at = a.batch * a.runs - 1 - (a.first + blockIdx.x);
+  const int64_t batch = at / a.runs, run = at - batch * a.runs;
   const int each = a.c / a.groups;
   const Place me = place(a.c);
   if (!me.in) return;
@@ -288,29 +359,32 @@ __global__ __launch_bounds__(kThreads) void group_norm_apply_kernel(const GroupN
     scale[i] = s[2] * vector_value(a.weight, c, 1.f);
     bias[i] = vector_value(a.bias, c, 0.f);
   }
-  for (int64_t r = p0 + me.row; r < p1; r += U * me.step) {
-    float v[U][8];
+  const int64_t block = kRows * me.step, blocks = (a.positions + block - 1) / block;
+  for (int64_t b = run + (blocks - 1 - run) / a.runs * a.runs; b >= 0; b -= a.runs) {
+    const int64_t r = b * block + me.row;
+    Raw<BF16> x[kRows];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t at = r + u * me.step < p1 ? r + u * me.step : r;
-      load_row<BF16, WHOLE>(v[u], a.x, batch * a.xs[0] + at * a.xs[1] + me.c, me.left);
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = r + u * me.step < a.positions ? r + u * me.step : a.positions - 1;
+      x[u] = load_row<BF16, WHOLE>(a.x, batch * a.xs[0] + row * a.xs[1] + me.c, me.left);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t at = r + u * me.step;
-      if (at >= p1) break;
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = r + u * me.step;
+      if (row >= a.positions) break;
+      float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float n = __builtin_fmaf(v[u][i] - pivot[i] - mean[i], scale[i], bias[i]);
-        v[u][i] = a.silu ? silu(n) : n;
+        const float n = __builtin_fmaf(value_of<BF16>(x[u], i) - pivot[i] - mean[i], scale[i], bias[i]);
+        v[i] = a.silu ? silu(n) : n;
       }
-      const int64_t to = batch * a.ys[0] + at * a.ys[1] + me.c;
+      const int64_t to = batch * a.ys[0] + row * a.ys[1] + me.c;
       if (WHOLE || me.left == 8) {
-        store_values<8>(v[u], a.y, a.y_bf16, to);
+        store_values<8>(v, a.y, a.y_bf16, to);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < me.left) store_values<1>(v[u] + i, a.y, a.y_bf16, to + i);
+          if (i < me.left) store_values<1>(v + i, a.y, a.y_bf16, to + i);
       }
     }
   }
@@ -323,7 +397,8 @@ void launch_held(GroupNormArgs a, hipStream_t stream) {
   const int threads = 64 * int(waves < 16 ? waves : 16);
   in_launches(a.batch * a.groups, threads, [&](int64_t first, unsigned count) {
     a.first = first;
-    hipLaunchKernelGGL((group_norm_held_kernel<BF16, V>), dim3(count), dim3(threads), 0, stream, a);
+    hipLaunchKernelGGL((group_norm_held_kernel<BF16, V>), dim3(count), dim3(threads),
+                       2 * (a.c / a.groups) * sizeof(float), stream, a);
   });
 }
 
@@ -335,9 +410,9 @@ void launch_large(GroupNormArgs a, hipStream_t stream) {
       a.first = first;
       hipLaunchKernelGGL((group_norm_stats_kernel<BF16, kWhole>), dim3(count), dim3(kThreads), 0, stream, a);
     });
-    in_launches(a.batch * a.groups, 64, [&](int64_t first, unsigned count) {
+    in_launches(a.batch * a.groups, kUniters, [&](int64_t first, unsigned count) {
       a.first = first;
-      hipLaunchKernelGGL(group_norm_unite_kernel<BF16>, dim3(count), dim3(64), 0, stream, a);
+      hipLaunchKernelGGL(group_norm_unite_kernel, dim3(count), dim3(kUniters), 0, stream, a);
     });
     in_launches(a.batch * a.runs, kThreads, [&](int64_t first, unsigned count) {
       a.first = first;
@@ -355,9 +430,12 @@ void launch_large(GroupNormArgs a, hipStream_t stream) {
 int64_t plan_group_norm(int64_t batch, int64_t positions, int c, int groups) {
   const int each = c / groups;
   if (positions * each <= 1024 * held_values(each % 8 == 0 ? 8 : 1)) return 0;
-  // Two workgroups for each CU, of whole steps of 8 rows.
-  const int64_t rows = 8 * (kThreads / ((c + 7) / 8));
-  int64_t runs = (2 * int64_t(device_cu_count()) + batch - 1) / batch;
+  // A run for each CU, with a block of rows at least.  1048576 positions of 128
+  // channels, 16384 of 512, 2 x 16384 of 320: 166, 26 and 29 us; with two
+  // 169, 31 and 35; with four 172, 31 and 40.  Two blocks at least: 3 x 1927 of
+  // 336 in float32 22.5 us instead of 20.2.
+  const int64_t rows = kRows * row_step(c);
+  int64_t runs = (int64_t(device_cu_count()) + batch - 1) / batch;
   if (runs > (positions + rows - 1) / rows) runs = (positions + rows - 1) / rows;
   return runs;
 }

@@ -217,7 +217,7 @@ struct GroupNormArgs {
   bool x_bf16, y_bf16, silu;
   VectorArgs weight, bias;
   int64_t runs;  // of an image's positions, or 0: a group in one workgroup
-  float* part;   // [batch][runs][groups] mean and squared differences, with runs
+  float* part;   // [batch][groups][runs] mean and squared differences, with runs
   float* stats;  // [batch][groups] first value, mean from it, 1 / deviation, unused
   int64_t first;  // workgroup of the launch's first one
 };
