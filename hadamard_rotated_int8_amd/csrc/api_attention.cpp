@@ -31,12 +31,15 @@ convrot_status check_sizes(const convrot_attention& a) {
 }
 
 // The parts of split keys: sums, then a maximum and a sum.
+int64_t part_rows(const convrot_attention& a, const convrot::AttentionPlan& plan) {
+  return plan.splits > 1 ? plan.splits * (a.batch * a.kv_heads * plan.tiles - plan.whole) * plan.rows : 0;
+}
 int64_t workspace_bytes(const convrot_attention& a, const convrot::AttentionPlan& plan) {
-  return plan.splits > 1 ? plan.splits * a.batch * a.m * a.heads * (a.d + 2) * 4 : 0;
+  return part_rows(a, plan) * (a.d + 2) * 4;
 }
 
 convrot::AttentionPlan plan_of(const convrot_attention& a) {
-  return convrot::plan_attention(a.batch, a.kv_heads, a.m * (a.heads / a.kv_heads), a.l);
+  return convrot::plan_attention(a.batch, a.kv_heads, a.m * (a.heads / a.kv_heads), a.l, a.d);
 }
 
 // A tensor's strides and alignment; `key`: its rows are loaded by tiles.
@@ -107,9 +110,10 @@ convrot_status convrot_attention_apply(const convrot_attention* a, void* stream)
   p.mask_stride = a->mask_stride;
   p.tiles = int(plan.tiles);
   p.splits = plan.splits;
+  p.whole = plan.whole;
   p.few = plan.few;
   p.part = static_cast<float*>(a->workspace);
-  p.stats = p.part + int64_t(plan.splits) * a->batch * a->m * a->heads * a->d;
+  p.stats = p.part + part_rows(*a, plan) * a->d;
   return from_hip(convrot::launch_attention(p, static_cast<hipStream_t>(stream)));
 }
 

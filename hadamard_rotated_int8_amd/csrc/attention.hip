@@ -149,9 +149,18 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, fh = lane >> 5;
   // Neighbouring workgroups of an XCD share a head's keys.
-  int slot = int(p.first) + xcd_slot(blockIdx.x, gridDim.x);
-  const int split = slot % p.splits;
-  slot /= p.splits;
+  // The keys of tiles from p.whole on (a multiple of the XCDs) are split.
+  int slot, split = 0, splits = 1;
+  if (p.splits == 1 || int(blockIdx.x) < p.whole) {
+    slot = int(p.first) + xcd_slot(blockIdx.x, p.splits == 1 ? gridDim.x : p.whole);
+  } else {
+    splits = p.splits;
+    slot = xcd_slot(blockIdx.x - p.whole, gridDim.x - p.whole);
+    split = slot % splits;
+    slot = p.whole + slot / splits;
+  }
+  // The first of the tile's rows among the parts of its split.
+  const int64_t part0 = (int64_t(split) * (p.batch * p.kv_heads * p.tiles - p.whole) + slot - p.whole) * (FEW ? 32 : kWaves * 32);
   const int tile = slot % p.tiles;
   slot /= p.tiles;
   const int head = slot % p.kv_heads, batch = slot / p.kv_heads;
@@ -165,7 +174,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     keys = n < 0 ? 0 : n < keys ? n : keys;
   }
   const int64_t all = (int64_t(keys) + kKeys - 1) / kKeys;  // tiles of keys
-  const int first = int(all * split / p.splits), last = int(all * (split + 1) / p.splits);
+  const int first = int(all * split / splits), last = int(all * (split + 1) / splits);
   const uint16_t* kbase = p.k + batch * p.ks[0] + head * p.ks[2];
   const uint16_t* vbase = p.v + batch * p.vs[0] + head * p.vs[2];
   const int dbytes = p.d * 2;
@@ -566,7 +575,9 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     const int64_t token = p.ratio == 1 ? r : int64_t(unsigned(r) / unsigned(p.ratio));
     return p.out + batch * p.os[0] + token * p.os[1] + (head * p.ratio + r - token * p.ratio) * p.os[2];
   };
-  const int64_t part0 = ((int64_t(split) * p.batch + batch) * p.kv_heads + head) * rows;  // row of the parts
+  int me = lane;
+  asm volatile("" : "+v"(me));  // (places are formed again: kept, they would be registers too many)
+  const int query = me & 31, half = me >> 5;
   const float all_sum = total + other_half(total);
   if constexpr (FEW) {
     // The waves' sums, in their order, by all threads.
@@ -576,11 +587,11 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     for (int n = 0; n < NF; ++n)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(sums + fr * kRow + 32 * n + 8 * q + 4 * fh) =
+        *reinterpret_cast<f32x4*>(sums + query * kRow + 32 * n + 8 * q + 4 * half) =
             f32x4{o[n][4 * q], o[n][4 * q + 1], o[n][4 * q + 2], o[n][4 * q + 3]};
-    if (fh == 0) {
-      sums[fr * kRow + D] = top == kMinusInf ? kMinusInf : base;
-      sums[fr * kRow + D + 1] = all_sum;
+    if (half == 0) {
+      sums[query * kRow + D] = top == kMinusInf ? kMinusInf : base;
+      sums[query * kRow + D + 1] = all_sum;
     }
     __syncthreads();
     const int chunks = p.d / 8;
@@ -601,13 +612,13 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
         lo += weight * *reinterpret_cast<const f32x4*>(src + f);
         hi += weight * *reinterpret_cast<const f32x4*>(src + f + 4);
       }
-      if (p.splits > 1) {
-        float* dst = p.part + (part0 + row0 + row) * p.d + f;
+      if (splits > 1) {
+        float* dst = p.part + (part0 + row) * p.d + f;
         *reinterpret_cast<f32x4*>(dst) = lo;
         *reinterpret_cast<f32x4*>(dst + 4) = hi;
         if (f == 0) {
-          p.stats[2 * (part0 + row0 + row)] = most;
-          p.stats[2 * (part0 + row0 + row) + 1] = sum;
+          p.stats[2 * (part0 + row)] = most;
+          p.stats[2 * (part0 + row) + 1] = sum;
         }
       } else {
         const float g = sum == 0.f ? 0.f : 1.f / sum;
@@ -616,11 +627,11 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
                   bf16_pair(hi[2] * g, hi[3] * g)};
       }
     }
-  } else if (p.splits > 1) {
-    const int64_t r = row0 + fr;
-    if (r >= rows) return;
+  } else if (splits > 1) {
+    if (row0 + query >= rows) return;
+    const int64_t r = wave * 32 + query;
     float* dst = p.part + (part0 + r) * p.d;
-    if (fh == 0) {
+    if (half == 0) {
       p.stats[2 * (part0 + r)] = top == kMinusInf ? kMinusInf : base;
       p.stats[2 * (part0 + r) + 1] = all_sum;
     }
@@ -628,22 +639,19 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     for (int n = 0; n < NF; ++n)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int f = 32 * n + 8 * q + 4 * fh;
+        const int f = 32 * n + 8 * q + 4 * half;
         if (f < p.d)
           *reinterpret_cast<f32x4*>(dst + f) = f32x4{o[n][4 * q], o[n][4 * q + 1], o[n][4 * q + 2], o[n][4 * q + 3]};
       }
   } else {
     // Whole rows out of the wave's own part of LDS (whose accesses stay in order).
     uint8_t* mine = smem + wave * 32 * kPitch;
-    int me = lane;
-    asm volatile("" : "+v"(me));  // (places are formed again: kept, they would be registers too many)
-    const int query = me & 31;
     const float g = all_sum == 0.f ? 0.f : 1.f / all_sum;
 #pragma unroll
     for (int n = 0; n < NF; ++n)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<u32x2*>(mine + query * kPitch + (((4 * n + q) ^ key_swizzle<kPitch>(query)) << 4) + 8 * fh) =
+        *reinterpret_cast<u32x2*>(mine + query * kPitch + (((4 * n + q) ^ key_swizzle<kPitch>(query)) << 4) + 8 * half) =
             u32x2{bf16_pair(o[n][4 * q] * g, o[n][4 * q + 1] * g), bf16_pair(o[n][4 * q + 2] * g, o[n][4 * q + 3] * g)};
 #pragma unroll
     for (int i = 0; i < 32 / (64 / kChunks); ++i) {
@@ -654,14 +662,17 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
   }
 }
 
-// The parts of a split, joined: thread = 4 features of a row.
+// The parts of the tiles whose keys are split, joined: thread = 4 features of a row.
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs p, int64_t first) {
-  const int quads = p.d / 4;
-  const int64_t rows = p.m * p.ratio, count = p.batch * p.kv_heads * rows;
+  const int quads = p.d / 4, tile_rows = p.few ? 32 : 128;
+  const int64_t rows = p.m * p.ratio, count = (p.batch * p.kv_heads * p.tiles - p.whole) * tile_rows;
   const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;
   const int64_t r = i / quads;
   const int f = int(i - r * quads) * 4;
   if (r >= count) return;
+  const int64_t slot = p.whole + r / tile_rows, pair = slot / p.tiles;
+  const int64_t in = (slot - pair * p.tiles) * tile_rows + r % tile_rows;  // row of the key head
+  if (in >= rows) return;
   float top = kMinusInf;
   for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.stats[2 * (s * count + r)]);
   const float base = top == kMinusInf ? 0.f : top;
@@ -673,7 +684,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
     v += w * *reinterpret_cast<const f32x4*>(p.part + (s * count + r) * p.d + f);
   }
   v *= sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t pair = r / rows, in = r - pair * rows, token = in / p.ratio;
+  const int64_t token = in / p.ratio;
   const int64_t batch = pair / p.kv_heads, head = (pair - batch * p.kv_heads) * p.ratio + in - token * p.ratio;
   *reinterpret_cast<u32x2*>(p.out + batch * p.os[0] + token * p.os[1] + head * p.os[2] + f) =
       u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
@@ -683,7 +694,8 @@ template <int D, bool FEW>
 hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
   constexpr int kThreads = attention_waves(D, FEW) * 64;
   AttentionArgs p = a;
-  in_launches(a.batch * a.kv_heads * a.tiles * a.splits, kThreads, [&](int64_t first, unsigned count) {
+  const int64_t tiles = a.batch * a.kv_heads * a.tiles;  // (with splits few enough for one launch)
+  in_launches(a.splits > 1 ? a.whole + (tiles - a.whole) * a.splits : tiles, kThreads, [&](int64_t first, unsigned count) {
     p.first = first;
     if (a.mask)
       hipLaunchKernelGGL((attention_kernel<D, FEW, true>), dim3(count), dim3(kThreads), 0, stream, p);
@@ -691,7 +703,7 @@ hipError_t launch_t(const AttentionArgs& a, hipStream_t stream) {
       hipLaunchKernelGGL((attention_kernel<D, FEW, false>), dim3(count), dim3(kThreads), 0, stream, p);
   });
   if (a.splits > 1) {
-    const int64_t values = a.batch * a.kv_heads * a.m * a.ratio * (a.d / 4);
+    const int64_t values = (tiles - a.whole) * (a.few ? 32 : 128) * (a.d / 4);
     in_launches((values + 255) / 256, 256, [&](int64_t first, unsigned count) {
       hipLaunchKernelGGL(attention_join_kernel, dim3(count), dim3(256), 0, stream, p, first);
     });
@@ -706,7 +718,7 @@ hipError_t launch_d(const AttentionArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l) {
+AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d) {
   AttentionPlan plan{};
   const int64_t cus = device_cu_count(), heads = batch * kv_heads;
   auto blocks = [&](int64_t n) { return heads * ((rows + n - 1) / n); };
@@ -715,14 +727,30 @@ AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int6
   // 44.5; 64 x 32760, 8 heads, 41.4 against 46.3; 300 x 2000, 8 heads, 19.1
   // against 22.4.  With up to twice as many, 2000 x 333, 8 heads: 19.9 against 13.8.
   plan.few = blocks(32) <= cus;
-  const int64_t tile_rows = plan.few ? 32 : 128;
-  plan.tiles = (rows + tile_rows - 1) / tile_rows;
+  plan.rows = plan.few ? 32 : 128;
+  plan.tiles = (rows + plan.rows - 1) / plan.rows;
   plan.splits = 1;
-  const int64_t key_tiles = (l + 127) / 128;
-  if (heads * plan.tiles > 0 && heads * plan.tiles < cus) {
-    int64_t want = cus / (heads * plan.tiles);
-    if (want > key_tiles / 4) want = key_tiles / 4;
-    if (want > 1) plan.splits = int(want);
+  const int64_t total = heads * plan.tiles, most = (l + 127) / 128 / 4;  // (512 keys to a part at least)
+  auto split = [&](int64_t whole, int64_t want) {
+    want = want < most ? want : most;
+    if (want > 1) {
+      plan.splits = int(want);
+      plan.whole = int(whole);
+    }
+  };
+  // Fewer tiles than CUs are split so that each CU has work.  Of more, those of
+  // a last round that would leave places free (a CU has two workgroups, one
+  // beyond 128 features) are split to fill them.  Up to a quarter of the places:
+  // 4608 x 4608, 30 heads of 64, 223 -> 208 us, 2176 x 1024, 31 of 128, 59 -> 54.
+  // Up to a half, where what is saved outweighs the parts' way through memory:
+  // 4095 x 32760, 40 of 128, 2630 -> 2540, 4096 x 4096, 20 of 160, 297 -> 271; but
+  // 4096 x 4096, 40 of 128, 337 -> 344, 2304 x 4096, 40 of 64, 127 -> 134.
+  const int64_t places = (plan.few || d > 128 ? 1 : 2) * cus;
+  if (total > 0 && total < cus) {
+    split(0, cus / total);
+  } else if (total > places && total <= (1 << 20)) {
+    const int64_t last = total % places;
+    if (last > 0 && last <= (d > 128 || l >= 16384 ? places / 2 : places / 4)) split(total - last, places / last);
   }
   return plan;
 }

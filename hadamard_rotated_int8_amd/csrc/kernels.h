@@ -235,18 +235,20 @@ struct AttentionArgs {
   const int32_t* lengths;  // [batch] or nullptr
   const uint8_t* mask;     // [batch] rows of l bytes, or nullptr
   int64_t mask_stride;
-  float* part;   // [splits][batch][kv_heads][m ratio][d] where the keys are split
+  float* part;   // [splits][rows of the tiles whose keys are split][d]
   float* stats;  // ... and the maximum (in powers of two) and sum of each row
-  int tiles, splits;
+  int tiles, splits, whole;
   bool few;
   int64_t first;  // workgroup of the launch's first one
 };
 struct AttentionPlan {
-  int64_t tiles;  // of a key head's queries
-  int splits;     // of the keys
+  int64_t tiles;  // of a key head's queries, each of ...
+  int rows;
+  int splits;     // of the keys ...
+  int whole;      // ... of all heads' tiles behind so many
   bool few;       // the waves of a workgroup share 32 queries (else each has 32)
 };
-AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l);
+AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t l, int d);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
 
 }  // namespace convrot

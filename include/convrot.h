@@ -665,8 +665,8 @@ typedef struct convrot_attention {
 
 /*
  * The bytes of workspace that a call of these sizes needs on the current
- * device: few queries over many keys are worked on by several workgroups,
- * whose parts meet there.  Reads batch, m, l, heads, kv_heads and d.
+ * device: where few tiles of queries are left for the chip, their keys are
+ * shared by several workgroups, whose parts meet there.  Reads batch, m, l, heads, kv_heads and d.
  * Errors: NULL, SHAPE, UNSUPPORTED.
  */
 convrot_status convrot_attention_workspace(const convrot_attention* a, int64_t* bytes);

@@ -56,6 +56,21 @@ def test_few_queries_over_many_keys(m, l, d):
     _check(q, k, v, cr.attention(q, k, v))
 
 
+@pytest.mark.parametrize("d, heads, kv, m", [(64, 26, 13, 2555), (128, 24, 24, 2700), (160, 13, 13, 2555)])
+def test_a_last_round_of_few_tiles(d, heads, kv, m):
+    # (520, 528 or 260 tiles, on 512 places or 256: the keys of the last ones are split)
+    l = 1100
+    q, k, v = _inputs(1, m, l, heads, kv, d, seed=d)
+    mask = torch.rand(1, l, device=DEV, generator=torch.Generator(device=DEV).manual_seed(d)) < 0.5
+    mask[0, 500:800] = False
+    at = [0, heads // 2, heads - 1]
+    for kw in ({}, {"lengths": torch.tensor([1027], dtype=torch.int32, device=DEV)}, {"mask": mask},
+               {"lengths": torch.tensor([0], dtype=torch.int32, device=DEV)}):
+        out = cr.attention(q, k, v, **kw)
+        key = [h // (heads // kv) for h in at]
+        _check(q[:, :, at], k[:, :, key], v[:, :, key], out[:, :, at], **kw)
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 @pytest.mark.parametrize("l", [77, 300, 5000])
 def test_lengths_of_a_batch(m, l):
