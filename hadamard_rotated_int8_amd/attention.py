@@ -70,12 +70,14 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | 
         if not _no_overlap(out):
             raise ValueError("out's elements must not overlap")
         lo, hi = _span(out)
-        if any(a < hi and lo < b for a, b in map(_span, (q, k, v))):
-            raise ValueError("out must not lie over q, k or v")
+        if any(a < hi and lo < b for a, b in map(_span, [t for t in (q, k, v, lengths, mask) if t is not None])):
+            raise ValueError("out must not lie over an input")
 
     def strides(t):
-        st = t.stride()
-        return st[:3] if dim == 4 else (0, *st[:2])
+        st = t.stride()[:3] if dim == 4 else (0, *t.stride()[:2])
+        if (st[0] | st[1] | st[2]) & 7:  # (an axis of one may state any distance)
+            st = tuple(0 if n == 1 else s for s, n in zip(st, t.shape[:3] if dim == 4 else (1, *t.shape[:2])))
+        return st
 
     if scale is None:
         scale = d ** -0.5 if d else 1.0

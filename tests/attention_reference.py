@@ -16,8 +16,8 @@ def seen_keys(batch, l, lengths=None, mask=None):
 def attention_ref(q, k, v, scale=None, lengths=None, mask=None):
     """(out, tol) in float64 on the CPU for 4-dimensional bfloat16 inputs.
 
-    With weights p_j (1 + a) rounded to bfloat16, |a| <= 2^-8, in the sum and in its divisor, and
-    A = sum p |v| / sum p, the quotient is off by (2^-8 (A + |out|)) / (1 - 2^-8), and the output's own
+    With weights p_j (1 + a) rounded to bfloat16, |a| <= 2^-8, in the sum and at most in its divisor,
+    and A = sum p |v| / sum p, the quotient is off by (2^-8 (A + |out|)) / (1 - 2^-8), and the output's own
     rounding by 2^-8 |out|.  A score's float32 sum of d products is off by (d + 1) 2^-24 sum |q k|,
     which the exponent carries, times scale, into a relative error of p; forming the exponent adds
     2^-22 of its size and the exponential 2^-22; the sums over l keys (l + 4) 2^-23 of A, twice (the

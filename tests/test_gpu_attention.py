@@ -170,6 +170,44 @@ def test_strides_and_outputs():
     assert torch.equal(shared[0], ref[0])
 
 
+def test_axes_of_one_may_state_any_stride():
+    g = torch.Generator(device=DEV).manual_seed(3)
+    flat = torch.randn(3, 4097, generator=g, device=DEV).to(torch.bfloat16)
+    q = flat[:1, :64].as_strided((1, 1, 1, 64), (4097, 5, 3, 1))
+    k = flat[1].as_strided((1, 32, 1, 64), (9, 128, 1, 1), 4104)
+    v = flat[1].as_strided((1, 32, 1, 64), (9, 128, 1, 1), 4104 + 64)
+    out = torch.empty(100, dtype=torch.bfloat16, device=DEV).as_strided((1, 1, 1, 64), (3, 1, 7, 1))
+    ref = cr.attention(q.contiguous(), k.contiguous(), v.contiguous())
+    assert torch.equal(cr.attention(q, k, v), ref)
+    assert torch.equal(cr.attention(q, k, v, out=out), ref)
+
+
+def test_outputs_over_inputs_are_refused():
+    q, k, v = _inputs(2, 8, 40, 2, 2, 64)
+    space = torch.empty(q.numel() * 2 + 80, dtype=torch.uint8, device=DEV)
+    out = space[:q.numel() * 2].view(torch.bfloat16).view(q.shape)
+    mask = space[q.numel() * 2 - 16:q.numel() * 2 + 64].view(torch.bool).view(2, 40)
+    lengths = space[:8].view(torch.int32)
+    for args, kw in (((q, k, v), {"out": q}), ((q, k, v), {"out": out, "mask": mask}),
+                     ((q, k, v), {"out": out, "lengths": lengths}), ((out, k, v), {"out": out})):
+        with pytest.raises(ValueError, match="over an input"):
+            cr.attention(*args, **kw)
+    with pytest.raises(ValueError, match="overlap"):
+        cr.attention(q, k, v, out=q.new_empty(1, 8, 2, 64).expand(2, 8, 2, 64))
+
+
+@pytest.mark.parametrize("l", [3, 31, 32, 33, 2049, 4500])
+def test_a_mask_at_any_address(l):
+    q, k, v = _inputs(2, 130, l, 2, 1, 64, seed=l)
+    g = torch.Generator(device=DEV).manual_seed(l)
+    wide = torch.rand(2, l + 9, generator=g, device=DEV) < 0.5
+    for at in (1, 2, 7):
+        _check(q, k, v, cr.attention(q, k, v, mask=wide[:, at:at + l]), mask=wide[:, at:at + l])
+    # a byte that is neither 0 nor 1 shows its key too
+    odd = (torch.randint(0, 3, (2, l), generator=g, device=DEV, dtype=torch.uint8) * 127)
+    _check(q, k, v, cr.attention(q, k, v, mask=odd.view(torch.bool)), mask=odd != 0)
+
+
 def test_empty_sizes():
     q, k, v = _inputs(2, 5, 7, 2, 2, 64)
     assert (cr.attention(q, k[:, :0], v[:, :0]) == 0).all()
