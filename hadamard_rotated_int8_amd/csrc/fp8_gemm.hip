@@ -325,16 +325,23 @@ hipError_t launch_g(const Fp8GemmArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT>
+enum { kLinears = 1, kPairs = 2 };  // what a shape is for
+
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool F32SCALE, bool EXACT, int FOR>
 hipError_t launch_t(const Fp8GemmArgs& a, hipStream_t stream) {
-  return a.gated ? launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, true>(a, stream)
-                 : launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, false>(a, stream);
+  if constexpr (FOR == kLinears)
+    return launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, false>(a, stream);
+  else if constexpr (FOR == kPairs)
+    return launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, true>(a, stream);
+  else
+    return a.gated ? launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, true>(a, stream)
+                   : launch_g<FM, FN, WM, WN, KG, STAGES, F32SCALE, EXACT, false>(a, stream);
 }
 
-template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool EXACT>
+template <int FM, int FN, int WM, int WN, int KG, int STAGES, bool EXACT, int FOR = kLinears | kPairs>
 hipError_t launch_type(const Fp8GemmArgs& a, hipStream_t stream) {
-  return a.f32_scale ? launch_t<FM, FN, WM, WN, KG, STAGES, true, EXACT>(a, stream)
-                     : launch_t<FM, FN, WM, WN, KG, STAGES, false, EXACT>(a, stream);
+  return a.f32_scale ? launch_t<FM, FN, WM, WN, KG, STAGES, true, EXACT, FOR>(a, stream)
+                     : launch_t<FM, FN, WM, WN, KG, STAGES, false, EXACT, FOR>(a, stream);
 }
 
 template <int FM, int FN, int WM, int WN, int KG, int STAGES>
@@ -388,7 +395,16 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   if (tiles(64, 64) <= cus) return launch_modes<1, 1, 2, 2, 2, 3>(a, stream);
   if (a.m <= 64) return launch_modes<1, 1, 2, 2, 1, 3>(a, stream);
   if (tiles(128, 64) <= cus) return launch_modes<2, 1, 2, 2, 2, 3>(a, stream);
-  if (tiles(128, 128) <= cus) return launch_modes<1, 2, 4, 2, 2, 2>(a, stream);
+  if (tiles(128, 128) <= cus) {
+    if (!a.y_bf16) return launch_type<1, 2, 4, 2, 2, 2, true>(a, stream);
+    // A pair with bfloat16 outputs has one group of waves and four stages,
+    // whose loads are longer under way: weights from memory, 128 x 5120 ->
+    // 13824, 256 x 5120 -> 8192, 333 x 4112 -> 4104: 43, 39 and 35 us, in two
+    // groups 47, 44 and 38.  (float32 outputs wait for the matrix cores: 512 x
+    // 5120 -> 4096 54 and 51.)
+    if (a.gated) return launch_type<2, 1, 2, 4, 1, 4, false, kPairs>(a, stream);
+    return launch_type<1, 2, 4, 2, 2, 2, false, kLinears>(a, stream);
+  }
   return launch_modes<2, 2, 2, 2, 1, 2>(a, stream);
 }
 
