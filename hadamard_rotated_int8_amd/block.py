@@ -1,6 +1,7 @@
 """The operators around a transformer block's linears: FP8 linears with a scale
-for each block of 128 features, the norms before and after a block with its
-gate and residual, and rotary positions.
+for each block of 128 features, alone or as the gated pair of a feed-forward
+with its way back, the norms before and after a block with its gate and
+residual, group norm, and rotary positions.
 
 Argument checks and marshalling only, like the package's other helpers: every
 step of the computation runs in the HIP kernels of libconvrot.so.  The call
@@ -8,9 +9,9 @@ path is kept short (arguments are packed straight into the C structs of
 include/convrot.h), since a single token's operators cost a few microseconds
 on the GPU.
 
-``block_norm`` -> ``fp8_linear_grouped`` (Q, K, V) -> ``rope`` -> attention ->
-``fp8_linear`` -> ``block_update`` -> ``fp8_linear`` (GELU) -> ``fp8_linear`` ->
-``block_update`` is one block of a diffusion transformer; ``block_norm`` and
+``block_norm`` -> ``fp8_linear_grouped`` (Q, K, V) -> ``rope`` -> ``attention`` ->
+``fp8_linear`` -> ``block_update`` -> ``fp8_linear`` (GELU) or ``fp8_gated`` ->
+``fp8_linear`` -> ``block_update`` is one block of a diffusion transformer; ``block_norm`` and
 ``block_update`` can hand the next linear its FP8 activation directly.
 """
 
