@@ -63,7 +63,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | 
             raise ValueError("all tensors of one call must be on the same device")
         mask_stride = mask.stride(0) if mask.dim() == 2 else 0
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         if out.dtype != torch.bfloat16 or out.shape != q.shape or out.stride(-1) != 1 or out.device != dev:
             raise ValueError("out must be bfloat16 of q's shape and device with unit stride along d")

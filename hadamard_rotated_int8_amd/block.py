@@ -679,7 +679,7 @@ def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
     if 0 in x.shape:
         positions = 0
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
         ys = c
     else:
         if out.dtype not in _DTYPE or (out_dtype is not None and out.dtype != out_dtype):

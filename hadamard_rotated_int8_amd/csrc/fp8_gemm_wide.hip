@@ -35,7 +35,7 @@ bool fp8_wide_wanted(const Fp8GemmArgs& a) {
   const int bn = a.f32_scale ? WideCfg<true>::BN : WideCfg<false>::BN;
   int64_t tiles = 0, small = 0;
   if (a.gated) {  // (as many rows of W to a tile, half as many columns of Y)
-    if (a.w[0].ldy >= kMaxLdy || a.ldk >= kMaxLdy) return false;
+    if (a.w[0].ldy >= kMaxLdy || (a.kept[0] && a.ldk >= kMaxLdy)) return false;
     tiles = ((a.m + kBM - 1) / kBM) * ((a.w[0].n + bn / 2 - 1) / (bn / 2));
     small = ((a.m + 127) / 128) * ((a.w[0].n + 63) / 64);
   }
