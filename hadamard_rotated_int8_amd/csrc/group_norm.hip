@@ -349,6 +349,19 @@ __global__ __launch_bounds__(kThreads) void group_norm_apply_kernel(const GroupN
   const int each = a.c / a.groups;
   const Place me = place(a.c);
   if (!me.in) return;
+  const int64_t block = kRows * me.step, blocks = (a.positions + block - 1) / block;
+  int64_t b = run + (blocks - 1 - run) / a.runs * a.runs;
+  // (the first rows before the statistics, the next ones before these are done)
+  Raw<BF16> held[kRows];
+  auto load = [&](int64_t b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = b * block + me.row + u * me.step;
+      held[u] = load_row<BF16, WHOLE>(a.x, batch * a.xs[0] + (row < a.positions ? row : a.positions - 1) * a.xs[1] + me.c,
+                                      me.left);
+    }
+  };
+  load(b);
   float pivot[8], mean[8], scale[8], bias[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -359,15 +372,12 @@ __global__ __launch_bounds__(kThreads) void group_norm_apply_kernel(const GroupN
     scale[i] = s[2] * vector_value(a.weight, c, 1.f);
     bias[i] = vector_value(a.bias, c, 0.f);
   }
-  const int64_t block = kRows * me.step, blocks = (a.positions + block - 1) / block;
-  for (int64_t b = run + (blocks - 1 - run) / a.runs * a.runs; b >= 0; b -= a.runs) {
+  for (; b >= 0; b -= a.runs) {
     const int64_t r = b * block + me.row;
     Raw<BF16> x[kRows];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t row = r + u * me.step < a.positions ? r + u * me.step : a.positions - 1;
-      x[u] = load_row<BF16, WHOLE>(a.x, batch * a.xs[0] + row * a.xs[1] + me.c, me.left);
-    }
+    for (int u = 0; u < kRows; ++u) x[u] = held[u];
+    if (b >= a.runs) load(b - a.runs);
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int64_t row = r + u * me.step;
