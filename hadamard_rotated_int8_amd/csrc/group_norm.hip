@@ -9,9 +9,10 @@
 // Larger ones take three launches: statistics of runs of positions, their
 // union, and the result, which goes through x from its end, where the first
 // pass left it in the last-level cache.  1048576 positions of 128 channels take
-// 166 us: 61 to read them once (4.4 TB/s), 101 to read them and write y (5.3
-// TB/s), 4.7 between.  Workgroups that unite the runs for themselves in the
-// third launch spend more than the second one takes (190 us).
+// 158 us: 65 to read them once (4.1 TB/s; a library's reductions read at 3.5 to
+// 4.0), 87 to read them and write y (6.2 TB/s, some of it from the last-level
+// cache), 4.6 between.  Workgroups that unite the runs for themselves in the
+// third launch spend more than the second one takes (190 us in all, 175 then).
 //
 // Sums are float32 in a fixed order.  In the first form the variance is taken
 // of the differences from the mean, whose own mean takes off the mean's
@@ -441,8 +442,8 @@ int64_t plan_group_norm(int64_t batch, int64_t positions, int c, int groups) {
   const int each = c / groups;
   if (positions * each <= 1024 * held_values(each % 8 == 0 ? 8 : 1)) return 0;
   // A run for each CU, with a block of rows at least.  1048576 positions of 128
-  // channels, 16384 of 512, 2 x 16384 of 320: 166, 26 and 29 us; with two
-  // 169, 31 and 35; with four 172, 31 and 40.  Two blocks at least: 3 x 1927 of
+  // channels, 16384 of 512, 2 x 16384 of 320: 166, 26 and 29 us (158 since the
+  // result's rows come ahead); with two 169, 31 and 35; with four 172, 31 and 40.  Two blocks at least: 3 x 1927 of
   // 336 in float32 22.5 us instead of 20.2.
   const int64_t rows = kRows * row_step(c);
   int64_t runs = (int64_t(device_cu_count()) + batch - 1) / batch;
