@@ -374,7 +374,8 @@ def fp8_gated(x: torch.Tensor | Fp8Activation, gate: Fp8Weights, up: Fp8Weights,
                 x, rows = fp8_pack_activations(x), None
     kept = None
     if keep:
-        kept = tuple(torch.empty((m, n), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        kept = (torch.empty((m, n), dtype=torch.bfloat16, device=dev),)
+        kept += (torch.empty_like(kept[0]),)
     args = weights + _GATED_TAIL.pack(out.data_ptr(), _row_stride(out), dt, code,
                                       kept[0].data_ptr() if keep else 0, kept[1].data_ptr() if keep else 0, n)
     if rows is None:
@@ -455,7 +456,8 @@ def fp8_gated_backward(dy: torch.Tensor, kept, back: Fp8Weights, act: str = "sil
     if n < 1 or back.q.shape[1] != 2 * np:
         raise ValueError("back must be fp8_transpose_weights([gate, up])")
     packed = _new_activation(m, 2 * np, dev)
-    dgate, dup = (torch.empty((m, n), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    dgate = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+    dup = torch.empty_like(dgate)
     pk = _writable(_pack_args(packed))
     _launch(lib().convrot_fp8_gated_backward, "convrot_fp8_gated_backward", dev,
             _GATED_BACKWARD.pack(dy.data_ptr(), kept[0].data_ptr(), kept[1].data_ptr(), dgate.data_ptr(),

@@ -217,7 +217,7 @@ CR_DEVICE float value_of(const Raw<BF16>& r, int i) {
 // us, 90 with each run in one piece.)
 template <bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads, 4) void group_norm_stats_kernel(const GroupNormArgs a) {
-  __shared__ float means[kThreads * 8], squares[kThreads * 8];
+  __shared__ float means[kThreads * 8], squares[kThreads * 8], met[2][kThreads / 64];
   const int64_t at = a.first + blockIdx.x;
   const int64_t batch = at / a.runs, run = at - batch * a.runs;
   const int each = a.c / a.groups;
@@ -280,33 +280,54 @@ __global__ __launch_bounds__(kThreads, 4) void group_norm_stats_kernel(const Gro
     squares[threadIdx.x * 8 + i] = sq[i];
   }
   __syncthreads();
-  // A group's channels of all rows, a wave to a group.
-  const int columns = (a.c + 7) / 8, lane = threadIdx.x & 63;
+  // A group's channels of all rows: a wave to a group, or with fewer groups than
+  // waves as many as there are for each (486708 positions of 24 channels in one
+  // group, float32: 33 us; with one wave 41).
+  constexpr int kWaves = kThreads / 64;
+  const int columns = (a.c + 7) / 8, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t rows = RunRows(a).of(run);
   const float some = float(rows / me.step);  // ... of a step's row, and one more of the first ones
   const int more = int(rows % me.step);
   const float all = float(rows) * float(each);
-  for (int g = threadIdx.x >> 6; g < a.groups; g += kThreads / 64) {
-    const int entries = each * me.step;
-    float s = 0.f;
-    for (int e = lane; e < entries; e += 64) {
-      const int row = e / each, c = g * each + e - row * each;
-      s += (row < more ? some + 1.f : some) * means[(row * columns + c / 8) * 8 + c % 8];
+  auto reduce = [&](auto one) __attribute__((always_inline)) {
+    constexpr bool kOne = decltype(one)::value;
+    const int team = kOne ? 1 : kWaves / a.groups, teams = kWaves / team;  // waves of a group, groups at once
+    for (int g0 = 0; g0 < a.groups; g0 += teams) {  // (once, where a team has more than one wave)
+      const int g = g0 + wave / team, member = wave % team;
+      const int entries = wave / team < teams && g < a.groups ? each * me.step : 0;
+      auto total = [&](float s, int slot) __attribute__((always_inline)) {
+        s = wave_total(s);
+        if constexpr (kOne) return s;
+        if (lane == 0) met[slot][wave] = s;
+        __syncthreads();
+        s = 0.f;
+        for (int w = wave - member; w < wave - member + team && w < kWaves; ++w) s += met[slot][w];
+        return s;
+      };
+      float s = 0.f;
+      for (int e = lane + 64 * member; e < entries; e += 64 * team) {
+        const int row = e / each, c = g * each + e - row * each;
+        s += (row < more ? some + 1.f : some) * means[(row * columns + c / 8) * 8 + c % 8];
+      }
+      const float m = total(s, 0) / all;
+      s = 0.f;
+      for (int e = lane + 64 * member; e < entries; e += 64 * team) {
+        const int row = e / each, c = g * each + e - row * each, i = (row * columns + c / 8) * 8 + c % 8;
+        const float d = means[i] - m;
+        s += squares[i] + (row < more ? some + 1.f : some) * d * d;
+      }
+      s = total(s, 1);
+      if (lane == 0 && member == 0 && entries > 0) {
+        reinterpret_cast<float2*>(a.part)[(batch * a.groups + g) * a.runs + run] = make_float2(m, s);
+        // (kept, since y may be x)
+        if (run == 0) a.stats[(batch * a.groups + g) * 4] = load_one(a.x, BF16, batch * a.xs[0] + g * each);
+      }
     }
-    const float m = wave_total(s) / all;
-    s = 0.f;
-    for (int e = lane; e < entries; e += 64) {
-      const int row = e / each, c = g * each + e - row * each, i = (row * columns + c / 8) * 8 + c % 8;
-      const float d = means[i] - m;
-      s += squares[i] + (row < more ? some + 1.f : some) * d * d;
-    }
-    s = wave_total(s);
-    if (lane == 0) {
-      reinterpret_cast<float2*>(a.part)[(batch * a.groups + g) * a.runs + run] = make_float2(m, s);
-      // (kept, since y may be x)
-      if (run == 0) a.stats[(batch * a.groups + g) * 4] = load_one(a.x, BF16, batch * a.xs[0] + g * each);
-    }
-  }
+  };
+  if (a.groups > kWaves / 2)
+    reduce(std::true_type{});
+  else
+    reduce(std::false_type{});
 }
 
 // The runs of a group, united; a workgroup to a group of an image.

@@ -70,7 +70,7 @@ def _affine(c, dtype, seed=1):
     (1, 16384, 2, 1), (1, 16385, 2, 1), (1, 32768, 3, 3), (1, 32769, 3, 3), (1, 1561, 63, 3), (1, 1562, 63, 3),
     # many positions, channels that fill no thread, more than one step of rows
     (1, 70001, 24, 4), (2, 40000, 129, 3), (1, 5000, 1027, 13), (1, 3000, 4096, 32), (3, 9001, 320, 10),
-    (1, 300, 4095, 1), (5, 33333, 10, 5)])
+    (1, 300, 4095, 1), (5, 33333, 10, 5), (1, 50001, 24, 1), (2, 50000, 14, 2)])
 def test_sizes(batch, positions, c, groups, silu, dtype):
     x = _x(batch, positions, c, dtype=dtype, seed=positions + c)
     weight, bias = _affine(c, dtype)
