@@ -146,7 +146,7 @@ int64_t group_norm_runs(const convrot_group_norm& g) {
 }
 // A mean and a sum of squares for each run, and what becomes of them.
 int64_t group_norm_bytes(const convrot_group_norm& g, int64_t runs) {
-  return runs > 0 ? g.batch * g.groups * (8 * runs + 16) : 0;
+  return runs > 0 ? g.batch * g.groups * (16 * runs + 16) : 0;
 }
 
 }  // namespace
@@ -470,7 +470,7 @@ convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* strea
   a.y_bf16 = g->y_dtype == CONVROT_BF16;
   a.silu = g->silu != 0;
   a.stats = static_cast<float*>(g->workspace);
-  a.part = a.stats + 4 * g->batch * g->groups;
+  a.part = reinterpret_cast<double*>(a.stats + 4 * g->batch * g->groups);
   return from_hip(convrot::launch_group_norm(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -16,10 +16,13 @@
 //
 // Sums are float32 in a fixed order.  In the first form the variance is taken
 // of the differences from the mean, whose own mean takes off the mean's
-// rounding; in the second all values are taken relative to the group's first
-// one, sums of 4 or 8 rows at a time are turned into a mean and squared
-// differences from it and those united pairwise, in 64 bits among workgroups.
-// Either way a large common part of a group costs no digits.
+// rounding.  In the second a thread takes each channel's values relative to the
+// first one that it reads, turns 4 rows at a time into a mean and squared
+// differences from it and unites those pairwise; threads and workgroups are
+// united in 64 bits, and the result takes the mean off in two parts of 32.
+// Either way neither a large common part of a group nor single values far from
+// the others cost digits (a value relative to one that is far away is rounded
+// to that one's spacing; only the thread that read it first is).
 #include <type_traits>
 
 #include "common.h"
@@ -211,24 +214,21 @@ CR_DEVICE float value_of(const Raw<BF16>& r, int i) {
     return __uint_as_float(r.w[i]);
 }
 
-// Mean (relative to the group's first value) and squared differences from it
-// of each group over one run.  (Neighbouring blocks go to different runs, and
+// Mean and squared differences from it of each group over one run.  (Neighbouring blocks go to different runs, and
 // all workgroups are on one stretch of x: 262144 positions of 256 channels 86
 // us, 90 with each run in one piece.)
 template <bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads, 4) void group_norm_stats_kernel(const GroupNormArgs a) {
-  __shared__ float means[kThreads * 8], squares[kThreads * 8], met[2][kThreads / 64];
+  __shared__ double means[kThreads * 8], met[2][kThreads / 64];
+  __shared__ float squares[kThreads * 8];
   const int64_t at = a.first + blockIdx.x;
   const int64_t batch = at / a.runs, run = at - batch * a.runs;
   const int each = a.c / a.groups;
   const Place me = place(a.c);
   const int64_t block = kRows * me.step, stride = block * a.runs;
-  float mean[8] = {}, sq[8] = {};
+  float pivot[8] = {}, mean[8] = {}, sq[8] = {};
   if (me.in) {
     const int64_t base = batch * a.xs[0];
-    float pivot[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) pivot[i] = load_one(a.x, BF16, base + (me.c + (i < me.left ? i : 0)) / each * each);
     // The next rows are on their way while these are summed.
     Raw<BF16> held[kRows];
     auto load = [&](int64_t r) __attribute__((always_inline)) {
@@ -271,12 +271,14 @@ __global__ __launch_bounds__(kThreads, 4) void group_norm_stats_kernel(const Gro
     };
     int64_t r = run * block + me.row;
     load(r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pivot[i] = value_of<BF16>(held[0], i);
     for (; r + (kRows - 1) * me.step < a.positions; r += stride) add(std::true_type{}, kRows, r + stride);
     if (r < a.positions) add(std::false_type{}, int((a.positions - r + me.step - 1) / me.step), r);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    means[threadIdx.x * 8 + i] = mean[i];
+    means[threadIdx.x * 8 + i] = double(pivot[i]) + double(mean[i]);
     squares[threadIdx.x * 8 + i] = sq[i];
   }
   __syncthreads();
@@ -286,42 +288,39 @@ __global__ __launch_bounds__(kThreads, 4) void group_norm_stats_kernel(const Gro
   constexpr int kWaves = kThreads / 64;
   const int columns = (a.c + 7) / 8, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t rows = RunRows(a).of(run);
-  const float some = float(rows / me.step);  // ... of a step's row, and one more of the first ones
+  const double some = double(rows / me.step);  // ... of a step's row, and one more of the first ones
   const int more = int(rows % me.step);
-  const float all = float(rows) * float(each);
+  const double all = double(rows) * each;
   auto reduce = [&](auto one) __attribute__((always_inline)) {
     constexpr bool kOne = decltype(one)::value;
     const int team = kOne ? 1 : kWaves / a.groups, teams = kWaves / team;  // waves of a group, groups at once
     for (int g0 = 0; g0 < a.groups; g0 += teams) {  // (once, where a team has more than one wave)
       const int g = g0 + wave / team, member = wave % team;
       const int entries = wave / team < teams && g < a.groups ? each * me.step : 0;
-      auto total = [&](float s, int slot) __attribute__((always_inline)) {
+      auto total = [&](double s, int slot) __attribute__((always_inline)) {
         s = wave_total(s);
         if constexpr (kOne) return s;
         if (lane == 0) met[slot][wave] = s;
         __syncthreads();
-        s = 0.f;
+        s = 0;
         for (int w = wave - member; w < wave - member + team && w < kWaves; ++w) s += met[slot][w];
         return s;
       };
-      float s = 0.f;
+      double s = 0;
       for (int e = lane + 64 * member; e < entries; e += 64 * team) {
         const int row = e / each, c = g * each + e - row * each;
-        s += (row < more ? some + 1.f : some) * means[(row * columns + c / 8) * 8 + c % 8];
+        s += (row < more ? some + 1 : some) * means[(row * columns + c / 8) * 8 + c % 8];
       }
-      const float m = total(s, 0) / all;
-      s = 0.f;
+      const double m = total(s, 0) / all;
+      s = 0;
       for (int e = lane + 64 * member; e < entries; e += 64 * team) {
         const int row = e / each, c = g * each + e - row * each, i = (row * columns + c / 8) * 8 + c % 8;
-        const float d = means[i] - m;
-        s += squares[i] + (row < more ? some + 1.f : some) * d * d;
+        const double d = means[i] - m;
+        s += double(squares[i]) + (row < more ? some + 1 : some) * d * d;
       }
       s = total(s, 1);
-      if (lane == 0 && member == 0 && entries > 0) {
-        reinterpret_cast<float2*>(a.part)[(batch * a.groups + g) * a.runs + run] = make_float2(m, s);
-        // (kept, since y may be x)
-        if (run == 0) a.stats[(batch * a.groups + g) * 4] = load_one(a.x, BF16, batch * a.xs[0] + g * each);
-      }
+      if (lane == 0 && member == 0 && entries > 0)
+        reinterpret_cast<double2*>(a.part)[(batch * a.groups + g) * a.runs + run] = make_double2(m, s);
     }
   };
   if (a.groups > kWaves / 2)
@@ -336,7 +335,7 @@ __global__ __launch_bounds__(kUniters) void group_norm_unite_kernel(const GroupN
   __shared__ double sums[2][kUniters / 64];
   const int64_t at = a.first + blockIdx.x;
   const int each = a.c / a.groups;
-  const float2* part = reinterpret_cast<const float2*>(a.part) + at * a.runs;
+  const double2* part = reinterpret_cast<const double2*>(a.part) + at * a.runs;
   const RunRows rows(a);
   auto total = [&](double s, int slot) {
     s = wave_total(s);
@@ -348,17 +347,18 @@ __global__ __launch_bounds__(kUniters) void group_norm_unite_kernel(const GroupN
     return s;
   };
   double s = 0;
-  for (int i = threadIdx.x; i < a.runs; i += kUniters) s += double(rows.of(i)) * double(part[i].x);
+  for (int i = threadIdx.x; i < a.runs; i += kUniters) s += double(rows.of(i)) * part[i].x;
   const double mean = total(s, 0) / double(a.positions);
   s = 0;
   for (int i = threadIdx.x; i < a.runs; i += kUniters) {
-    const float2 p = part[i];
-    const double d = double(p.x) - mean;
-    s += double(p.y) + double(rows.of(i)) * each * d * d;
+    const double2 p = part[i];
+    const double d = p.x - mean;
+    s += p.y + double(rows.of(i)) * each * d * d;
   }
   const double var = total(s, 1) / (double(a.positions) * each);
   if (threadIdx.x == 0) {
-    a.stats[4 * at + 1] = float(mean);
+    a.stats[4 * at] = float(mean);
+    a.stats[4 * at + 1] = float(mean - double(float(mean)));
     a.stats[4 * at + 2] = float(1.0 / sqrt(var + double(a.eps)));
   }
 }
@@ -384,13 +384,13 @@ __global__ __launch_bounds__(kThreads) void group_norm_apply_kernel(const GroupN
     }
   };
   load(b);
-  float pivot[8], mean[8], scale[8], bias[8];
+  float mean[8], rest[8], scale[8], bias[8];  // (the mean is the two's sum)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = me.c + (i < me.left ? i : 0);
     const f32x4 s = reinterpret_cast<const f32x4*>(a.stats)[batch * a.groups + c / each];
-    pivot[i] = s[0];
-    mean[i] = s[1];
+    mean[i] = s[0];
+    rest[i] = s[1];
     scale[i] = s[2] * vector_value(a.weight, c, 1.f);
     bias[i] = vector_value(a.bias, c, 0.f);
   }
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(kThreads) void group_norm_apply_kernel(const GroupN
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float n = __builtin_fmaf(value_of<BF16>(x[u], i) - pivot[i] - mean[i], scale[i], bias[i]);
+        const float n = __builtin_fmaf(value_of<BF16>(x[u], i) - mean[i] - rest[i], scale[i], bias[i]);
         v[i] = a.silu ? silu(n) : n;
       }
       const int64_t to = batch * a.ys[0] + row * a.ys[1] + me.c;

@@ -217,8 +217,8 @@ struct GroupNormArgs {
   bool x_bf16, y_bf16, silu;
   VectorArgs weight, bias;
   int64_t runs;  // of an image's positions, or 0: a group in one workgroup
-  float* part;   // [batch][groups][runs] mean and squared differences, with runs
-  float* stats;  // [batch][groups] first value, mean from it, 1 / deviation, unused
+  double* part;  // [batch][groups][runs] mean and squared differences, with runs
+  float* stats;  // [batch][groups] mean, what its rounding took off, 1 / deviation, unused
   int64_t first;  // workgroup of the launch's first one
 };
 int64_t plan_group_norm(int64_t batch, int64_t positions, int c, int groups);
