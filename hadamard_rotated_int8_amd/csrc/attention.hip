@@ -181,16 +181,17 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     keys = n < 0 ? 0 : n < keys ? n : keys;
   }
   const int64_t all = (int64_t(keys) + kKeys - 1) / kKeys;  // tiles of keys
-  const int first = int(all * split / splits), last = int(all * (split + 1) / splits);
+  const int first = int(all * split / splits);
+  int last = int(all * (split + 1) / splits);
   const uint16_t* kbase = p.k + batch * p.ks[0] + head * p.ks[2];
   const uint16_t* vbase = p.v + batch * p.vs[0] + head * p.vs[2];
   const int dbytes = p.d * 2;
 
   // MASK: a bit for each key of 64 blocks of 32 from block `window` on, a word in
   // each lane; read anew where a tile's step needs words behind them.  (2 x 4096
-  // x 77, 10 heads of 64: 16.4 us with a mask, 12.6 without; 4096 x 4096, 16 of
-  // 128: 173 and 155, 181 where no two blocks hide the same keys.  As scalar
-  // loads from words that another kernel made: 18.7 and 203, and 3.8 for that.)
+  // x 77, 10 heads of 64: 12.4 us with a mask, 11.4 without; 4096 x 4096, 16 of
+  // 128, no two blocks hiding the same keys: 147 and 140.  As scalar loads from
+  // words that another kernel made 18.7 and 203, and 3.8 for that.)
   unsigned seen = 0;
   int window = first * (kKeys / 32);
   auto mask_words = [&](int block) __attribute__((always_inline)) {
@@ -204,9 +205,8 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
 #pragma unroll
       for (int i = 0; i < 8; ++i) bits |= byte_bits(w[i]) << (4 * i);
       bits = at - from < 32 ? bits >> (at - from) : 0u;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) bits |= row[i < p.l ? i : 0] ? 1u << i : 0u;
+    } else {  // (a byte to a lane)
+      bits = unsigned(__ballot(lane < p.l && row[lane < p.l ? lane : 0] != 0));
     }
     return bits;
   };
@@ -216,7 +216,21 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
       seen = mask_words(window);
     }
   };
-  if (MASK && first < last) seen = mask_words(window);
+  if (MASK && first < last) {
+    seen = mask_words(window);
+    // Without a key that is seen there is nothing to do (a NaN or infinity of a
+    // query times the zeros of hidden keys would be a NaN).
+    const unsigned blocks = last * (kKeys / 32), end = unsigned(last) * kKeys < unsigned(keys) ? last * kKeys : keys;
+    auto none = [&](unsigned bits, int block) {
+      const unsigned at = unsigned(block + lane) * 32, left = at < end ? end - at : 0;
+      return __ballot((left < 32 ? bits & ((1u << left) - 1) : bits) != 0) == 0;
+    };
+    if (none(seen, window)) {
+      unsigned b = window + 64;
+      while (b < blocks && none(mask_words(b), b)) b += 64;
+      if (b >= blocks) last = first;
+    }
+  }
   auto block_word = [&](int t, int row) __attribute__((always_inline)) {
     return unsigned(__builtin_amdgcn_readlane(seen, t * (kKeys / 32) + row / 32 - window));
   };
