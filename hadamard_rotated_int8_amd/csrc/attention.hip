@@ -33,6 +33,7 @@ typedef __attribute__((address_space(3))) uint8_t lds_byte;
 constexpr float kLog2e = 1.44269504f;
 constexpr float kSlack = 8.f;  // powers of two that a weight may exceed 1 by
 constexpr float kMinusInf = -__builtin_inff();
+constexpr float kLowest = -3.40282347e38f;
 
 // Bytes of a key's or value's row in LDS.
 constexpr int row_pitch(int d) { return d <= 64 ? 128 : d <= 128 ? 256 : 512; }
@@ -600,6 +601,10 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
   asm volatile("" : "+v"(me));  // (places are formed again: kept, they would be registers too many)
   const int query = me & 31, half = me >> 5;
   const float all_sum = total + other_half(total);
+  // What a part's sums are relative to.  Minus infinity: there were no keys.  The
+  // lowest number: keys that are seen, but all their scores minus infinity; where
+  // that is so of a whole row, 0 / 0 is what its softmax is.
+  const float relative = first == last ? kMinusInf : top == kMinusInf ? kLowest : base;
   if constexpr (FEW) {
     // The waves' sums, in their order, by all threads.
     constexpr int kRow = D + 4;  // (a row's distance in floats: 16 bytes off the banks of the one before)
@@ -611,7 +616,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
         *reinterpret_cast<f32x4*>(sums + query * kRow + 32 * n + 8 * q + 4 * half) =
             f32x4{o[n][4 * q], o[n][4 * q + 1], o[n][4 * q + 2], o[n][4 * q + 3]};
     if (half == 0) {
-      sums[query * kRow + D] = top == kMinusInf ? kMinusInf : base;
+      sums[query * kRow + D] = relative;
       sums[query * kRow + D + 1] = all_sum;
     }
     __syncthreads();
@@ -642,7 +647,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
           p.stats[2 * (part0 + row) + 1] = sum;
         }
       } else {
-        const float g = sum == 0.f ? 0.f : 1.f / sum;
+        const float g = most == kMinusInf ? 0.f : 1.f / sum;
         *reinterpret_cast<u32x4*>(out_row(row0 + row) + f) =
             u32x4{bf16_pair(lo[0] * g, lo[1] * g), bf16_pair(lo[2] * g, lo[3] * g), bf16_pair(hi[0] * g, hi[1] * g),
                   bf16_pair(hi[2] * g, hi[3] * g)};
@@ -653,7 +658,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     const int64_t r = wave * 32 + query;
     float* dst = p.part + (part0 + r) * p.d;
     if (half == 0) {
-      p.stats[2 * (part0 + r)] = top == kMinusInf ? kMinusInf : base;
+      p.stats[2 * (part0 + r)] = relative;
       p.stats[2 * (part0 + r) + 1] = all_sum;
     }
 #pragma unroll
@@ -667,7 +672,7 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
   } else {
     // Whole rows out of the wave's own part of LDS (whose accesses stay in order).
     uint8_t* mine = smem + wave * 32 * kPitch;
-    const float g = all_sum == 0.f ? 0.f : 1.f / all_sum;
+    const float g = relative == kMinusInf ? 0.f : 1.f / all_sum;
 #pragma unroll
     for (int n = 0; n < NF; ++n)
 #pragma unroll
@@ -704,7 +709,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
     sum += w * p.stats[2 * (s * count + r) + 1];
     v += w * *reinterpret_cast<const f32x4*>(p.part + (s * count + r) * p.d + f);
   }
-  v *= sum == 0.f ? 0.f : 1.f / sum;
+  v *= top == kMinusInf ? 0.f : 1.f / sum;
   const int64_t token = in / p.ratio;
   const int64_t batch = pair / p.kv_heads, head = (pair - batch * p.kv_heads) * p.ratio + in - token * p.ratio;
   *reinterpret_cast<u32x2*>(p.out + batch * p.os[0] + token * p.os[1] + head * p.os[2] + f) =

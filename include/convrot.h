@@ -632,6 +632,8 @@ convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* strea
  * the first three axes (stride 1 along d), 16-byte aligned with strides that
  * are multiples of 8.  Strides of 0 share keys or values among a batch.
  * What a hidden key or its value holds does not matter (a NaN neither).
+ * As by the formula, scores of minus infinity weigh nothing, and a query all of
+ * whose seen scores are that gives NaN.
  * ---------------------------------------------------------------------------
  */
 #define CONVROT_MAX_HEAD_DIM 192
