@@ -15,6 +15,7 @@ using convrot::kMaxRows;
 namespace {
 
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr float kMaxScale = 2.35e38f;  // (times log2 e it is finite)
 // 128 rows of keys or values lie in 31 bits.
 constexpr int64_t kMaxKeyStride = int64_t(1) << 23;
 
@@ -69,7 +70,7 @@ convrot_status convrot_attention_apply(const convrot_attention* a, void* stream)
   if (!a) return CONVROT_ERR_NULL;
   convrot_status st = check_sizes(*a);
   if (st != CONVROT_OK) return st;
-  if (!(a->scale > 0.f) || a->scale > 3.4e38f) return CONVROT_ERR_UNSUPPORTED;  // a NaN too
+  if (!(a->scale > 0.f && a->scale <= kMaxScale)) return CONVROT_ERR_UNSUPPORTED;  // a NaN too
   if (a->mask && (a->mask_stride < 0 || a->mask_stride > kMaxStride)) return CONVROT_ERR_SHAPE;
   if (a->batch == 0 || a->m == 0) return CONVROT_OK;
   if ((st = check_tensor(a->q, a->q_stride, a->m, a->d, false)) != CONVROT_OK) return st;

@@ -643,7 +643,7 @@ convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* strea
  *                 of k and v at most 2^23, and 0 or at least d.  out's elements must not overlap one
  *                 another nor an input.
  *   d           : a multiple of 8 in 8 .. CONVROT_MAX_HEAD_DIM
- *   scale       : > 0 and finite
+ *   scale       : > 0, at most 2.35e38 (the kernel's powers of two take it times 1.443)
  *   lengths     : device int32 [batch]: keys lengths[b] .. l - 1 of batch entry
  *                 b are hidden; or NULL
  *   mask        : device bytes [batch, l], row stride mask_stride >= 0: keys
