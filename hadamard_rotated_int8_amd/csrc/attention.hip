@@ -331,7 +331,8 @@ __global__ __launch_bounds__(attention_waves(D, FEW) * 64, D <= 128 && !FEW ? 2 
     }
   }
 
-  const float c = p.scale * kLog2e, slack = kSlack / c;
+  // (slack finite: a row that has seen no key yet has a limit of minus infinity plus it)
+  const float c = p.scale * kLog2e, slack = fminf(kSlack / c, -kLowest);
   f32x16 o[NF] = {}, s[2];
   u32x4 pf[2][2] = {};
   bf16x8 kf[kAhead], vf[kAhead];
