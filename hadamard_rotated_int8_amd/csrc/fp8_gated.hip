@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256) void gated_back_kernel(const GatedBackArgs a) 
         act = g[i] * phi;
         slope = __builtin_fmaf(g[i] * 0.39894228f, __builtin_amdgcn_exp2f(-0.72134752f * g[i] * g[i]), phi);
       } else {
-        const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g[i]));
+        const float s = sigmoid_rough(g[i]);
         act = g[i] * s;
         slope = s * __builtin_fmaf(g[i], 1.f - s, 1.f);
       }

@@ -126,22 +126,29 @@ struct GatedOut {
   void *y, *gate, *up;  // (gate, up: nullptr where they are not kept)
   int64_t ldy, ldk;
   int n;
-  bool bf16, gelu;
+  bool gelu;
 };
 CR_DEVICE GatedOut gated_out(const Fp8Params& p) {
-  return {p.seg[0].y, p.kept[0], p.kept[1], p.seg[0].ldy, p.ldk, p.seg[0].n, p.y_bf16 != 0, p.act == kActGelu};
+  return {p.seg[0].y, p.kept[0], p.kept[1], p.seg[0].ldy, p.ldk, p.seg[0].n, p.act == kActGelu};
 }
 
-// Four consecutive columns of an output row from the biased sums.
+// Four consecutive columns of an output row (BF16: in bfloat16) from the biased sums.
+template <bool BF16>
 CR_DEVICE void store_gated4(const GatedOut& o, int64_t m, int n, const float* g, const float* u) {
   const int left = o.n - n;
   auto vector = [&](const void* y, int64_t ld, unsigned bytes) {
     return left >= 4 && (ld & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & (bytes - 1)) == 0;
   };
   float v[4];
+  auto gate = [&](auto act) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = (o.gelu ? gelu_erf(g[e]) : silu(g[e])) * u[e];
-  store4(o.y, m * o.ldy + n, v, left, o.bf16, vector(o.y, o.ldy, o.bf16 ? 8 : 16));
+    for (int e = 0; e < 4; ++e) v[e] = act(g[e]) * u[e];
+  };
+  if (o.gelu)
+    gate([](float y) { return gelu_erf(y); });
+  else
+    gate([](float y) { return BF16 ? silu_rough(y) : silu(y); });
+  store4(o.y, m * o.ldy + n, v, left, BF16, vector(o.y, o.ldy, BF16 ? 8 : 16));
   if (o.gate) {
     store4(o.gate, m * o.ldk + n, g, left, true, vector(o.gate, o.ldk, 8));
     store4(o.up, m * o.ldk + n, u, left, true, vector(o.up, o.ldk, 8));

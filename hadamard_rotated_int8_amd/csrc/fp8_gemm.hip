@@ -54,7 +54,7 @@ CR_DEVICE f32x16 mfma_bf16(const Bf16Frag& a, const Bf16Frag& b, f32x16 c) {
 // step's block lie side by side and come along as one load (every wave makes
 // its own copy, so that all have the same number of loads to wait for); the
 // weights' scales of the whole tile are laid out in LDS as 32-bit values first.
-// EXACT: bfloat16 instructions (float32 outputs).
+// EXACT: bfloat16 instructions, for float32 outputs (the others are bfloat16).
 //
 // GATED: of the BN rows of W in a tile every 32 are 16 of the gate's and the
 // same 16 of the up projection's.  A lane then holds both sums of 8 of its 16
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void fp8_gemm_kernel(const Fp8Para
             g[e] = acc[i][j][4 * q + e] + bias[c + e];
             u[e] = acc[i][j][8 + 4 * q + e] + bias[OUTS + c + e];
           }
-          if (m < p.M && n < sg.n) store_gated4(out, m, n, g, u);
+          if (m < p.M && n < sg.n) store_gated4<!EXACT>(out, m, n, g, u);
         }
     } else {
 #pragma unroll

@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void fp8_rows_kernel(const Fp8Param
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = sum[e] + (bias && n + e < sg.n ? bias[n + e] : 0.f);
       }
-      store_gated4(gated_out(p), row, n, v[0], v[1]);
+      store_gated4<!EXACT>(gated_out(p), row, n, v[0], v[1]);
     }
     return;
   }

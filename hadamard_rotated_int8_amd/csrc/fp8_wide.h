@@ -485,7 +485,7 @@ CR_DEVICE void fp8_wide(const Fp8Params& p, int total) {
     // act(gate) * up of the biased sums.
     auto gate4 = [&](f32x4 g, f32x4 u) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) g[e] = (p.act == kActGelu ? gelu_erf(g[e]) : silu(g[e])) * u[e];
+      for (int e = 0; e < 4; ++e) g[e] = (p.act == kActGelu ? gelu_erf(g[e]) : silu_rough(g[e])) * u[e];
       return g;
     };
     // 8 columns of a row, `row` and `col` from the wave's first.

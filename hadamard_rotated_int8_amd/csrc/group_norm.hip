@@ -61,6 +61,16 @@ CR_DEVICE void store_values(const float* v, void* p, bool bf16, int64_t at) {
     __builtin_memcpy(static_cast<float*>(p) + at, v, 4 * V);
   }
 }
+template <int V>
+CR_DEVICE void silu_all(float* v, bool bf16) {
+  if (bf16) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = silu_rough(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
+  }
+}
 CR_DEVICE float load_one(const void* p, bool bf16, int64_t at) {
   return bf16 ? __uint_as_float(unsigned(static_cast<const uint16_t*>(p)[at]) << 16)
               : static_cast<const float*>(p)[at];
@@ -147,10 +157,9 @@ __global__ __launch_bounds__(1024) void group_norm_held_kernel(const GroupNormAr
     const int e = thread + i * blockDim.x, row = e / columns, c = (e - row * columns) * V;
     if (e < vectors) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float n = __builtin_fmaf((v[i][j] - off) * r, affine[c + j], affine[each + c + j]);
-        v[i][j] = a.silu ? silu(n) : n;
-      }
+      for (int j = 0; j < V; ++j)
+        v[i][j] = __builtin_fmaf((v[i][j] - off) * r, affine[c + j], affine[each + c + j]);
+      if (a.silu) silu_all<V>(v[i], a.y_bf16);
       store_values<V>(v[i], a.y, a.y_bf16, ybase + row * a.ys[1] + c);
     }
   }
@@ -394,32 +403,39 @@ __global__ __launch_bounds__(kThreads) void group_norm_apply_kernel(const GroupN
     scale[i] = s[2] * vector_value(a.weight, c, 1.f);
     bias[i] = vector_value(a.bias, c, 0.f);
   }
-  for (; b >= 0; b -= a.runs) {
-    const int64_t r = b * block + me.row;
-    Raw<BF16> x[kRows];
+  // (The three ways apart: with the choice at each row 2 x 16384 x 320 takes 29.6 us instead of 28.8.)
+  auto finish = [&](auto act) __attribute__((always_inline)) {
+    for (; b >= 0; b -= a.runs) {
+      const int64_t r = b * block + me.row;
+      Raw<BF16> x[kRows];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) x[u] = held[u];
-    if (b >= a.runs) load(b - a.runs);
+      for (int u = 0; u < kRows; ++u) x[u] = held[u];
+      if (b >= a.runs) load(b - a.runs);
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t row = r + u * me.step;
-      if (row >= a.positions) break;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = __builtin_fmaf(value_of<BF16>(x[u], i) - mean[i] - rest[i], scale[i], bias[i]);
-        v[i] = a.silu ? silu(n) : n;
-      }
-      const int64_t to = batch * a.ys[0] + row * a.ys[1] + me.c;
-      if (WHOLE || me.left == 8) {
-        store_values<8>(v, a.y, a.y_bf16, to);
-      } else {
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t row = r + u * me.step;
+        if (row >= a.positions) break;
+        float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < me.left) store_values<1>(v + i, a.y, a.y_bf16, to + i);
+          v[i] = act(__builtin_fmaf(value_of<BF16>(x[u], i) - mean[i] - rest[i], scale[i], bias[i]));
+        const int64_t to = batch * a.ys[0] + row * a.ys[1] + me.c;
+        if (WHOLE || me.left == 8) {
+          store_values<8>(v, a.y, a.y_bf16, to);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < me.left) store_values<1>(v + i, a.y, a.y_bf16, to + i);
+        }
       }
     }
-  }
+  };
+  if (!a.silu)
+    finish([](float n) { return n; });
+  else if (a.y_bf16)
+    finish([](float n) { return silu_rough(n); });
+  else
+    finish([](float n) { return silu(n); });
 }
 
 template <bool BF16, int V>
