@@ -669,7 +669,8 @@ def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
     x            : float32 or bfloat16 [batch, ..., c], the positions at one distance from one
                    another (for [batch, c, height, width] in channels-last memory: x.permute(0, 2, 3, 1))
     weight, bias : float32 or bfloat16 [c]
-    Returns float32 or bfloat16 in x's shape (x's type by default; ``out`` may be x).
+    Returns float32 or bfloat16 in x's shape (x's type by default; ``out`` may be x, and lies over
+    neither weight nor bias).
     """
     dev = _device(x, "x")
     if x.dtype not in _DTYPE or (out_dtype is not None and out_dtype not in _DTYPE):
@@ -695,6 +696,9 @@ def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
             (a, b), (lo, hi) = _span(x), _span(out)
             if a < hi and lo < b:
                 raise ValueError("out must be x itself or lie in memory of its own")
+        lo, hi = _span(out)  # (workgroups read these while others write)
+        if any(a < hi and lo < b for a, b in map(_span, [t for t in (weight, bias) if t is not None])):
+            raise ValueError("out must not lie over weight or bias")
     args = [x.data_ptr(), out.data_ptr(), x.stride(0), xs, out.stride(0), ys, batch, positions, c, groups,
             _DTYPE[x.dtype], _DTYPE[out.dtype], eps, 1 if silu else 0,
             *_vector_args(weight, c, "weight", dev), *_vector_args(bias, c, "bias", dev), 0, 0]

@@ -445,6 +445,12 @@ convrot_status convrot_group_norm_apply(const convrot_group_norm* g, void* strea
   if (g->batch == 0 || g->positions == 0) return CONVROT_OK;
   if (!g->x || !g->y) return CONVROT_ERR_NULL;
   if (!aligned(g->x, size_of(g->x_dtype)) || !aligned(g->y, size_of(g->y_dtype))) return CONVROT_ERR_UNSUPPORTED;
+  // (workgroups read weight and bias while others write)
+  const convrot::Range one = convrot::range_of(g->y, g->positions, g->y_stride[1], g->c, size_of(g->y_dtype));
+  const convrot::Range y = convrot::range_of(g->y, g->batch, g->y_stride[0], int64_t(one.hi - one.lo) / size_of(g->y_dtype),
+                                             size_of(g->y_dtype));
+  for (const convrot_vector* v : {&g->weight, &g->bias})
+    if (convrot::meet(y, convrot::range_of(v->data, 1, 0, g->c, size_of(v->dtype)))) return CONVROT_ERR_UNSUPPORTED;
   if (g->x == g->y && (g->x_dtype != g->y_dtype || g->x_stride[0] != g->y_stride[0] ||
                        g->x_stride[1] != g->y_stride[1]))
     return CONVROT_ERR_UNSUPPORTED;

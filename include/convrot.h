@@ -587,8 +587,9 @@ convrot_status convrot_rope_apply(const convrot_rope* r, void* stream);
  *   x, y     : device [batch, positions, c] of x_dtype and y_dtype (CONVROT_F32
  *              or CONVROT_BF16), element strides of image and position at most
  *              2^40 (stride 1 along c); y may be x itself with the same strides
- *              and type, and must not overlap it otherwise.  Pointers need
- *              their element's alignment only.
+ *              and type, and must not overlap it otherwise, nor lie over
+ *              weight or bias (refused).  Pointers need their element's
+ *              alignment only.
  *   weight, bias : c values each, or absent (a norm's: stride and rows are not read)
  *   c        : at most CONVROT_MAX_GROUP_NORM_C, groups divide it; eps >= 0
  *   silu     : 1 for v / (1 + exp(-v)) of the result, else 0
