@@ -339,7 +339,8 @@ def fp8_gated(x: torch.Tensor | Fp8Activation, gate: Fp8Weights, up: Fp8Weights,
     gate, up : [n, k] each, with scales of one type
     act  : "silu" or "gelu" (erf form), of the unrounded G
     Returns float32 (by default) or bfloat16 [m, n]; with ``keep`` also the pair (G, U) as bfloat16
-    [m, n], which ``fp8_gated_backward`` takes.  ``out`` may lie over an unpacked x.
+    [m, n], which ``fp8_gated_backward`` takes.  ``out`` may lie over an unpacked x, not over a packed
+    one or the weights.
     """
     code = _gated_act(act)
     rows = None

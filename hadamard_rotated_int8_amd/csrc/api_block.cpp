@@ -126,6 +126,22 @@ convrot_status check_gated(const convrot_gated* g, convrot::Fp8GemmArgs* a) {
         g->kept_gate == g->y || g->kept_up == g->y)
       return CONVROT_ERR_UNSUPPORTED;
   }
+  if (a->count > 0) {
+    // Workgroups read these while others write.  (Not an unpacked X: its rows may lie between Y's.)
+    const convrot::Range out[3] = {convrot::range_of(g->y, a->m, g->ldy, g->gate.n, size_of(g->y_dtype)),
+                                   convrot::range_of(g->kept_gate, a->m, g->ldk, g->gate.n, 2),
+                                   convrot::range_of(g->kept_up, a->m, g->ldk, g->gate.n, 2)};
+    const int64_t kb = blocks(a->k);
+    convrot::Range in[8] = {convrot::range_of(a->qx, a->m, a->k, a->k, 1), convrot::range_of(a->sx, kb, a->lds, a->m, 1)};
+    for (int i = 0; i < 2; ++i) {
+      in[2 + 3 * i] = convrot::range_of(w[i].q, w[i].n, a->k, a->k, 1);
+      in[3 + 3 * i] = convrot::range_of(w[i].scale, blocks(w[i].n), kb, kb, a->f32_scale ? 4 : 1);
+      in[4 + 3 * i] = convrot::range_of(w[i].bias, 1, 0, w[i].n, 4);
+    }
+    for (const convrot::Range& o : out)
+      for (const convrot::Range& i : in)
+        if (convrot::meet(o, i)) return CONVROT_ERR_UNSUPPORTED;
+  }
   a->gated = true;
   a->act = g->act == CONVROT_ACT_GELU ? convrot::kActGelu : convrot::kActSilu;
   a->kept[0] = g->kept_gate;

@@ -378,7 +378,8 @@ convrot_status convrot_fp8_linear_rows(const void* x, int32_t x_dtype, int64_t m
  *   act       : CONVROT_ACT_SILU or CONVROT_ACT_GELU
  *   kept_gate, kept_up : device bfloat16 [m, n], row stride ldk >= n, for G and U,
  *               which convrot_fp8_gated_backward takes; both or neither (NULL)
- * Outputs must not overlap one another or any input.
+ * Outputs must not overlap one another or any input (the codes and scales of a
+ * packed X, the weights': refused).
  */
 typedef struct convrot_gated {
   convrot_fp8_weights gate, up;
