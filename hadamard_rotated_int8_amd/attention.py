@@ -10,7 +10,7 @@ import struct
 import torch
 
 from . import lib
-from .block import _device, _launch, _no_overlap, _span, _workspace
+from .block import _DETACH, _device, _launch, _no_gradient, _no_overlap, _recording, _span, _workspace
 
 MAX_HEAD_DIM = 192
 
@@ -31,9 +31,12 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | 
     out     : where the result goes, in memory of its own; by default a new contiguous tensor
     d is a multiple of 8 up to 192.  Any strides but 1 along d that are multiples of 8, 16-byte
     aligned (column ranges of a projection's rows, expanded batches).  Returns bfloat16 in q's
-    shape; a query that sees no key gives zeros.  Hidden keys and values may hold anything.
+    shape; a query that sees no key gives zeros.  Hidden keys and values may hold anything.  There is
+    no gradient: autograd raises where it comes back to the result.
     """
     dev = _device(q, "q")
+    if _recording() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return _no_gradient(attention, (q, k, v, scale, lengths, mask), _DETACH, out, q, k, v)
     dim = q.dim()
     for t, what in ((q, "q"), (k, "k"), (v, "v")):
         if t.dtype != torch.bfloat16 or t.dim() != dim or dim not in (3, 4) or \

@@ -78,6 +78,33 @@ def _device(x: torch.Tensor, what: str) -> torch.device:
     return x.device
 
 
+class _NoGradient(torch.autograd.Function):
+    """Stands behind results of operators that record no gradient, where one is asked for: going back
+    through them is an error, not a gradient that is missing without a word."""
+
+    @staticmethod
+    def forward(ctx, fn, args, instead, *inputs):
+        ctx.message = f"{fn.__name__} records no gradient: {instead}"
+        return fn(*args)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError(ctx.message)
+
+
+_recording = torch.is_grad_enabled  # (asked first: it is the shorter way)
+
+
+def _no_gradient(fn, args, instead, out, *inputs):
+    """fn(*args) where one of the inputs requires a gradient; without ``out``, as torch's own functions."""
+    if out is not None:
+        raise ValueError("out cannot be given where an input requires a gradient: use torch.no_grad()")
+    return _NoGradient.apply(fn, args, instead, *inputs)
+
+
+_DETACH = "call it under torch.no_grad() or on detached tensors"
+
+
 def _rows(x: torch.Tensor, what: str, dev=None, shape=None) -> int:
     """Check a float matrix with unit column stride; returns its type's code."""
     dt = _DTYPE.get(x.dtype)
@@ -331,6 +358,18 @@ def _gated_act(act: str) -> int:
     return code
 
 
+def _gated_result(kept, *args):
+    """The first of what fp8_gated returns; what it keeps goes into ``kept``."""
+    y = fp8_gated(*args)
+    if isinstance(y, tuple):
+        kept.append(y[1])
+        return y[0]
+    return y
+
+
+_gated_result.__name__ = "fp8_gated"
+
+
 def fp8_gated(x: torch.Tensor | Fp8Activation, gate: Fp8Weights, up: Fp8Weights, act: str = "silu",
               out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, keep: bool = False):
     """act(G) * U of a gated feed-forward, G = X gate^T + its bias, U = X up^T + its bias, in one kernel.
@@ -340,8 +379,16 @@ def fp8_gated(x: torch.Tensor | Fp8Activation, gate: Fp8Weights, up: Fp8Weights,
     act  : "silu" or "gelu" (erf form), of the unrounded G
     Returns float32 (by default) or bfloat16 [m, n]; with ``keep`` also the pair (G, U) as bfloat16
     [m, n], which ``fp8_gated_backward`` takes.  ``out`` may lie over an unpacked x, not over a packed
-    one or the weights.
+    one or the weights.  Autograd goes back through it only where the caller's own
+    torch.autograd.Function calls ``fp8_gated_backward``; by itself the result raises there.
     """
+    b, c = gate.bias, up.bias
+    if _recording() and (b is not None and b.requires_grad or c is not None and c.requires_grad or
+                         isinstance(x, torch.Tensor) and x.requires_grad):
+        kept = []
+        y = _no_gradient(_gated_result, (kept, x, gate, up, act, None, out_dtype, keep), "fp8_gated_backward gives it",
+                         out, x if isinstance(x, torch.Tensor) else None, b, c)
+        return (y, kept[0]) if keep else y
     code = _gated_act(act)
     rows = None
     if isinstance(x, Fp8Activation):
@@ -671,9 +718,13 @@ def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
                    another (for [batch, c, height, width] in channels-last memory: x.permute(0, 2, 3, 1))
     weight, bias : float32 or bfloat16 [c]
     Returns float32 or bfloat16 in x's shape (x's type by default; ``out`` may be x, and lies over
-    neither weight nor bias).
+    neither weight nor bias).  There is no gradient: autograd raises where it comes back to the result.
     """
     dev = _device(x, "x")
+    if _recording() and (x.requires_grad or weight is not None and weight.requires_grad or
+                         bias is not None and bias.requires_grad):
+        return _no_gradient(group_norm, (x, groups, weight, bias, eps, silu, None, out_dtype), _DETACH, out, x, weight,
+                            bias)
     if x.dtype not in _DTYPE or (out_dtype is not None and out_dtype not in _DTYPE):
         raise ValueError("x and out must be float32 or bfloat16")
     batch, positions, xs = _positions(x, "x")
