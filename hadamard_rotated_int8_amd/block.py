@@ -697,6 +697,8 @@ def _positions(x: torch.Tensor, what: str) -> tuple[int, int, int]:
         raise ValueError(f"{what} must be [batch, ..., c] with unit stride along c")
     count, stride = 1, None
     for n, st in zip(reversed(x.shape[1:-1]), reversed(x.stride()[1:-1])):
+        if n == 0:
+            return x.shape[0], 0, x.shape[-1]
         if n == 1:
             continue
         if stride is None:
