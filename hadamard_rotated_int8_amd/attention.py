@@ -38,9 +38,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | 
     if _recording() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return _no_gradient(attention, (q, k, v, scale, lengths, mask), _DETACH, out, q, k, v)
     dim = q.dim()
+    known = dim == 3 or dim == 4
     for t, what in ((q, "q"), (k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16 or t.dim() != dim or dim not in (3, 4) or \
-                (t.stride(-1) != 1 and t.shape[-1] != 1):
+        if not known or t.dtype != torch.bfloat16 or t.dim() != dim or (t.stride(-1) != 1 and t.shape[-1] != 1):
             raise ValueError(f"{what} must be bfloat16 [batch, tokens, heads, d] or [tokens, heads, d] "
                              "with unit stride along d")
         if t.device != dev:

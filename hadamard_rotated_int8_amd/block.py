@@ -733,8 +733,6 @@ def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
     c = x.shape[-1]
     if not 1 <= c <= MAX_GROUP_NORM_C or groups < 1 or c % groups:
         raise ValueError(f"groups must divide the channels, which are 1 to {MAX_GROUP_NORM_C}")
-    if 0 in x.shape:
-        positions = 0
     if out is None:
         out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
         ys = c
