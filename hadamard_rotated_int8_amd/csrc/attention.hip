@@ -766,18 +766,29 @@ AttentionPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int6
     }
   };
   // Fewer tiles than CUs are split so that each CU has work.  Of more, those of
-  // a last round that would leave places free (a CU has two workgroups, one
-  // beyond 128 features) are split to fill them.  Up to a quarter of the places:
-  // 4608 x 4608, 30 heads of 64, 223 -> 208 us, 2176 x 1024, 31 of 128, 59 -> 54.
-  // Up to a half, where what is saved outweighs the parts' way through memory:
-  // 4095 x 32760, 40 of 128, 2630 -> 2540, 4096 x 4096, 20 of 160, 297 -> 271; but
-  // 4096 x 4096, 40 of 128, 337 -> 344, 2304 x 4096, 40 of 64, 127 -> 134.
+  // a last round that would leave places free are split to fill them, counting
+  // two places to a CU, beyond 128 features one.  (Up to 64 features a third
+  // workgroup fits, but three take the time of three there: 520 tiles of 1100
+  // keys 35.6 us with the last 8 split, 37.6 without; 640 tiles of 1100 keys 41.8
+  // and 39.6, of 4096 115 and 121; with three places in the count 1080 tiles of
+  // 4096 keys 198 instead of 186, though 800 tiles 140 instead of 166.)
+  // Up to a quarter of the places: 4608 x 4608, 30 heads of 64, 223 -> 208 us, 2176
+  // x 1024, 31 of 128, 59 -> 54.  Up to a half where what is saved outweighs the
+  // parts' way through memory: beyond 128 features (4096 x 4096, 20 of 160, 297 ->
+  // 271), or with 12288 keys.  1280, 720 and 700 tiles of 128 features, split and
+  // not: 4096 keys 345 / 335, 207 / 202, 203 / 200 us; 8192 663 / 656, 392 / 393, 385
+  // / 389; 12288 976 / 983, 584 / 606, 573 / 588; 32760 2518 / 2574, 1503 / 1592, 1463
+  // / 1557; of 96 features 8192 keys 572 / 570, 345 / 350, 337 / 344; 12288 843 / 848,
+  // 507 / 518, 495 / 511.  Of 64 features the tiles that fit three to a CU run at
+  // once: 12288 keys 607 / 618, but 381 / 372, 375 / 363; 32760 1599 / 1649, but 988
+  // / 975, 975 / 956.
   const int64_t places = (plan.few || d > 128 ? 1 : 2) * cus;
+  const bool half = d > 128 || (l >= 12288 && (d > 64 || total > 3 * cus));
   if (total > 0 && total < cus) {
     split(0, cus / total);
   } else if (total > places && total <= (1 << 20)) {
     const int64_t last = total % places;
-    if (last > 0 && last <= (d > 128 || l >= 16384 ? places / 2 : places / 4)) split(total - last, places / last);
+    if (last > 0 && last <= (half ? places / 2 : places / 4)) split(total - last, places / last);
   }
   return plan;
 }
