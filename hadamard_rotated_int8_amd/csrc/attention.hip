@@ -8,12 +8,15 @@
 // name its 16 terms in any order, as long as it is the same).  V^T is read
 // from LDS with the transposing read, so K and V lie there as they come.
 //
-// With many keys the matrix cores bind it at the chip's power limit: 4095 x
-// 32760, 40 heads of 128, takes 2540 us, 1.08 PFLOP/s (a large library product
-// 1.36).  With few the workgroups' starts and ends come to as much: 32760 x
-// 512 440 us, 0.78 PFLOP/s; 3 x 1023 x 333, 32 heads of 80 on 8, with a mask,
-// 30 us, five tiles of keys to a workgroup.  One query over 512 keys, 40 heads:
-// 10.6 us, the steps' and loads' latency.
+// With many keys power binds it, and how products and vector instructions share
+// the cycles that it leaves: 4095 x 32760, 40 heads of 128, takes 2500 to 2650
+// us, 1.04 to 1.1 PFLOP/s (a large library product 1.36), at 1.72 of 2.4 GHz,
+// with the matrix cores busy in 58 % of the cycles, vector instructions issued
+// in 54 % and waves waiting in 25 % of theirs.  With few keys the workgroups'
+// starts and ends come to as much: 32760 x 512 440 us, 0.78 PFLOP/s, matrix
+// cores busy in 39 %; 3 x 1023 x 333, 32 heads of 80 on 8, with a mask, 29 us,
+// five tiles of keys to a workgroup.  One query over 512 keys, 40 heads: 10.6 us,
+// the steps' and loads' latency.
 #include "common.h"
 #include "kernels.h"
 

@@ -2,8 +2,9 @@
 // bu) in one kernel (fp8_wide.h), its way back to the projections, and the
 // weights' transpose, on which the way back to X is a linear like any other.
 // 4096 x 5120 -> 13824, 1728 tiles on 256 CUs: 490 us with both projections
-// kept, bound by the matrix cores at the chip's power limit (2.4 PFLOP/s) with
-// 340 MB of outputs stored beside them.
+// kept (2.4 PFLOP/s), bound by power (1.96 of 2.4 GHz) and the stores of 340 MB
+// of outputs: the matrix cores are busy in 54 % of the cycles (72 % in the wide
+// kernel without them).
 #include "fp8_wide.h"
 
 namespace convrot {
@@ -130,7 +131,8 @@ __global__ __launch_bounds__(256) void gated_back_kernel(const GatedBackArgs a) 
   }
 }
 
-// One 64 x 64 tile of codes through LDS.  Offline.
+// One 64 x 64 tile of codes through LDS, byte by byte.  Offline: once for a
+// weight (2 x 13824 x 5120 148 us, 2.6 times a copy).
 __global__ __launch_bounds__(256) void fp8_transpose_kernel(const uint8_t* q, int64_t n, int64_t k, uint8_t* out,
                                                             int64_t ldq, int tiles, int64_t first) {
   __shared__ uint8_t tile[64][68];
