@@ -475,6 +475,14 @@ def _whole_rounds(m: int, w: Fp8Weights, dev) -> int:
     return at if rest <= cus * wide // 128 else 0
 
 
+def _gradients(*args):
+    dx, grads = fp8_gated_backward(*args)
+    return dx, *grads
+
+
+_gradients.__name__ = "fp8_gated_backward"
+
+
 def fp8_gated_backward(dy: torch.Tensor, kept, back: Fp8Weights, act: str = "silu"):
     """The way back through ``fp8_gated``: (dX, (dG, dU)), all bfloat16.
 
@@ -497,6 +505,9 @@ def fp8_gated_backward(dy: torch.Tensor, kept, back: Fp8Weights, act: str = "sil
     for t in kept:
         if not isinstance(t, torch.Tensor) or _rows(t, "a kept projection", dev, dy.shape) != BF16:
             raise ValueError("the kept projections must be bfloat16")
+    if _recording() and (dy.requires_grad or kept[0].requires_grad or kept[1].requires_grad):
+        dx, *grads = _no_gradient(_gradients, (dy, kept, back, act), "there is no second one", None, dy, *kept)
+        return dx, tuple(grads)
     if kept[0].stride() != kept[1].stride():
         raise ValueError("the kept projections must share their strides")
     np = _blocks(n) * FP8_BLOCK

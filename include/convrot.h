@@ -579,7 +579,8 @@ convrot_status convrot_rope_apply(const convrot_rope* r, void* stream);
  * Group norm of channels-last features, with an optional SiLU behind it:
  *   y = act((x - mean) / sqrt(var + eps) * weight + bias)
  * mean and var (of the differences from the mean) over an image's positions
- * and a group's c / groups neighbouring channels, in float32.
+ * and a group's c / groups neighbouring channels, in float32 (squared
+ * differences too: a group's sum of them has to stay below 3.4e38).
  * ---------------------------------------------------------------------------
  */
 #define CONVROT_MAX_GROUP_NORM_C 4096

@@ -98,3 +98,19 @@ def test_a_callers_own_function_goes_back():
     _Gated.apply(x, gate, up, back).backward(dy)
     kept = cr.fp8_gated(x.detach(), gate, up, keep=True)[1]
     assert torch.equal(x.grad, cr.fp8_gated_backward(dy, kept, back)[0].float())
+
+
+@pytest.mark.gpu
+def test_no_second_gradient_vanishes():
+    n, k = 256, 128
+    gate, up = (cr.fp8_quantize_weights(torch.randn(n, k, device="cuda")) for _ in range(2))
+    back = cr.fp8_transpose_weights([gate, up])
+    kept = cr.fp8_gated(torch.randn(8, k, device="cuda"), gate, up, keep=True)[1]
+    dy = torch.randn(8, n, device="cuda")
+    want, (dg, du) = cr.fp8_gated_backward(dy, kept, back)
+    dx, grads = cr.fp8_gated_backward(dy.clone().requires_grad_(), kept, back)
+    assert dx.requires_grad and torch.equal(dx.detach(), want)
+    assert torch.equal(grads[0].detach(), dg) and torch.equal(grads[1].detach(), du)
+    for t in (dx, *grads):
+        with pytest.raises(NotImplementedError, match="fp8_gated_backward"):
+            t.float().sum().backward(retain_graph=True)
